@@ -1,5 +1,5 @@
-"""Thin ctypes binding of ``libfs_sinkhorn.so`` (the C ABI in include/fs_sinkhorn.h
-and include/fs_probe.h).
+"""Thin ctypes binding of ``libfs_sinkhorn.so`` (the C ABI in include/fs_sinkhorn.h,
+include/fs_attention.h and include/fs_probe.h).
 
 Argument marshalling only: torch tensors provide device memory and the current
 HIP stream; every step of the solver runs in the library's kernels.  If the
@@ -30,6 +30,9 @@ __all__ = [
     "fs_sampled_marginal_error", "fs_bs_coarse_start", "fs_bs_apply_transport",
     "fs_bs_apply_transport_t", "fs_bs_gradient", "fs_static_scratch_bytes",
     "fs_sinkhorn_solve_static",
+    "fs_bucket_edges", "fs_attention_workspace_bytes", "fs_attention_forward",
+    "fs_attention_backward", "fs_qk_norm_workspace_bytes", "fs_qk_norm_rotate",
+    "fs_qk_norm_rotate_backward",
 ]
 
 FS_OK, FS_ERR_INVALID_ARG, FS_ERR_WORKSPACE, FS_ERR_DEVICE, FS_ERR_NONFINITE, \
@@ -72,6 +75,33 @@ class HvpInfo(ctypes.Structure):
 class CoarseInfo(ctypes.Structure):
     _fields_ = [("rounds", ctypes.c_int32), ("accepted", ctypes.c_int32),
                 ("err_rows", ctypes.c_float), ("err_cols", ctypes.c_float)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_batch", ctypes.c_int64),
+                ("stride_row", ctypes.c_int64), ("stride_head", ctypes.c_int64)]
+
+
+class AttentionDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("m", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("dv", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("causal", ctypes.c_int32), ("offset", ctypes.c_int32),
+                ("offsets", ctypes.c_void_p), ("q_len", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("key_mask", ctypes.c_void_p),
+                ("key_mask_stride", ctypes.c_int64), ("bias", ctypes.c_void_p),
+                ("edges", ctypes.POINTER(ctypes.c_int32)), ("n_edges", ctypes.c_int32),
+                ("two_sided", ctypes.c_int32)]
+
+
+class QkNormDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("heads_q", ctypes.c_int32), ("heads_k", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("cos_table", ctypes.c_void_p),
+                ("sin_table", ctypes.c_void_p), ("n_pos", ctypes.c_int32),
+                ("positions", ctypes.c_void_p), ("positions_stride", ctypes.c_int64),
+                ("offset", ctypes.c_int32)]
 
 
 class FsError(RuntimeError):
@@ -189,6 +219,24 @@ def load():
     lib.fs_sinkhorn_solve_static.argtypes = [_fp, _fp, _fp, _fp, i64, i64, i32, ctypes.c_int,
                                              ctypes.POINTER(SolveOpts), _fp, _fp,
                                              ctypes.POINTER(SolveInfo), _vp]
+    i32p = ctypes.POINTER(i32)
+    desc, norm = ctypes.POINTER(AttentionDesc), ctypes.POINTER(QkNormDesc)
+    lib.fs_bucket_edges.restype = ctypes.c_int
+    lib.fs_bucket_edges.argtypes = [i32, i32, i32p]
+    lib.fs_attention_workspace_bytes.restype = sz
+    lib.fs_attention_workspace_bytes.argtypes = [desc, i32]
+    lib.fs_attention_forward.restype = ctypes.c_int
+    lib.fs_attention_forward.argtypes = [desc] + [Rows] * 4 + [_fp, _vp, sz, _vp]
+    lib.fs_attention_backward.restype = ctypes.c_int
+    lib.fs_attention_backward.argtypes = [desc] + [Rows] * 4 + [_fp, Rows, _fp] + [Rows] * 3 + \
+        [_fp, _vp, sz, _vp]
+    lib.fs_qk_norm_workspace_bytes.restype = sz
+    lib.fs_qk_norm_workspace_bytes.argtypes = [norm]
+    lib.fs_qk_norm_rotate.restype = ctypes.c_int
+    lib.fs_qk_norm_rotate.argtypes = [norm, Rows, Rows, _fp, _fp, Rows, Rows, _vp]
+    lib.fs_qk_norm_rotate_backward.restype = ctypes.c_int
+    lib.fs_qk_norm_rotate_backward.argtypes = [norm, Rows, Rows, _fp, _fp] + [Rows] * 4 + \
+        [_fp, _fp, _vp, sz, _vp]
     _LIB = lib
     return lib
 
@@ -674,3 +722,281 @@ def solve(X, Y, a, b, *, eps: float, iters: int, prec="auto", n_stages: int = 1,
                              eps_start=eps_start, tol=tol, check_every=check_every,
                              raise_not_converged=False)
     return p, f, g, info
+
+
+# ---- attention (include/fs_attention.h) -----------------------------------
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_NO_ROWS = Rows(None, 0, 0, 0)
+
+
+def fs_bucket_edges(side_buckets: int, max_distance: int) -> list:
+    """The edges of one side's buckets: one distance each for the first half,
+    then evenly spaced in the logarithm up to max_distance."""
+    out = (ctypes.c_int32 * max(side_buckets, 1))()
+    _check(load().fs_bucket_edges(side_buckets, max_distance, out), "fs_bucket_edges")
+    return list(out[:side_buckets - 1])
+
+
+def _on(t: torch.Tensor, name: str, like: torch.Tensor):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a device tensor")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, q on {like.device}")
+
+
+def _rows(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape) -> Rows:
+    """A [batch, rows, heads, width] tensor of q's type as fs_rows."""
+    if t is None:
+        return _NO_ROWS
+    _on(t, name, like)
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} is {t.dtype}, q is {like.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)} (is {tuple(t.shape)})")
+    s = t.stride()
+    if s[3] != 1 and shape[3] != 1:
+        raise ValueError(f"{name}'s last axis must be contiguous")
+    return Rows(t.data_ptr(), s[0], s[1], s[2])
+
+
+def _flat(t: Optional[torch.Tensor], name: str, like: torch.Tensor, dtype, shape) -> Optional[int]:
+    """A contiguous tensor of this type and shape, as its address."""
+    if t is None:
+        return None
+    _on(t, name, like)
+    if t.dtype != dtype or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)} (is {tuple(t.shape)})")
+    return t.data_ptr()
+
+
+def _work(workspace: Optional[torch.Tensor], need: int, like: torch.Tensor, stream):
+    """Aligned address and size of the workspace, and the tensor to keep: the
+    caller's, or one of `need` bytes that the stream holds until it is done."""
+    if workspace is None:
+        workspace = torch.empty(need + 256, dtype=torch.uint8, device=like.device)
+        if stream is not None:
+            s = stream if isinstance(stream, torch.cuda.Stream) else \
+                torch.cuda.ExternalStream(int(stream), device=like.device)
+            workspace.record_stream(s)
+    else:
+        _on(workspace, "workspace", like)
+        if not workspace.is_contiguous():
+            raise TypeError("workspace must be contiguous")
+    base = workspace.data_ptr()
+    aligned = (base + 255) // 256 * 256
+    return aligned, max(0, workspace.numel() * workspace.element_size() - (aligned - base)), workspace
+
+
+def _run_on(like: torch.Tensor, stream, call):
+    """call(stream handle) with q's device current."""
+    if torch.cuda.current_device() == like.device.index:
+        return call(_stream(stream))
+    with torch.cuda.device(like.device):
+        return call(_stream(stream))
+
+
+def _attention_desc(q, k, v, scale, causal, offset, offsets, q_len, kv_len, key_mask, bias, edges,
+                    two_sided) -> AttentionDesc:
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise TypeError("q must be a device tensor")
+    if q.dtype not in _DTYPES:
+        raise TypeError(f"q must be float32, bfloat16 or float16 (is {q.dtype})")
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k and v must be [batch, rows, heads, width]")
+    batch, n, heads, d = q.shape
+    m, kv_heads = k.shape[1], k.shape[2]
+    dv = v.shape[3]
+    lens = (batch,)
+    i32 = torch.int32
+    a = AttentionDesc(_DTYPES[q.dtype], batch, n, m, heads, kv_heads, d, dv,
+                      scale if scale is not None else d ** -0.5, bool(causal), offset)
+    if offsets is not None:
+        a.offsets = _flat(offsets, "offsets", q, i32, lens)
+    if q_len is not None:
+        a.q_len = _flat(q_len, "q_len", q, i32, lens)
+    if kv_len is not None:
+        a.kv_len = _flat(kv_len, "kv_len", q, i32, lens)
+    if key_mask is not None:
+        _on(key_mask, "key_mask", q)
+        if key_mask.dtype not in (torch.uint8, torch.bool):
+            raise TypeError("key_mask must be uint8 or bool")
+        if key_mask.shape != (batch, m) or (m > 1 and key_mask.stride(1) != 1):
+            raise ValueError(f"key_mask must be ({batch}, {m}) with a contiguous last axis")
+        a.key_mask = key_mask.data_ptr()
+        a.key_mask_stride = key_mask.stride(0) if batch > 1 else 0
+    if bias is not None:
+        e = [] if edges is None else edges
+        buckets = (len(e) + 1) * (2 if two_sided else 1)
+        a.bias = _flat(bias, "bias", q, torch.float32, (buckets, heads))
+        a.edges = (ctypes.c_int32 * max(len(e), 1))(*e)
+        a.n_edges = len(e)
+        a.two_sided = bool(two_sided)
+    return a
+
+
+def fs_attention_workspace_bytes(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, edges=None,
+                                 two_sided: bool = True, backward: bool = False) -> int:
+    """Bytes that serve the forward call, and the backward call if asked, on
+    tensors of these shapes; edges: the bias's (None without a bias)."""
+    a = AttentionDesc(_DTYPES[q.dtype], q.shape[0], q.shape[1], k.shape[1], q.shape[2],
+                      k.shape[2], q.shape[3], v.shape[3], 1.0)
+    if edges is not None:
+        a.bias = 1  # only tested against NULL
+        a.edges = (ctypes.c_int32 * max(len(edges), 1))(*edges)
+        a.n_edges = len(edges)
+        a.two_sided = bool(two_sided)
+    need = [int(load().fs_attention_workspace_bytes(ctypes.byref(a), b))
+            for b in ((0, 1) if backward else (0,))]
+    if 0 in need:
+        _check(FS_ERR_INVALID_ARG, "fs_attention_workspace_bytes")
+    return max(need)
+
+
+def fs_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                         lse: Optional[torch.Tensor] = None, *, scale: Optional[float] = None,
+                         causal: bool = False, offset: int = 0, offsets=None, q_len=None,
+                         kv_len=None, key_mask=None, bias=None, edges=None,
+                         two_sided: bool = True, workspace: Optional[torch.Tensor] = None,
+                         stream=None):
+    """o <- softmax(scale q.k + bias) v over the visible keys, lse <- the rows'
+    log-sum-exps.  q, o: [batch, n, heads, d or dv]; k, v: [batch, m, kv_heads,
+    d or dv]; lse: [batch, heads, n] float32; scale: 1/sqrt(d) unless given."""
+    lib = load()
+    a = _attention_desc(q, k, v, scale, causal, offset, offsets, q_len, kv_len, key_mask, bias,
+                        edges, two_sided)
+    need = 0
+    if workspace is None:
+        need = lib.fs_attention_workspace_bytes(ctypes.byref(a), 0)
+        if need == 0:
+            _check(FS_ERR_INVALID_ARG, "fs_attention_forward")
+    ws, size, _keep = _work(workspace, need, q, stream)
+    args = (ctypes.byref(a), _rows(q, "q", q, q.shape),
+            _rows(k, "k", q, (a.batch, a.m, a.kv_heads, a.d)),
+            _rows(v, "v", q, (a.batch, a.m, a.kv_heads, a.dv)),
+            _rows(o, "o", q, (a.batch, a.n, a.heads, a.dv)),
+            _flat(lse, "lse", q, torch.float32, (a.batch, a.heads, a.n)), ws, size)
+    return _check(_run_on(q, stream, lambda s: lib.fs_attention_forward(*args, s)),
+                  "fs_attention_forward")
+
+
+def fs_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                          lse: torch.Tensor, d_o: torch.Tensor, d_q=None, d_k=None, d_v=None, *,
+                          d_lse=None, d_bias=None, scale: Optional[float] = None,
+                          causal: bool = False, offset: int = 0, offsets=None, q_len=None,
+                          kv_len=None, key_mask=None, bias=None, edges=None,
+                          two_sided: bool = True, workspace: Optional[torch.Tensor] = None,
+                          stream=None):
+    """Gradients of fs_attention_forward from those of o (d_o) and lse (d_lse,
+    optional): writes d_q, d_k, d_v and d_bias, each of its input's shape;
+    None: not wanted."""
+    lib = load()
+    a = _attention_desc(q, k, v, scale, causal, offset, offsets, q_len, kv_len, key_mask, bias,
+                        edges, two_sided)
+    need = 0
+    if workspace is None:
+        need = lib.fs_attention_workspace_bytes(ctypes.byref(a), 1)
+        if need == 0:
+            _check(FS_ERR_INVALID_ARG, "fs_attention_backward")
+    ws, size, _keep = _work(workspace, need, q, stream)
+    f32, lses = torch.float32, (a.batch, a.heads, a.n)
+    if lse is None or o is None or d_o is None:
+        raise TypeError("o, lse and d_o must be given")
+    ks, vs = (a.batch, a.m, a.kv_heads, a.d), (a.batch, a.m, a.kv_heads, a.dv)
+    os_ = (a.batch, a.n, a.heads, a.dv)
+    args = (ctypes.byref(a), _rows(q, "q", q, q.shape), _rows(k, "k", q, ks),
+            _rows(v, "v", q, vs), _rows(o, "o", q, os_), _flat(lse, "lse", q, f32, lses),
+            _rows(d_o, "d_o", q, os_), _flat(d_lse, "d_lse", q, f32, lses),
+            _rows(d_q, "d_q", q, q.shape), _rows(d_k, "d_k", q, ks), _rows(d_v, "d_v", q, vs),
+            _flat(d_bias, "d_bias", q, f32, bias.shape if bias is not None else ()), ws, size)
+    return _check(_run_on(q, stream, lambda s: lib.fs_attention_backward(*args, s)),
+                  "fs_attention_backward")
+
+
+def _norm_desc(q, k, eps, cos, sin, positions, offset, interleaved):
+    like = q if q is not None else k
+    if not isinstance(like, torch.Tensor) or not like.is_cuda:
+        raise TypeError("q or k must be a device tensor")
+    if like.dtype not in _DTYPES:
+        raise TypeError(f"q and k must be float32, bfloat16 or float16 (is {like.dtype})")
+    if like.dim() != 4:
+        raise ValueError("q and k must be [batch, rows, heads, d]")
+    batch, n, _, d = like.shape
+    a = QkNormDesc(_DTYPES[like.dtype], batch, n, q.shape[2] if q is not None else 0,
+                   k.shape[2] if k is not None else 0, d, 0, bool(interleaved), eps)
+    if (cos is None) != (sin is None):
+        raise TypeError("cos and sin must both be given or both be None")
+    if cos is not None:
+        if cos.dim() != 2:
+            raise ValueError("cos and sin must be [positions, rot / 2]")
+        a.rot, a.n_pos = 2 * cos.shape[1], cos.shape[0]
+        a.cos_table = _flat(cos, "cos", like, torch.float32, cos.shape)
+        a.sin_table = _flat(sin, "sin", like, torch.float32, cos.shape)
+    if positions is not None:
+        _on(positions, "positions", like)
+        if positions.dtype != torch.int32 or positions.shape != (batch, n) or \
+                (n > 1 and positions.stride(1) != 1):
+            raise TypeError(f"positions must be int32 ({batch}, {n}) with a contiguous last axis")
+        a.positions = positions.data_ptr()
+        a.positions_stride = positions.stride(0) if batch > 1 else 0
+    a.offset = offset
+    return a, like
+
+
+def _norm_shapes(a):
+    return (a.batch, a.n, a.heads_q, a.d), (a.batch, a.n, a.heads_k, a.d)
+
+
+def fs_qk_norm_workspace_bytes(q, k) -> int:
+    """Bytes of workspace of fs_qk_norm_rotate_backward on tensors of these shapes."""
+    a, _ = _norm_desc(q, k, 0.0, None, None, None, 0, False)
+    need = int(load().fs_qk_norm_workspace_bytes(ctypes.byref(a)))
+    if need == 0:
+        _check(FS_ERR_INVALID_ARG, "fs_qk_norm_workspace_bytes")
+    return need
+
+
+def fs_qk_norm_rotate(q, k, q_weight, k_weight, q_out, k_out, *, eps: float = 1e-6, cos=None,
+                      sin=None, positions=None, offset: int = 0, interleaved: bool = False,
+                      stream=None):
+    """Norm of every head's row of q and k ([batch, n, heads, d]; either may be
+    None) times its weight, and the rotation of the first 2 * cos.shape[1]
+    elements by the position's row of cos and sin ([positions, rot / 2])."""
+    lib = load()
+    a, like = _norm_desc(q, k, eps, cos, sin, positions, offset, interleaved)
+    qs, ks = _norm_shapes(a)
+    f32, w = torch.float32, (a.d,)
+    args = (ctypes.byref(a), _rows(q, "q", like, qs), _rows(k, "k", like, ks),
+            _flat(q_weight, "q_weight", like, f32, w), _flat(k_weight, "k_weight", like, f32, w),
+            _rows(q_out, "q_out", like, qs), _rows(k_out, "k_out", like, ks))
+    return _check(_run_on(like, stream, lambda s: lib.fs_qk_norm_rotate(*args, s)),
+                  "fs_qk_norm_rotate")
+
+
+def fs_qk_norm_rotate_backward(q, k, q_weight, k_weight, d_q_out, d_k_out, d_q, d_k,
+                               d_q_weight=None, d_k_weight=None, *, eps: float = 1e-6, cos=None,
+                               sin=None, positions=None, offset: int = 0,
+                               interleaved: bool = False,
+                               workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of fs_qk_norm_rotate: writes d_q, d_k and, where given, the
+    weights' gradients."""
+    lib = load()
+    a, like = _norm_desc(q, k, eps, cos, sin, positions, offset, interleaved)
+    need = 0
+    if workspace is None:
+        need = lib.fs_qk_norm_workspace_bytes(ctypes.byref(a))
+        if need == 0:
+            _check(FS_ERR_INVALID_ARG, "fs_qk_norm_rotate_backward")
+    ws, size, _keep = _work(workspace, need, like, stream)
+    qs, ks = _norm_shapes(a)
+    f32, w = torch.float32, (a.d,)
+    args = (ctypes.byref(a), _rows(q, "q", like, qs), _rows(k, "k", like, ks),
+            _flat(q_weight, "q_weight", like, f32, w), _flat(k_weight, "k_weight", like, f32, w),
+            _rows(d_q_out, "d_q_out", like, qs), _rows(d_k_out, "d_k_out", like, ks),
+            _rows(d_q, "d_q", like, qs), _rows(d_k, "d_k", like, ks),
+            _flat(d_q_weight, "d_q_weight", like, f32, w),
+            _flat(d_k_weight, "d_k_weight", like, f32, w), ws, size)
+    return _check(_run_on(like, stream, lambda s: lib.fs_qk_norm_rotate_backward(*args, s)),
+                  "fs_qk_norm_rotate_backward")
