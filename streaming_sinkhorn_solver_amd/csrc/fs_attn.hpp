@@ -53,6 +53,26 @@ struct El<OP_F32> {
     }
 };
 
+// Shared memory by its LDS address (the low half of a shared object's generic
+// address): loads and stores of a known address space whatever the pointer
+// went through.
+__device__ __forceinline__ uint32_t lds_addr(const void* p) { return (uint32_t)(uintptr_t)p; }
+template <typename V>
+__device__ __forceinline__ V lds_read(uint32_t a) {
+    typedef __attribute__((address_space(3))) V lds_v;
+    return *(const lds_v*)(uintptr_t)a;
+}
+template <typename V>
+__device__ __forceinline__ void lds_write(uint32_t a, const V& v) {
+    typedef __attribute__((address_space(3))) V lds_v;
+    *(lds_v*)(uintptr_t)a = v;
+}
+struct LdsFloats {
+    uint32_t a;
+    __device__ __forceinline__ float operator[](int i) const { return lds_read<float>(a + 4 * i); }
+    __device__ __forceinline__ void set(int i, float x) const { lds_write<float>(a + 4 * i, x); }
+};
+
 // The other half's value of the same column (lane l ^ 32).
 __device__ __forceinline__ float half_max(float x) {
     auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -83,13 +103,13 @@ struct Tile {
 
     // Operand whose rows (or columns) are the tile's rows r0 + (lane & 31),
     // contraction over elements 16 kk + 8 h + 0..7.
-    static __device__ __forceinline__ Frag frag_rows(const char* t, int r0, int kk, int lane) {
+    static __device__ __forceinline__ Frag frag_rows(uint32_t t, int r0, int kk, int lane) {
         const int r = r0 + (lane & 31), h = lane >> 5;
         if constexpr (sizeof(T) == 2) {
-            return *(const Frag*)(t + at(r, 2 * kk + h));
+            return lds_read<Frag>(t + at(r, 2 * kk + h));
         } else {
-            const f32x4 lo = *(const f32x4*)(t + at(r, 4 * kk + 2 * h));
-            const f32x4 hi = *(const f32x4*)(t + at(r, 4 * kk + 2 * h + 1));
+            const f32x4 lo = lds_read<f32x4>(t + at(r, 4 * kk + 2 * h));
+            const f32x4 hi = lds_read<f32x4>(t + at(r, 4 * kk + 2 * h + 1));
             return Frag{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         }
     }
@@ -98,7 +118,7 @@ struct Tile {
     // contraction over the tile's rows r0 + 8 (e >> 2) + 4 h + (e & 3).
     // 16-bit types: ds_read_b64_tr_b16 hands lane i of 16 the i-th column of
     // the 4 x 16 block whose row i >> 2, columns 4 (i & 3) + 0..3 it addresses.
-    static __device__ __forceinline__ Frag frag_cols(const char* t, int r0, int cb, int lane) {
+    static __device__ __forceinline__ Frag frag_cols(uint32_t t, int r0, int cb, int lane) {
         const int h = lane >> 5;
         if constexpr (sizeof(T) == 2) {
             typedef __attribute__((__vector_size__(8))) short s16x4;
@@ -106,13 +126,13 @@ struct Tile {
             const int i = lane & 15;
             const int r = r0 + 4 * h + (i >> 2);
             const int c = cb * 4 + ((lane >> 4) & 1) * 2 + ((i & 3) >> 1);
-            const char* p = t + at(r, c) + (i & 1) * 8;
+            const uint32_t p = t + at(r, c) + (i & 1) * 8;
             union {
                 s16x4 q[2];
                 Frag f;
             } u;
-            u.q[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-            u.q[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 8 * kRow));
+            u.q[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)p);
+            u.q[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(p + 8 * kRow));
             return u.f;
         } else {
             Frag f;
@@ -120,7 +140,7 @@ struct Tile {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int r = r0 + 8 * (e >> 2) + 4 * h + (e & 3);
-                f[e] = *(const float*)(t + at(r, x >> 2) + (x & 3) * 4);
+                f[e] = lds_read<float>(t + at(r, x >> 2) + (x & 3) * 4);
             }
             return f;
         }
@@ -173,38 +193,96 @@ __device__ __forceinline__ void load_row_frags(const typename El<OP>::T* row, bo
     }
 }
 
-// A tile's rows on their way from global memory to LDS, in the registers of
-// NT threads: loaded while the previous tile is in use, stored when it is
-// done with.  Rows whose bit in `seen` is clear are stored as zeros and never
-// read: what stands there (NaN in padding, memory behind the tensor) cannot
-// enter a product.
+// Sixteen bytes that no one writes: the source of rows that do not exist.
+static __device__ __attribute__((aligned(16))) const uint32_t attn_zeros[4] = {0, 0, 0, 0};
+
+// One wave-wide 16-byte-per-lane copy to LDS: lane i's bytes at src_i land at
+// lds + 16 i (lds wave-uniform).  Not modelled by the compiler: the
+// caller waits (dma_wait) before it reads, and before a barrier publishes it.
+__device__ __forceinline__ void dma_lane16(const char* src, uint32_t lds) {
+    uint32_t saved;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %1\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dwordx4 %2, off\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src)
+        : "memory");
+}
+// The same with 4 bytes a lane.
+__device__ __forceinline__ void dma_lane4(const char* src, uint32_t lds) {
+    uint32_t saved;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %1\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dword %2, off\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src)
+        : "memory");
+}
+// The wave's copies have landed and its own LDS reads are done (so the buffer
+// they came from may be filled again).
+__device__ __forceinline__ void dma_wait() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+}
+
+// Fills a tile of ROWS rows in LDS from global memory, by NT threads (whole
+// waves; t counts within them).  Chunk positions in LDS are dealt out in
+// order, so a lane fetches the chunk that belongs at its position.  Rows whose
+// bit in `seen` is clear are filled with zeros and never read: what stands
+// there (NaN in padding, memory behind the tensor) cannot enter a product.
+// Aligned rows (vec) go straight to LDS and are complete after dma_wait();
+// others are loaded element by element and stored at once.
 template <int OP, int DP, int ROWS, int NT>
-struct Stage {
+struct Loader {
     using L = Tile<OP, DP>;
     using T = typename El<OP>::T;
-    static constexpr int kN = ROWS * L::kCh / NT;
-    static_assert(ROWS * L::kCh % NT == 0 && (NT % L::kCh) == 0, "whole rows per step");
-    u32x4 v[kN];
+    static constexpr int kN = ROWS * L::kCh / NT, kStep = NT / L::kCh;
+    static_assert(ROWS * L::kCh % NT == 0 && NT % L::kCh == 0, "whole rows per step");
+    static constexpr uint64_t kAll = ROWS == 64 ? ~0ull : (1ull << ROWS) - 1;
 
-    __device__ __forceinline__ void load(const T* base, int64_t stride, uint64_t seen, int d,
-                                         bool vec, int t) {
-        const int c = t % L::kCh, r0 = t / L::kCh;
+    static __device__ __forceinline__ void fill(uint32_t lds, const T* base, int64_t stride,
+                                                uint64_t seen, int w, bool vec, int t) {
+        const int c0 = t % L::kCh, r0 = t / L::kCh;
+        const uint32_t dst = lds + (t & ~63) * 16;
+        if (vec) {
+            const char* src = (const char*)(base + r0 * stride);
+            const int64_t step = kStep * stride * (int64_t)sizeof(T);
+            if (w == DP && (seen & kAll) == kAll) {
 #pragma unroll
-        for (int s = 0; s < kN; ++s) {
-            const int r = r0 + s * (NT / L::kCh);
-            T x[L::kEpc];
+                for (int s = 0; s < kN; ++s, src += step)
+                    dma_lane16(src + ((c0 ^ L::swz(r0 + s * kStep)) << 4), dst + s * NT * 16);
+            } else {
 #pragma unroll
-            for (int e = 0; e < L::kEpc; ++e) x[e] = (T)0.f;
-            if ((seen >> r) & 1) load_elems<OP, L::kEpc>(base + r * stride, c * L::kEpc, d, vec, x);
-            __builtin_memcpy(&v[s], x, 16);
+                for (int s = 0; s < kN; ++s, src += step) {
+                    const int r = r0 + s * kStep, c = c0 ^ L::swz(r);
+                    const bool ok = ((seen >> r) & 1) && c * L::kEpc < w;
+                    dma_lane16(ok ? src + (c << 4) : (const char*)attn_zeros, dst + s * NT * 16);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < kN; ++s) {
+                const int r = r0 + s * kStep, c = c0 ^ L::swz(r);
+                T x[L::kEpc];
+#pragma unroll
+                for (int e = 0; e < L::kEpc; ++e) x[e] = (T)0.f;
+                if ((seen >> r) & 1) load_elems<OP, L::kEpc>(base + r * stride, c * L::kEpc, w, false, x);
+                u32x4 v;
+                __builtin_memcpy(&v, x, 16);
+                lds_write<u32x4>(lds + (s * NT + t) * 16, v);
+            }
         }
     }
-    __device__ __forceinline__ void store(char* lds, int t) const {
-        const int c = t % L::kCh, r0 = t / L::kCh;
-#pragma unroll
-        for (int s = 0; s < kN; ++s) *(u32x4*)(lds + L::at(r0 + s * (NT / L::kCh), c)) = v[s];
-    }
 };
+
+// Order between a wave's own LDS stores and loads (issued in order; the fence
+// keeps the compiler from exchanging them).
+__device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
 // The keys of a batch entry that exist, and the position of query row 0.
 __device__ __forceinline__ int attn_kv_len(const AttnArgs& a, int b) {
@@ -251,9 +329,9 @@ __device__ __forceinline__ int bucket_of(const AttnArgs& a, int r) {
 // weight: in base 2 the lowest would leave the range, and next to it scores
 // would be lost in rounding anyway.
 __device__ __forceinline__ float bias2(float x) { return x <= -1e30f ? -INFINITY : x * kLog2e; }
-__device__ __forceinline__ void load_line(const AttnArgs& a, int head, float* line, int t, int nt) {
+__device__ __forceinline__ void load_line(const AttnArgs& a, int head, LdsFloats line, int t, int nt) {
     for (int i = t; i < a.r0 + a.rp + 1; i += nt)
-        line[i] = bias2(a.bias[(int64_t)bucket_of(a, i - a.r0) * a.H + head]);
+        line.set(i, bias2(a.bias[(int64_t)bucket_of(a, i - a.r0) * a.H + head]));
 }
 
 // Work item of a 1-D grid, consecutive ones on the same XCD: workgroups go to

@@ -153,6 +153,8 @@ fs_status take_desc(const fs_attention_desc* p, AttnArgs& a) {
     a.G = d.heads / d.kv_heads;
     a.d = d.d;
     a.dv = d.dv;
+    a.n_pad = (int)(cdiv(d.n, kAttnRowPad) * kAttnRowPad);
+    a.dv_pad = (d.dv + 3) / 4 * 4;
     a.scale = d.scale;
     a.c = d.scale * 1.4426950408889634f;
     a.causal = d.causal != 0;
@@ -200,16 +202,24 @@ fs_status take_desc(const fs_attention_desc* p, AttnArgs& a) {
         a.split_keys = (int)(cdiv(cdiv(d.m, s), 128) * 128);
         a.n_split = (int)cdiv(d.m, a.split_keys);
     }
-    const int64_t kitems = (int64_t)d.batch * d.kv_heads * cdiv(d.m, kAttnRows);
+    // Backward passes: 128 rows a workgroup where that fills the chip, else 32,
+    // and then the queries in ranges if there are few keys.
+    const int width = std::max(d.d, d.dv), es = elem_size(d.dtype);
+    const bool can = (width <= 64 ? 64 : width <= 128 ? 128 : 256) * es <= 256;
+    a.alone_q = can && (int64_t)d.batch * d.heads * cdiv(d.n, kAttnRows) < kCus;
+    a.alone_k = can && (int64_t)d.batch * d.kv_heads * cdiv(d.m, kAttnRows) < kCus;
+    const int64_t kblocks = cdiv(d.m, a.alone_k ? 32 : kAttnRows);
+    const int64_t kitems = (int64_t)d.batch * d.kv_heads * kblocks;
     a.q_split = 1;
     a.split_rows = d.n;
     if (kitems > 0 && d.n > 0) {
         const int64_t want = kCus / kitems;
-        const int64_t most = std::min<int64_t>(16, (int64_t)d.n * a.G / 512);
+        const int64_t most = std::min<int64_t>(16, d.n / 256);
         const int64_t s = std::max<int64_t>(1, std::min(want, most));
         a.split_rows = (int)(cdiv(cdiv(d.n, s), 64) * 64);
         a.q_split = (int)cdiv(d.n, a.split_rows);
     }
+    a.line_blocks = (int)(a.q_split * kblocks);
     return FS_OK;
 }
 
@@ -222,17 +232,19 @@ FwdLayout fwd_layout(const AttnArgs& a) {
         const size_t rows = (size_t)a.B * a.H * a.n;
         l.ml = 0;
         l.o = up((size_t)a.n_split * rows * sizeof(float2));
-        l.total = l.o + up((size_t)a.n_split * rows * a.dv * 4);
+        l.total = l.o + up((size_t)a.n_split * rows * a.dv_pad * 4);
     }
     return l;
 }
 
 struct BwdLayout {
-    size_t delta = 0, pk = 0, pv = 0, line = 0, total = kAlign;
+    size_t nl2 = 0, delta = 0, pk = 0, pv = 0, line = 0, total = kAlign;
 };
 BwdLayout bwd_layout(const AttnArgs& a) {
     BwdLayout l;
-    size_t at = up((size_t)a.B * a.H * a.n * 4);
+    const size_t terms = up((size_t)a.B * a.H * a.n_pad * 4);
+    l.delta = terms;
+    size_t at = 2 * terms;
     if (a.q_split > 1) {
         const size_t rows = (size_t)a.B * a.K * a.m;
         l.pk = at;
@@ -242,7 +254,7 @@ BwdLayout bwd_layout(const AttnArgs& a) {
     }
     if (a.bias) {
         l.line = at;
-        at += up((size_t)a.H * a.B * cdiv(a.n, kAttnRows) * (a.r0 + a.rp + 1) * 4);
+        at += up((size_t)a.H * a.B * a.line_blocks * (a.r0 + a.rp + 1) * 4);
     }
     l.total = std::max(at, kAlign);
     return l;
@@ -414,6 +426,7 @@ fs_status fs_attention_backward(const fs_attention_desc* desc, fs_rows q, fs_row
     a.lse = const_cast<float*>(lse);
     a.glse = d_lse;
     a.gbias = d_bias;
+    a.nl2 = (float*)((char*)workspace + l.nl2);
     a.delta = (float*)((char*)workspace + l.delta);
     a.part_k = (float*)((char*)workspace + l.pk);
     a.part_v = (float*)((char*)workspace + l.pv);
@@ -422,11 +435,11 @@ fs_status fs_attention_backward(const fs_attention_desc* desc, fs_rows q, fs_row
     const char* where = "fs_attention_backward";
     const bool rows = a.B > 0 && a.n > 0, keys = a.B > 0 && a.m > 0;
     if (rows) FS_TRY(hip_status(launch_attn_delta(a, s), where));
-    if (keys && (a.gk.p || a.gv.p)) {
+    if (rows && (a.gq.p || a.gbias)) FS_TRY(hip_status(launch_attn_bwd_q(a, s), where));
+    if (keys && (a.gk.p || a.gv.p || a.gbias)) {
         FS_TRY(hip_status(launch_attn_bwd_kv(a, s), where));
         if (a.q_split > 1) FS_TRY(hip_status(launch_attn_kv_merge(a, s), where));
     }
-    if (rows && (a.gq.p || a.gbias)) FS_TRY(hip_status(launch_attn_bwd_q(a, s), where));
     if (a.gbias) FS_TRY(hip_status(launch_attn_bias_sum(a, s), where));
     return FS_OK;
 }

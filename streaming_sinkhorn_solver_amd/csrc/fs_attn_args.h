@@ -14,6 +14,7 @@ constexpr int kAttnMaxEdge = 1024;     // the largest edge (a bias line stays wi
 constexpr int kAttnMaxOffset = 1 << 29;  // j - i - offset stays a 32-bit number
 constexpr int kAttnMaxSplit = 64;
 constexpr int kAttnRows = 128;         // query (or key) rows of a workgroup of four waves
+constexpr int kAttnRowPad = 64;       // row terms are padded to whole query tiles
 constexpr int kAttnFewRows = 32;       // packed rows of a workgroup of the few-row kernel
 
 // Strides are in elements: batch, row, head.
@@ -28,7 +29,11 @@ struct AttnArgs {
     AttnView go, gq, gk, gv;  // backward: gradients of o, q, k, v
     float* lse;               // [B][H][n]
     const float* glse;        // gradient of lse or NULL
-    float* delta;             // backward workspace: [B][H][n]
+    int n_pad;                // n rounded up to kAttnRowPad
+    float* nl2;               // backward workspace: [B][H][n_pad] -lse in base 2, and
+    float* delta;             //   do.o - glse, refined by the pass over the keys
+    int alone_q, alone_k;     // backward passes with 32 rows a workgroup (see BwdShape)
+    int line_blocks;          // parts of a batch entry in line_part
     int op;                   // ScoreOp
     int B, n, m, H, K, G, d, dv;
     float scale, c;           // c = scale log2(e)
@@ -42,12 +47,13 @@ struct AttnArgs {
     int n_edges, two_sided, r0, rp;
     uint16_t edges[kAttnMaxEdges + 1];
     int n_split, split_keys;  // key ranges of the forward pass
-    float* part_o;            // [n_split][B H n][dv]
+    int dv_pad;               // dv rounded up to whole 16-byte chunks of fp32
+    float* part_o;            // [n_split][B H n][dv_pad]
     float2* part_ml;          // [n_split][B H n]: reference and sum
     int q_split, split_rows;  // query ranges of the key gradients
     float* part_k;            // [q_split][B K m][d]
     float* part_v;            // [q_split][B K m][dv]
-    float* line_part;         // bias gradient: [H][B q-blocks][r0 + rp + 1]
+    float* line_part;         // bias gradient: [H][B line_blocks][r0 + rp + 1]
     float* gbias;             // [buckets][H]
 };
 

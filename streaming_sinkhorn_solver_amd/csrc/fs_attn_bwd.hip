@@ -30,24 +30,26 @@ __device__ __forceinline__ void store4(typename El<OP>::T* row, int x0, int d, b
     }
 }
 
-// ---- delta ----------------------------------------------------------------
-// 16 lanes a row.
+// ---- row terms ------------------------------------------------------------
+// Per query row, for the two passes: -L in base 2 (-inf for a row that takes
+// no part: 2^(s - inf) = 0) and delta from the stored o.  Rows are padded to
+// whole tiles with the values of a row that takes no part.  16 lanes a row.
 template <int OP>
 __global__ __launch_bounds__(256) void attn_delta_kernel(const AttnArgs a) {
     using T = typename El<OP>::T;
     constexpr int EPC = 16 / sizeof(T);
-    const int64_t rows = (int64_t)a.B * a.n * a.H;
+    const int64_t rows = (int64_t)a.B * a.n_pad * a.H;
     const int64_t r = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
     const int lane = threadIdx.x & 15;
     if (r >= rows) return;
     const int head = (int)(r % a.H);
     const int64_t bi = r / a.H;
-    const int i = (int)(bi % a.n), b = (int)(bi / a.n);
-    const T* o = (const T*)a.o.p + b * a.o.sb + (int64_t)i * a.o.sr + head * a.o.sh;
-    const T* g = (const T*)a.go.p + b * a.go.sb + (int64_t)i * a.go.sr + head * a.go.sh;
+    const int i = (int)(bi % a.n_pad), b = (int)(bi / a.n_pad);
     const bool ok = i < attn_q_len(a, b);
     float s = 0.f;
-    if (ok)
+    if (ok) {
+        const T* o = (const T*)a.o.p + b * a.o.sb + (int64_t)i * a.o.sr + head * a.o.sh;
+        const T* g = (const T*)a.go.p + b * a.go.sb + (int64_t)i * a.go.sr + head * a.go.sh;
         for (int x = lane * EPC; x < a.dv; x += 16 * EPC) {
             T p[EPC], q[EPC];
             load_elems<OP, EPC>(o, x, a.dv, a.o.vec, p);
@@ -55,20 +57,25 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(const AttnArgs a) {
 #pragma unroll
             for (int e = 0; e < EPC; ++e) s = fmaf((float)p[e], (float)q[e], s);
         }
+    }
 #pragma unroll
     for (int m = 8; m >= 1; m >>= 1) s += __shfl_xor(s, m, 64);
     if (lane == 0) {
         const int64_t at = ((int64_t)b * a.H + head) * a.n + i;
-        a.delta[at] = ok ? s - (a.glse ? a.glse[at] : 0.f) : 0.f;
+        const float l = ok ? a.lse[at] : -INFINITY;
+        const bool part = l != -INFINITY;
+        const int64_t to = ((int64_t)b * a.H + head) * a.n_pad + i;
+        a.nl2[to] = part ? -l * kLog2e : -INFINITY;
+        a.delta[to] = part ? s - (a.glse ? a.glse[at] : 0.f) : 0.f;
     }
 }
 
 // ---- rounding of dS -------------------------------------------------------
 // dS goes into its product in the element type.  Its size follows the
 // gradient's, which fp16's exponents need not hold, so for fp16 every column
-// (a lane pair) carries a power of two that keeps its largest value so far
-// between 2^6 and 2^15, and the sums are divided by it at the end.  P is at
-// most 1 and is lifted by 2^14 (fp16).
+// (a lane pair) carries a power of two, set by its first values to bring the
+// largest to 2^10 and lowered when one passes 2^15 (fp16 ends at 2^16), and
+// the sums are divided by it at the end.  P is at most 1 and is lifted by 2^14.
 template <int OP>
 constexpr float kLiftP = OP == OP_F16 ? 16384.f : 1.f;
 
@@ -107,39 +114,94 @@ struct DsScale {
     __device__ __forceinline__ float undo() const { return 1.f / f; }
 };
 
-template <int OP, int DP>
-constexpr int kBwdTile = DP * (int)sizeof(typename El<OP>::T) <= 256 ? 64 : 32;
+// Rows of a tile, and whether the waves of a workgroup share it.  Shared: four
+// waves hold 32 rows each and pass over the same tiles, fetched once for all.
+// Alone (few rows in all): they hold the same 32 rows, each passes over every
+// fourth tile, fetched for itself, and their sums are joined at the end -- four
+// times the workgroups and a quarter of the steps for four times the fetches.
+// Rows of 512 bytes leave no LDS for tiles of four waves: always shared.
+template <int OP, int DP, bool ALONE>
+struct BwdShape {
+    static constexpr int kRow = Tile<OP, DP>::kRow;
+    static constexpr int kTile = !ALONE && kRow <= 256 ? 64 : 32;
+    static constexpr int kBufs = ALONE && kRow > 128 ? 1 : 2;
+    static constexpr int kSets = ALONE ? 4 : 1;
+    static constexpr int kRows = ALONE ? 32 : kAttnRows;  // rows a workgroup holds
+};
 
-// ---- dK, dV ---------------------------------------------------------------
-// A workgroup holds 128 keys of one key head, 32 a wave, as operands, and
-// passes over the queries of every head of the group in tiles staged in LDS.
-// Scores are formed with queries in the rows, so a lane holds one key's
-// column: a key that is masked out spoils nothing but its own column, which
-// is written as zero, and needs no test in the loop.
-template <int OP, int DP, bool BIAS>
-__global__ __launch_bounds__(256, 1) void attn_bwd_kv_kernel(const AttnArgs a) {
+// Joins one lane-held 32-column result of four waves: adds waves 1..3 to wave 0
+// through LDS (buf: 3 * DP * 32 floats), in order.
+template <int DP, int ND>
+__device__ __forceinline__ void join_waves(f32x16 (&x)[ND], LdsFloats buf, int wid, int lane) {
+    const int h = lane >> 5;
+    __syncthreads();
+    if (wid > 0) {
+#pragma unroll
+        for (int cb = 0; cb < ND; ++cb)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                buf.set(((wid - 1) * DP + 32 * cb + 8 * (r >> 2) + 4 * h + (r & 3)) * 32 + (lane & 31),
+                        x[cb][r]);
+    }
+    __syncthreads();
+    if (wid == 0) {
+#pragma unroll
+        for (int w = 0; w < 3; ++w)
+#pragma unroll
+            for (int cb = 0; cb < ND; ++cb)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    x[cb][r] += buf[(w * DP + 32 * cb + 8 * (r >> 2) + 4 * h + (r & 3)) * 32 + (lane & 31)];
+    }
+}
+
+// ---- dK, dV, dT -----------------------------------------------------------
+// A workgroup holds keys of one key head, 32 a wave, as operands, and passes
+// over the queries of every head of the group in tiles staged in LDS.  Scores
+// are formed with queries in the rows, so a lane holds one key's column: a key
+// that is masked out spoils nothing but its own column, which is written as
+// zero, and needs no test in the loop (but for the bias, whose sums run over
+// columns).
+//
+// Bias gradient: dS summed over the pairs of every relative position r, and
+// those sums over each bucket by attn_bias_sum_kernel.  A block whose pairs all
+// lie beyond the last edge goes into one of two running sums of the lane.  For
+// a block near the diagonal a wave writes the 32 x 32 values to its own LDS
+// with key x's row moved by x, so that a relative position is a column, and 63
+// lanes sum a column each; positions between the last edges are added to the
+// wave's line in LDS (one lane a position), those beyond to the lane's sums.
+constexpr int kDiag = 64;
+template <int OP, int DP, bool BIAS, bool ALONE>
+__global__ __launch_bounds__(256, (Tile<OP, DP>::kRow <= 128 && !(BIAS && ALONE) ? 2 : 1)) void attn_bwd_kv_kernel(const AttnArgs a) {
     using E = El<OP>;
     using T = typename E::T;
     using L = Tile<OP, DP>;
-    constexpr int QT = 32, ND = DP / 32, NK = DP / 16;
-    __shared__ __attribute__((aligned(256))) char qt[QT * L::kRow];
-    __shared__ __attribute__((aligned(256))) char gt[QT * L::kRow];
-    __shared__ __attribute__((aligned(16))) float row_l[QT], row_d[QT];
-    __shared__ float line[BIAS ? 2 * kAttnMaxEdge + 1 : 1];
+    using S = BwdShape<OP, DP, ALONE>;
+    constexpr int QT = S::kTile, ND = DP / 32, NK = DP / 16;
+    using Load = Loader<OP, DP, QT, ALONE ? 64 : 256>;
+    __shared__ __attribute__((aligned(256))) char tiles[S::kSets][S::kBufs][2][QT * L::kRow];
+    __shared__ __attribute__((aligned(16))) float row_t[S::kSets][S::kBufs][2][QT];
+    __shared__ float diag[BIAS ? 4 : 1][BIAS ? 32 * kDiag : 1];
+    extern __shared__ float lines[];  // BIAS: [1 + 4][n_line], the bias and the waves' sums
+    static_assert(!ALONE || sizeof(tiles) >= 3 * 32 * DP * 4, "the waves' sums fit the tiles' memory");
 
     const int t = threadIdx.x, lane = t & 63, wid = t >> 6, h = lane >> 5;
-    const int nkb = (a.m + kAttnRows - 1) / kAttnRows;
+    const int set = ALONE ? wid : 0;
+    const int nkb = (a.m + S::kRows - 1) / S::kRows;
     int w = xcd_item(blockIdx.x, gridDim.x);
     const int kb = w % nkb;
     w /= nkb;
     const int split = w % a.q_split;
     w /= a.q_split;
     const int kvh = w % a.K, b = w / a.K;
+    const int n_line = a.r0 + a.rp + 1;
+    const LdsFloats line{lds_addr(lines)}, gline{line.a + 4 * (1 + wid) * n_line};
+    const LdsFloats dg{lds_addr(diag[BIAS ? wid : 0])};
 
     const int off = attn_offset(a, b);
     const int len = attn_kv_len(a, b);
     const int qlen = attn_q_len(a, b);
-    const int j0 = kb * kAttnRows + wid * 32, j = j0 + (lane & 31);
+    const int j0 = kb * S::kRows + (ALONE ? 0 : wid * 32), j = j0 + (lane & 31);
     bool key_ok = j < len;
     if (key_ok && a.key_mask) key_ok = a.key_mask[b * a.mask_stride + j] != 0;
 
@@ -155,109 +217,192 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_kv_kernel(const AttnArgs a) {
         for (int r = 0; r < 16; ++r) dk[x][r] = dvv[x][r] = 0.f;
     DsScale<OP, ND> dss;
 
-    // the first query that sees a key of this block
+    // tiles of this workgroup's query range, from the first that sees a key of
+    // this block on
     int first = split * a.split_rows;
     const int end = a.q_split == 1 ? qlen : min(qlen, first + a.split_rows);
-    if (a.causal) first = max(first, (max(0, kb * kAttnRows - off) / QT) * QT);
-    if (kb * kAttnRows >= len) first = end;
+    if (a.causal) first = max(first, (max(0, kb * S::kRows - off) / QT) * QT);
+    if (kb * S::kRows >= len) first = end;
+    const int n_tiles = first < end ? (end - first + QT - 1) / QT : 0;
+    if (BIAS && a.gbias)
+        for (int x = lane; x < 32 * kDiag; x += 64) dg.set(x, 0.f);
 
-    for (int g = 0; g < a.G; ++g) {
-        const int head = kvh * a.G + g;
-        const T* qbase = (const T*)a.q.p + b * a.q.sb + head * a.q.sh;
-        const T* gbase = (const T*)a.go.p + b * a.go.sb + head * a.go.sh;
-        const int64_t lrow = ((int64_t)b * a.H + head) * a.n;
+    // With a bias the heads are taken one after the other (each has its line);
+    // else the tiles of all heads are one sequence.
+    const int step = ALONE ? 4 : 1;
+    for (int g0 = 0; g0 < (BIAS ? a.G : 1); ++g0) {
+        const int n_all = BIAS ? n_tiles : n_tiles * a.G;
+        float sum_lo = 0.f, sum_hi = 0.f;
         if (BIAS) {
             __syncthreads();
-            load_line(a, head, line, t, 256);
+            load_line(a, kvh * a.G + g0, line, t, 256);
+            if (a.gbias)
+                for (int x = lane; x < n_line; x += 64) gline.set(x, 0.f);
+            __syncthreads();
         }
-        Stage<OP, DP, QT, 256> qs, gs;
-        float nl = 0.f, nd = 0.f;
-        auto fetch = [&](int i0) {
-            const uint64_t seen = bits_upto(end - 1 - i0);
-            qs.load(qbase + (int64_t)i0 * a.q.sr, a.q.sr, seen, a.d, a.q.vec, t);
-            gs.load(gbase + (int64_t)i0 * a.go.sr, a.go.sr, seen, a.dv, a.go.vec, t);
-            if (t < QT) {
-                const bool ok = i0 + t < end;
-                nl = ok ? a.lse[lrow + i0 + t] : -INFINITY;
-                nd = ok ? a.delta[lrow + i0 + t] : 0.f;
+        const auto fetch = [&](int u, int buf) {
+            const int g = BIAS ? g0 : u / n_tiles;
+            const int i0 = first + (BIAS ? u : u - g * n_tiles) * QT, head = kvh * a.G + g;
+            const uint64_t seen = QT == 64 ? ((uint64_t)bits_upto(end - 33 - i0) << 32) | bits_upto(end - 1 - i0)
+                                           : bits_upto(end - 1 - i0);
+            const int tt = ALONE ? lane : t;
+            Load::fill(lds_addr(tiles[set][buf][0]),
+                       (const T*)a.q.p + b * a.q.sb + head * a.q.sh + (int64_t)i0 * a.q.sr, a.q.sr,
+                       seen, a.d, a.q.vec, tt);
+            Load::fill(lds_addr(tiles[set][buf][1]),
+                       (const T*)a.go.p + b * a.go.sb + head * a.go.sh + (int64_t)i0 * a.go.sr,
+                       a.go.sr, seen, a.dv, a.go.vec, tt);
+            // the row terms: 2 QT floats, by one wave (two for QT = 64)
+            const int64_t lrow = ((int64_t)b * a.H + head) * a.n_pad + i0;
+            if (ALONE || wid < 2 * QT / 64) {
+                const int x = ALONE ? lane : t;
+                const float* src = (x < QT ? a.nl2 : a.delta - QT) + lrow + x;
+                dma_lane4((const char*)src, lds_addr(row_t[set][buf]) + 4 * (x & ~63));
             }
         };
-        if (first < end) fetch(first);
-        for (int i0 = first; i0 < end; i0 += QT) {
+        int u = ALONE ? wid : 0, cur = 0;
+        if (u < n_all) fetch(u, 0);
+        for (; u < n_all; u += step) {
+            dma_wait();
+            if (ALONE)
+                wave_fence();
+            else
+                __builtin_amdgcn_s_barrier();
+            const uint32_t qt = lds_addr(tiles[set][cur][0]);
+            const uint32_t gt = lds_addr(tiles[set][cur][1]);
+            const uint32_t row_l = lds_addr(row_t[set][cur][0]), row_d = lds_addr(row_t[set][cur][1]);
+            if (S::kBufs == 2) {
+                cur ^= 1;
+                if (u + step < n_all) fetch(u + step, cur);
+            }
+            const int i00 = first + (BIAS ? u : u % n_tiles) * QT;
+#pragma unroll
+            for (int qb = 0; qb < QT / 32; ++qb) {
+                const int i0 = i00 + 32 * qb;
+                f32x16 s, dp;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < NK; ++kk)
+                    s = E::mfma(L::frag_rows(qt, 32 * qb, kk, lane), kf[kk], s);
+#pragma unroll
+                for (int kk = 0; kk < NK; ++kk)
+                    dp = E::mfma(L::frag_rows(gt, 32 * qb, kk, lane), vf[kk], dp);
+                float rl[16], rd[16];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f32x4 x = lds_read<f32x4>(row_l + 4 * (32 * qb + 8 * q + 4 * h));
+                    const f32x4 y = lds_read<f32x4>(row_d + 4 * (32 * qb + 8 * q + 4 * h));
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        rl[4 * q + r] = x[r];
+                        rd[4 * q + r] = y[r];
+                    }
+                }
+                bool lo_far = false, hi_far = false;
+                if (BIAS) {
+                    const int lo = j0 - i0 - 31 - off, hi = j0 + 31 - i0 - off;
+                    lo_far = hi <= -a.r0;
+                    hi_far = !lo_far && lo >= a.rp;
+                    if (lo_far || hi_far) {
+                        const float ca = line[lo_far ? 0 : n_line - 1];
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) rl[r] += ca;
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            rl[r] += line[line_index(a, j - (i0 + 8 * (r >> 2) + 4 * h + (r & 3)) - off)];
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[r] = ex2(fmaf(s[r], a.c, rl[r]));
+                if (a.causal && j0 + 31 - off > i0) {
+                    // queries from j - off on see key j
+                    const uint32_t vis = ~bits_upto(j - off - i0 - 1) >> (4 * h);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s[r] = flag(vis, r) ? s[r] : 0.f;
+                }
+                f32x16 ds;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    ds[r] = s[r] * (dp[r] - rd[r]);
+                    if (kLiftP<OP> != 1.f) s[r] *= kLiftP<OP>;
+                }
+                if (BIAS && a.gbias) {
+                    if (lo_far || hi_far) {
+                        float x = 0.f;
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) x += ds[r];
+                        x = key_ok ? x : 0.f;
+                        if (lo_far) sum_lo += x;
+                        else sum_hi += x;
+                    } else {
+                        const int k = lane & 31;
+                        wave_fence();
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            dg.set(k * kDiag + k - (8 * (r >> 2) + 4 * h + (r & 3)) + 31,
+                                   key_ok ? ds[r] : 0.f);
+                        wave_fence();
+                        float x = 0.f;
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) x += dg[y * kDiag + lane];
+                        const int r = j0 - i0 - 31 - off + lane;  // lane 63: no pair, x = 0
+                        if (r <= -a.r0) sum_lo += x;
+                        else if (r >= a.rp) sum_hi += x;
+                        else gline.set(r + a.r0, gline[r + a.r0] + x);
+                        wave_fence();
+                    }
+                }
+                dss.apply(ds, dk);
+#pragma unroll
+                for (int rc = 0; rc < 2; ++rc) {
+                    const typename E::Frag pf = L::pack(s, rc), df = L::pack(ds, rc);
+#pragma unroll
+                    for (int cb = 0; cb < ND; ++cb) {
+                        dvv[cb] = E::mfma(L::frag_cols(gt, 32 * qb + 16 * rc, cb, lane), pf, dvv[cb]);
+                        dk[cb] = E::mfma(L::frag_cols(qt, 32 * qb + 16 * rc, cb, lane), df, dk[cb]);
+                    }
+                }
+            }
+            if (S::kBufs == 1 && u + step < n_all) {
+                dma_wait();
+                wave_fence();
+                fetch(u + step, 0);
+            }
+        }
+        if (BIAS && a.gbias) {
+            sum_lo = wave_sum(sum_lo);
+            sum_hi = wave_sum(sum_hi);
+            if (lane == 0) {
+                gline.set(0, gline[0] + sum_lo);
+                gline.set(n_line - 1, gline[n_line - 1] + sum_hi);
+            }
             __syncthreads();
-            qs.store(qt, t);
-            gs.store(gt, t);
-            if (t < QT) {
-                // a row without keys gives no weight: 2^(s - inf) = 0
-                row_l[t] = nl == -INFINITY ? -INFINITY : -nl * kLog2e;
-                row_d[t] = nd;
-            }
-            __syncthreads();
-            if (i0 + QT < end) fetch(i0 + QT);
-
-            f32x16 s, dp;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < NK; ++kk) s = E::mfma(L::frag_rows(qt, 0, kk, lane), kf[kk], s);
-#pragma unroll
-            for (int kk = 0; kk < NK; ++kk) dp = E::mfma(L::frag_rows(gt, 0, kk, lane), vf[kk], dp);
-            float rl[16], rd[16];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const f32x4 x = *(const f32x4*)&row_l[8 * q + 4 * h];
-                const f32x4 y = *(const f32x4*)&row_d[8 * q + 4 * h];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    rl[4 * q + r] = x[r];
-                    rd[4 * q + r] = y[r];
-                }
-            }
-            if (BIAS) {
-                const int lo = j0 - i0 - (QT - 1) - off, hi = j0 + 31 - i0 - off;
-                if (hi <= -a.r0) {
-                    const float ca = line[0];
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) rl[r] += ca;
-                } else if (lo >= a.rp) {
-                    const float ca = line[a.r0 + a.rp];
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) rl[r] += ca;
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        rl[r] += line[line_index(a, j - (i0 + 8 * (r >> 2) + 4 * h + (r & 3)) - off)];
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < 16; ++r) s[r] = ex2(fmaf(s[r], a.c, rl[r]));
-            if (a.causal) {
-                // queries from j - off on see key j
-                const uint32_t vis = ~bits_upto(j - off - i0 - 1) >> (4 * h);
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] = flag(vis, r) ? s[r] : 0.f;
-            }
-            f32x16 ds;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                ds[r] = s[r] * (dp[r] - rd[r]);
-                s[r] *= kLiftP<OP>;
-            }
-            dss.apply(ds, dk);
-#pragma unroll
-            for (int rc = 0; rc < 2; ++rc) {
-                const typename E::Frag pf = L::pack(s, rc), df = L::pack(ds, rc);
-#pragma unroll
-                for (int cb = 0; cb < ND; ++cb) {
-                    dvv[cb] = E::mfma(L::frag_cols(gt, 16 * rc, cb, lane), pf, dvv[cb]);
-                    dk[cb] = E::mfma(L::frag_cols(qt, 16 * rc, cb, lane), df, dk[cb]);
-                }
-            }
+            const int64_t parts = (int64_t)a.B * a.line_blocks;
+            float* part = a.line_part + ((int64_t)(kvh * a.G + g0) * parts +
+                                         (int64_t)b * a.line_blocks + split * nkb + kb) * n_line;
+            for (int x = t; x < n_line; x += 256)
+                part[x] = (line[n_line + x] + line[2 * n_line + x]) +
+                          (line[3 * n_line + x] + line[4 * n_line + x]);
         }
     }
 
-    if (j >= a.m) return;
     const float fk = a.scale * dss.undo(), fv = 1.f / kLiftP<OP>;
+#pragma unroll
+    for (int cb = 0; cb < ND; ++cb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            dk[cb][r] *= fk;
+            dvv[cb][r] *= fv;
+        }
+    if (ALONE) {
+        const LdsFloats buf{lds_addr(tiles)};
+        join_waves<DP, ND>(dk, buf, wid, lane);
+        join_waves<DP, ND>(dvv, buf, wid, lane);
+        if (wid > 0) return;
+    }
+    if (j >= a.m) return;
     if (a.q_split > 1) {
         const int64_t row = ((int64_t)b * a.K + kvh) * a.m + j;
         const int64_t rows = (int64_t)a.B * a.K * a.m;
@@ -268,8 +413,8 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_kv_kernel(const AttnArgs a) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const int x = 32 * cb + 8 * (r >> 2) + 4 * h + (r & 3);
-                if (x < a.d) pk[x] = key_ok ? dk[cb][r] * fk : 0.f;
-                if (x < a.dv) pv[x] = key_ok ? dvv[cb][r] * fv : 0.f;
+                if (x < a.d) pk[x] = key_ok ? dk[cb][r] : 0.f;
+                if (x < a.dv) pv[x] = key_ok ? dvv[cb][r] : 0.f;
             }
         return;
     }
@@ -282,8 +427,8 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_kv_kernel(const AttnArgs a) {
             float y[4], z[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                y[r] = key_ok ? dk[cb][4 * q + r] * fk : 0.f;
-                z[r] = key_ok ? dvv[cb][4 * q + r] * fv : 0.f;
+                y[r] = key_ok ? dk[cb][4 * q + r] : 0.f;
+                z[r] = key_ok ? dvv[cb][4 * q + r] : 0.f;
             }
             if (a.gk.p) store4<OP>(ok, 32 * cb + 8 * q + 4 * h, a.d, a.gk.vec, y[0], y[1], y[2], y[3]);
             if (a.gv.p) store4<OP>(ov, 32 * cb + 8 * q + 4 * h, a.dv, a.gv.vec, z[0], z[1], z[2], z[3]);
@@ -319,35 +464,32 @@ __global__ __launch_bounds__(256) void attn_kv_merge_kernel(const AttnArgs a) {
     }
 }
 
-// ---- dQ, dT ---------------------------------------------------------------
-// The mirror image: 128 query rows of a head, 32 a wave, keys in tiles, keys
-// in the rows of the scores.  Here a masked key does enter sums over keys, so
-// its weight is set to zero.
+// ---- dQ -------------------------------------------------------------------
+// The mirror image: query rows of a head, keys in tiles, keys in the rows of
+// the scores.  Here a masked key does enter sums over keys, so its weight is
+// set to zero.
 //
-// Bias gradient: dS summed over the pairs of every relative position r, and
-// those sums over each bucket by attn_bias_sum_kernel.  A tile whose pairs all
-// lie beyond the last edge goes into one of two running sums of the lane.  In
-// a tile near the diagonal a wave writes each 32 x 32 block to its own LDS
-// with query x's row moved by x, so that a relative position is a column, and
-// 63 lanes sum a column each; positions between the last edges are added to
-// the wave's line in LDS (one lane a position), those beyond to the lane's
-// running sums.
-constexpr int kDiag = 64;
-template <int OP, int DP, bool BIAS>
-__global__ __launch_bounds__(256, 1) void attn_bwd_q_kernel(const AttnArgs a) {
+// The stored o is rounded, and with it delta: enough for a gradient that is
+// rounded as well, but not for the bias's, an fp32 sum over many rows.  Since
+// sum_j P_ij = 1, sum_j dS_ij is what delta lacks of sum_j P_ij do_i.v_j (and
+// dL_i); the pass adds it, and the pass over the queries after it uses the
+// result.
+template <int OP, int DP, bool BIAS, bool ALONE>
+__global__ __launch_bounds__(256, (Tile<OP, DP>::kRow <= 128 ? 2 : 1)) void attn_bwd_q_kernel(const AttnArgs a) {
     using E = El<OP>;
     using T = typename E::T;
     using L = Tile<OP, DP>;
-    constexpr int KT = kBwdTile<OP, DP>, NB = KT / 32, ND = DP / 32, NK = DP / 16;
-    constexpr int kLine = 2 * kAttnMaxEdge + 1;
-    __shared__ __attribute__((aligned(256))) char kt[KT * L::kRow];
-    __shared__ __attribute__((aligned(256))) char vt[KT * L::kRow];
-    __shared__ float line[BIAS ? kLine : 1];
-    __shared__ float diag[BIAS ? 4 : 1][BIAS ? 32 * kDiag : 1];
-    __shared__ float gline[BIAS ? 4 : 1][BIAS ? kLine : 1];
+    using S = BwdShape<OP, DP, ALONE>;
+    constexpr int KT = S::kTile, NB = KT / 32, ND = DP / 32, NK = DP / 16;
+    using Load = Loader<OP, DP, KT, ALONE ? 64 : 256>;
+    __shared__ __attribute__((aligned(256))) char tiles[S::kSets][S::kBufs][2][KT * L::kRow];
+    __shared__ float line_mem[BIAS ? 2 * kAttnMaxEdge + 1 : 1];
+    const LdsFloats line{lds_addr(line_mem)};
+    __shared__ float wsum[4][32];
 
     const int t = threadIdx.x, lane = t & 63, wid = t >> 6, h = lane >> 5;
-    const int nqb = (a.n + kAttnRows - 1) / kAttnRows;
+    const int set = ALONE ? wid : 0;
+    const int nqb = (a.n + S::kRows - 1) / S::kRows;
     int w = xcd_item(blockIdx.x, gridDim.x);
     const int qb = w % nqb;
     w /= nqb;
@@ -355,52 +497,57 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_q_kernel(const AttnArgs a) {
     const int n_line = a.r0 + a.rp + 1;
 
     const int off = attn_offset(a, b);
-    const int i0 = qb * kAttnRows + wid * 32, i = i0 + (lane & 31);
+    const int i0 = qb * S::kRows + (ALONE ? 0 : wid * 32), i = i0 + (lane & 31);
     const bool row_ok = i < attn_q_len(a, b);
     int len = attn_kv_len(a, b);
-    if (a.causal) len = min(len, max(0, min(qb * kAttnRows + kAttnRows, a.n) + off));
+    if (a.causal) len = min(len, max(0, min((qb + 1) * S::kRows, a.n) + off));
 
     if (BIAS) {
         load_line(a, head, line, t, 256);
-        if (a.gbias) {
-            for (int x = lane; x < n_line; x += 64) gline[wid][x] = 0.f;
-            for (int x = lane; x < 32 * kDiag; x += 64) diag[wid][x] = 0.f;
-        }
+        __syncthreads();
     }
     typename E::Frag qf[NK], gf[NK];
     load_row_frags<OP, DP>((const T*)a.q.p + b * a.q.sb + (int64_t)i * a.q.sr + head * a.q.sh,
                            row_ok, a.d, a.q.vec, lane, qf);
     load_row_frags<OP, DP>((const T*)a.go.p + b * a.go.sb + (int64_t)i * a.go.sr + head * a.go.sh,
                            row_ok, a.dv, a.go.vec, lane, gf);
-    const int64_t lrow = ((int64_t)b * a.H + head) * a.n;
-    const float lse = row_ok ? a.lse[lrow + i] : -INFINITY;
-    const float rl = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
-    const float rd = row_ok ? a.delta[lrow + i] : 0.f;
+    const int64_t lrow = ((int64_t)b * a.H + head) * a.n_pad + i;
+    const bool in = i < a.n;
+    const float rl = in ? a.nl2[lrow] : -INFINITY;
+    const float rd = in ? a.delta[lrow] : 0.f;
     f32x16 acc[ND];
 #pragma unroll
     for (int x = 0; x < ND; ++x)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[x][r] = 0.f;
     DsScale<OP, ND> dss;
-    float sum_lo = 0.f, sum_hi = 0.f;
+    float rest = 0.f;  // sum of dS
 
     const T* kbase = (const T*)a.k.p + b * a.k.sb + kvh * a.k.sh;
     const T* vbase = (const T*)a.v.p + b * a.v.sb + kvh * a.v.sh;
-    Stage<OP, DP, KT, 256> ks, vs;
     uint64_t next = 0;
-    auto fetch = [&](int j0) {
+    const auto fetch = [&](int j0, int buf) {
+        const int tt = ALONE ? lane : t;
         next = seen_keys(a, b, len, j0, lane);
-        ks.load(kbase + (int64_t)j0 * a.k.sr, a.k.sr, next, a.d, a.k.vec, t);
-        vs.load(vbase + (int64_t)j0 * a.v.sr, a.v.sr, next, a.dv, a.v.vec, t);
+        Load::fill(lds_addr(tiles[set][buf][0]), kbase + (int64_t)j0 * a.k.sr, a.k.sr, next, a.d, a.k.vec, tt);
+        Load::fill(lds_addr(tiles[set][buf][1]), vbase + (int64_t)j0 * a.v.sr, a.v.sr, next, a.dv, a.v.vec, tt);
     };
-    if (len > 0) fetch(0);
-    for (int j0 = 0; j0 < len; j0 += KT) {
+    const int step = ALONE ? 4 * KT : KT;
+    int j0 = ALONE ? wid * KT : 0, cur = 0;
+    if (j0 < len) fetch(j0, 0);
+    for (; j0 < len; j0 += step) {
         const uint64_t seen = next;
-        __syncthreads();
-        ks.store(kt, t);
-        vs.store(vt, t);
-        __syncthreads();
-        if (j0 + KT < len) fetch(j0 + KT);
+        dma_wait();
+        if (ALONE)
+            wave_fence();
+        else
+            __builtin_amdgcn_s_barrier();
+        const uint32_t kt = lds_addr(tiles[set][cur][0]);
+        const uint32_t vt = lds_addr(tiles[set][cur][1]);
+        if (S::kBufs == 2) {
+            cur ^= 1;
+            if (j0 + step < len) fetch(j0 + step, cur);
+        }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             const int jb = j0 + 32 * nb;
@@ -438,31 +585,10 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_q_kernel(const AttnArgs a) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) ds[r] = flag(vis, r) ? ds[r] : 0.f;
             }
-            if (BIAS && a.gbias) {
-                if (lo_far || hi_far) {
-                    float x = 0.f;
+            float x = 0.f;
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) x += ds[r];
-                    if (lo_far) sum_lo += x;
-                    else sum_hi += x;
-                } else {
-                    float* dg = diag[wid];
-                    const int q = lane & 31;
-                    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        dg[q * kDiag + 8 * (r >> 2) + 4 * h + (r & 3) - q + 31] = ds[r];
-                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                    float x = 0.f;
-#pragma unroll
-                    for (int y = 0; y < 32; ++y) x += dg[y * kDiag + lane];
-                    const int r = jb - i0 - 31 - off + lane;  // lane 63: no pair, x = 0
-                    if (r <= -a.r0) sum_lo += x;
-                    else if (r >= a.rp) sum_hi += x;
-                    else gline[wid][r + a.r0] += x;
-                    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-                }
-            }
+            for (int r = 0; r < 16; ++r) x += ds[r];
+            rest += x;
             dss.apply(ds, acc);
 #pragma unroll
             for (int rc = 0; rc < 2; ++rc) {
@@ -472,33 +598,37 @@ __global__ __launch_bounds__(256, 1) void attn_bwd_q_kernel(const AttnArgs a) {
                     acc[cb] = E::mfma(L::frag_cols(kt, 32 * nb + 16 * rc, cb, lane), df, acc[cb]);
             }
         }
+        if (S::kBufs == 1 && j0 + step < len) {
+            dma_wait();
+            wave_fence();
+            fetch(j0 + step, 0);
+        }
     }
 
-    if (BIAS && a.gbias) {
-        sum_lo = wave_sum(sum_lo);
-        sum_hi = wave_sum(sum_hi);
-        if (lane == 0) {
-            // both ends are one bucket each; with no edges they are one entry
-            gline[wid][0] += sum_lo;
-            gline[wid][n_line - 1] += sum_hi;
-        }
-        __syncthreads();
-        float* part = a.line_part + ((int64_t)head * a.B * nqb + (int64_t)b * nqb + qb) * n_line;
-        for (int x = t; x < n_line; x += 256)
-            part[x] = (gline[0][x] + gline[1][x]) + (gline[2][x] + gline[3][x]);
-    }
-    if (i >= a.n || !a.gq.p) return;
+    rest = half_sum(rest);
     const float f = a.scale * dss.undo();
+#pragma unroll
+    for (int cb = 0; cb < ND; ++cb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[cb][r] *= f;
+    if (ALONE) {
+        if (h == 0) wsum[wid][lane] = rest;
+        join_waves<DP, ND>(acc, LdsFloats{lds_addr(tiles)}, wid, lane);
+        if (wid > 0) return;
+        rest = (wsum[0][lane & 31] + wsum[1][lane & 31]) + (wsum[2][lane & 31] + wsum[3][lane & 31]);
+    }
+    if (!in) return;
+    if (h == 0 && rl != -INFINITY)
+        a.delta[lrow] = rd + rest - (a.glse ? a.glse[((int64_t)b * a.H + head) * a.n + i] : 0.f);
+    if (!a.gq.p) return;
     T* o = (T*)a.gq.p + b * a.gq.sb + (int64_t)i * a.gq.sr + head * a.gq.sh;
 #pragma unroll
     for (int cb = 0; cb < ND; ++cb)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float y[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) y[r] = row_ok ? acc[cb][4 * q + r] * f : 0.f;
-            store4<OP>(o, 32 * cb + 8 * q + 4 * h, a.d, a.gq.vec, y[0], y[1], y[2], y[3]);
-        }
+        for (int q = 0; q < 4; ++q)
+            store4<OP>(o, 32 * cb + 8 * q + 4 * h, a.d, a.gq.vec, row_ok ? acc[cb][4 * q] : 0.f,
+                       row_ok ? acc[cb][4 * q + 1] : 0.f, row_ok ? acc[cb][4 * q + 2] : 0.f,
+                       row_ok ? acc[cb][4 * q + 3] : 0.f);
 }
 
 // dT[bucket, head]: the bucket's positions of every part's line, in 64 bits
@@ -507,7 +637,7 @@ __global__ __launch_bounds__(256) void attn_bias_sum_kernel(const AttnArgs a) {
     __shared__ double red[256];
     const int bucket = blockIdx.x, head = blockIdx.y, t = threadIdx.x;
     const int n_line = a.r0 + a.rp + 1;
-    const int parts = a.B * ((a.n + kAttnRows - 1) / kAttnRows);
+    const int parts = a.B * a.line_blocks;
     // the line positions of this bucket: distances [from, to), on one side
     const int E1 = a.n_edges + 1;
     const bool after = a.two_sided && bucket >= E1;
@@ -538,24 +668,35 @@ __global__ __launch_bounds__(256) void attn_bias_sum_kernel(const AttnArgs a) {
     if (t == 0) a.gbias[(int64_t)bucket * a.H + head] = (float)red[0];
 }
 
-template <int OP, int DP>
-hipError_t bwd_kv(const AttnArgs& a, hipStream_t s) {
-    const int64_t g = (int64_t)a.B * a.K * a.q_split * ((a.m + kAttnRows - 1) / kAttnRows);
-    if (a.bias)
-        attn_bwd_kv_kernel<OP, DP, true><<<(unsigned)g, 256, 0, s>>>(a);
-    else
-        attn_bwd_kv_kernel<OP, DP, false><<<(unsigned)g, 256, 0, s>>>(a);
+template <int OP, int DP, bool BIAS, bool ALONE>
+hipError_t bwd_kv_as(const AttnArgs& a, hipStream_t s) {
+    constexpr int rows = BwdShape<OP, DP, ALONE>::kRows;
+    const int64_t g = (int64_t)a.B * a.K * a.q_split * ((a.m + rows - 1) / rows);
+    const size_t lds = BIAS ? (size_t)5 * (a.r0 + a.rp + 1) * sizeof(float) : 0;
+    attn_bwd_kv_kernel<OP, DP, BIAS, ALONE><<<(unsigned)g, 256, lds, s>>>(a);
     return hipGetLastError();
 }
+template <int OP, int DP>
+hipError_t bwd_kv(const AttnArgs& a, hipStream_t s) {
+    if constexpr (Tile<OP, DP>::kRow <= 256)
+        if (a.alone_k)
+            return a.bias ? bwd_kv_as<OP, DP, true, true>(a, s) : bwd_kv_as<OP, DP, false, true>(a, s);
+    return a.bias ? bwd_kv_as<OP, DP, true, false>(a, s) : bwd_kv_as<OP, DP, false, false>(a, s);
+}
 
+template <int OP, int DP, bool BIAS, bool ALONE>
+hipError_t bwd_q_as(const AttnArgs& a, hipStream_t s) {
+    constexpr int rows = BwdShape<OP, DP, ALONE>::kRows;
+    const int64_t g = (int64_t)a.B * a.H * ((a.n + rows - 1) / rows);
+    attn_bwd_q_kernel<OP, DP, BIAS, ALONE><<<(unsigned)g, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
 template <int OP, int DP>
 hipError_t bwd_q(const AttnArgs& a, hipStream_t s) {
-    const int64_t g = (int64_t)a.B * a.H * ((a.n + kAttnRows - 1) / kAttnRows);
-    if (a.bias)
-        attn_bwd_q_kernel<OP, DP, true><<<(unsigned)g, 256, 0, s>>>(a);
-    else
-        attn_bwd_q_kernel<OP, DP, false><<<(unsigned)g, 256, 0, s>>>(a);
-    return hipGetLastError();
+    if constexpr (Tile<OP, DP>::kRow <= 256)
+        if (a.alone_q)
+            return a.bias ? bwd_q_as<OP, DP, true, true>(a, s) : bwd_q_as<OP, DP, false, true>(a, s);
+    return a.bias ? bwd_q_as<OP, DP, true, false>(a, s) : bwd_q_as<OP, DP, false, false>(a, s);
 }
 
 }  // namespace
@@ -579,7 +720,7 @@ hipError_t launch_attn_bwd_kv(const AttnArgs& a, hipStream_t s) { FS_ATTN_DISPAT
 hipError_t launch_attn_bwd_q(const AttnArgs& a, hipStream_t s) { FS_ATTN_DISPATCH(bwd_q) }
 
 hipError_t launch_attn_delta(const AttnArgs& a, hipStream_t s) {
-    const int64_t rows = (int64_t)a.B * a.n * a.H;
+    const int64_t rows = (int64_t)a.B * a.n_pad * a.H;
     const unsigned g = (unsigned)((rows + 15) / 16);
     if (a.op == OP_BF16)
         attn_delta_kernel<OP_BF16><<<g, 256, 0, s>>>(a);

@@ -89,9 +89,10 @@ void attn_fwd_kernel(const AttnArgs a) {
     using T = typename E::T;
     using L = Tile<OP, DP>;
     constexpr int KT = kTileKeys<OP, DP>, NB = KT / 32, ND = DP / 32, NK = DP / 16;
-    __shared__ __attribute__((aligned(256))) char kt[KT * L::kRow];
-    __shared__ __attribute__((aligned(256))) char vt[KT * L::kRow];
-    __shared__ float line[BIAS ? 2 * kAttnMaxEdge + 1 : 1];
+    using Load = Loader<OP, DP, KT, 256>;
+    __shared__ __attribute__((aligned(256))) char tiles[2][2][KT * L::kRow];
+    __shared__ float line_mem[BIAS ? 2 * kAttnMaxEdge + 1 : 1];
+    const LdsFloats line{lds_addr(line_mem)};
 
     const int t = threadIdx.x, lane = t & 63, wid = t >> 6, h = lane >> 5;
     const int nqb = (a.n + kAttnRows - 1) / kAttnRows;
@@ -124,24 +125,22 @@ void attn_fwd_kernel(const AttnArgs a) {
 
     const T* kbase = (const T*)a.k.p + b * a.k.sb + kvh * a.k.sh;
     const T* vbase = (const T*)a.v.p + b * a.v.sb + kvh * a.v.sh;
-    Stage<OP, DP, KT, 256> ks, vs;
     uint64_t next = 0;
-    if (jb < je) {
-        next = seen_keys(a, b, je, jb, lane);
-        ks.load(kbase + (int64_t)jb * a.k.sr, a.k.sr, next, a.d, a.k.vec, t);
-        vs.load(vbase + (int64_t)jb * a.v.sr, a.v.sr, next, a.dv, a.v.vec, t);
-    }
-    for (int j0 = jb; j0 < je; j0 += KT) {
+    const auto fetch = [&](int j0, int buf) {
+        next = seen_keys(a, b, je, j0, lane);
+        Load::fill(lds_addr(tiles[buf][0]), kbase + (int64_t)j0 * a.k.sr, a.k.sr, next, a.d, a.k.vec, t);
+        Load::fill(lds_addr(tiles[buf][1]), vbase + (int64_t)j0 * a.v.sr, a.v.sr, next, a.dv, a.v.vec, t);
+    };
+    if (jb < je) fetch(jb, 0);
+    int cur = 0;
+    for (int j0 = jb; j0 < je; j0 += KT, cur ^= 1) {
         const uint64_t seen = next;
-        __syncthreads();
-        ks.store(kt, t);
-        vs.store(vt, t);
-        __syncthreads();
-        if (j0 + KT < je) {
-            next = seen_keys(a, b, je, j0 + KT, lane);
-            ks.load(kbase + (int64_t)(j0 + KT) * a.k.sr, a.k.sr, next, a.d, a.k.vec, t);
-            vs.load(vbase + (int64_t)(j0 + KT) * a.v.sr, a.v.sr, next, a.dv, a.v.vec, t);
-        }
+        // this tile has landed, and no wave reads the other buffer any more
+        dma_wait();
+        __builtin_amdgcn_s_barrier();
+        if (j0 + KT < je) fetch(j0 + KT, cur ^ 1);
+        const uint32_t kt = lds_addr(tiles[cur][0]);
+        const uint32_t vt = lds_addr(tiles[cur][1]);
         f32x16 s[NB];
         uint32_t vis[NB];
         bool all = true;
@@ -212,14 +211,16 @@ void attn_fwd_kernel(const AttnArgs a) {
     if (a.n_split > 1) {
         const int64_t row = (int64_t)(b * a.H + head) * a.n + i;
         const int64_t rows = (int64_t)a.B * a.H * a.n;
-        if (h == 0) a.part_ml[split * rows + row] = make_float2(st.sum > 0.f || st.sum != st.sum ? st.ref : -INFINITY, st.sum);
-        float* po = a.part_o + (split * rows + row) * a.dv;
+        if (h == 0) a.part_ml[split * rows + row] = make_float2(st.sum == 0.f ? -INFINITY : st.ref, st.sum);
+        float* po = a.part_o + (split * rows + row) * a.dv_pad;
 #pragma unroll
         for (int cb = 0; cb < ND; ++cb)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int x = 32 * cb + 8 * (r >> 2) + 4 * h + (r & 3);
-                if (x < a.dv) po[x] = row_ok ? acc[cb][r] : 0.f;
+            for (int q = 0; q < 4; ++q) {
+                const int x = 32 * cb + 8 * q + 4 * h;
+                if (x < a.dv)
+                    *(f32x4*)(po + x) = f32x4{acc[cb][4 * q], acc[cb][4 * q + 1], acc[cb][4 * q + 2],
+                                              acc[cb][4 * q + 3]};
             }
         return;
     }
@@ -247,17 +248,25 @@ void attn_fwd_kernel(const AttnArgs a) {
 // wave's own part of LDS with the next tile's loads in flight, without
 // barriers, and their four results are joined at the end.  Long key ranges
 // are split over workgroups and joined by a second kernel.
+template <int OP, int DP>
+struct RowsShape {
+    static constexpr int kRow = Tile<OP, DP>::kRow;
+    static constexpr int kWaves = kRow <= 128 ? 8 : 4;
+    static constexpr int kBufs = kRow <= 256 ? 2 : 1;
+};
 template <int OP, int DP, bool BIAS>
-__global__ __launch_bounds__(256, DP * sizeof(typename El<OP>::T) <= 256 ? 2 : 1)
+__global__ __launch_bounds__((64 * RowsShape<OP, DP>::kWaves), (RowsShape<OP, DP>::kWaves / 4))
 void attn_rows_kernel(const AttnArgs a) {
     using E = El<OP>;
     using T = typename E::T;
     using L = Tile<OP, DP>;
     constexpr int KT = 32, ND = DP / 32, NK = DP / 16;
-    __shared__ __attribute__((aligned(256))) char tiles[4][2][KT * L::kRow];
-    static_assert(sizeof(tiles) >= 4 * 32 * DP * 4, "the four results fit the tiles' memory");
+    constexpr int NW = RowsShape<OP, DP>::kWaves, NB = RowsShape<OP, DP>::kBufs;
+    using Load = Loader<OP, DP, KT, 64>;
+    __shared__ __attribute__((aligned(256))) char tiles[NW][NB][2][KT * L::kRow];
+    static_assert(sizeof(tiles) >= NW * 32 * DP * 4, "the waves' results fit the tiles' memory");
     __shared__ short bucket[BIAS ? 2 * kAttnMaxEdge + 1 : 1];
-    __shared__ float wref[4][32], wsum[4][32];
+    __shared__ float wref[NW][32], wsum[NW][32];
 
     const int t = threadIdx.x, lane = t & 63, wid = t >> 6, h = lane >> 5;
     const int rows = a.G * a.n;
@@ -281,7 +290,7 @@ void attn_rows_kernel(const AttnArgs a) {
 
     float bias_lo = 0.f, bias_hi = 0.f;
     if (BIAS) {
-        for (int x = t; x < a.r0 + a.rp + 1; x += 256) bucket[x] = (short)bucket_of(a, x - a.r0);
+        for (int x = t; x < a.r0 + a.rp + 1; x += 64 * NW) bucket[x] = (short)bucket_of(a, x - a.r0);
         __syncthreads();
         bias_lo = bias2(a.bias[(int64_t)bucket[0] * a.H + head]);
         bias_hi = bias2(a.bias[(int64_t)bucket[a.r0 + a.rp] * a.H + head]);
@@ -299,28 +308,25 @@ void attn_rows_kernel(const AttnArgs a) {
 
     const T* kbase = (const T*)a.k.p + b * a.k.sb + kvh * a.k.sh;
     const T* vbase = (const T*)a.v.p + b * a.v.sb + kvh * a.v.sh;
-    char* kt = tiles[wid][0];
-    char* vt = tiles[wid][1];
-    Stage<OP, DP, KT, 64> ks, vs;
-    const int j_first = jb + wid * KT;
     uint32_t next = 0;
-    if (j_first < je) {
-        next = (uint32_t)seen_keys(a, b, je, j_first, lane);
-        ks.load(kbase + (int64_t)j_first * a.k.sr, a.k.sr, next, a.d, a.k.vec, lane);
-        vs.load(vbase + (int64_t)j_first * a.v.sr, a.v.sr, next, a.dv, a.v.vec, lane);
-    }
-    for (int j0 = j_first; j0 < je; j0 += 4 * KT) {
+    const auto fetch = [&](int j0, int buf) {
+        next = (uint32_t)seen_keys(a, b, je, j0, lane);
+        Load::fill(lds_addr(tiles[wid][buf][0]), kbase + (int64_t)j0 * a.k.sr, a.k.sr, next, a.d, a.k.vec, lane);
+        Load::fill(lds_addr(tiles[wid][buf][1]), vbase + (int64_t)j0 * a.v.sr, a.v.sr, next, a.dv, a.v.vec, lane);
+    };
+    const int j_first = jb + wid * KT;
+    if (j_first < je) fetch(j_first, 0);
+    int cur = 0;
+    for (int j0 = j_first; j0 < je; j0 += NW * KT) {
         const uint32_t seen = next;
-        // the wave's own LDS: its reads of the last tile are in registers by now
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        ks.store(kt, lane);
-        vs.store(vt, lane);
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        if (j0 + 4 * KT < je) {
-            const int jn = j0 + 4 * KT;
-            next = (uint32_t)seen_keys(a, b, je, jn, lane);
-            ks.load(kbase + (int64_t)jn * a.k.sr, a.k.sr, next, a.d, a.k.vec, lane);
-            vs.load(vbase + (int64_t)jn * a.v.sr, a.v.sr, next, a.dv, a.v.vec, lane);
+        // the wave's own buffers: no barrier
+        dma_wait();
+        wave_fence();
+        const uint32_t kt = lds_addr(tiles[wid][cur][0]);
+        const uint32_t vt = lds_addr(tiles[wid][cur][1]);
+        if (NB == 2) {
+            cur ^= 1;
+            if (j0 + NW * KT < je) fetch(j0 + NW * KT, cur);
         }
         uint32_t vis = seen;
         if (a.causal) vis &= bits_upto(i + off - j0);
@@ -364,17 +370,22 @@ void attn_rows_kernel(const AttnArgs a) {
             for (int cb = 0; cb < ND; ++cb)
                 acc[cb] = E::mfma(L::frag_cols(vt, 16 * rc, cb, lane), pf, acc[cb]);
         }
+        if (NB == 1 && j0 + NW * KT < je) {
+            dma_wait();
+            wave_fence();
+            fetch(j0 + NW * KT, 0);
+        }
     }
 
-    // join the four waves' results: [wave][element][row] in the tiles' memory
+    // join the waves' results: [wave][element][row] in the tiles' memory
     st.sum = half_sum(st.sum);
     __syncthreads();
-    float* buf = (float*)&tiles[0][0][0];
+    const LdsFloats buf{lds_addr(tiles)};
 #pragma unroll
     for (int cb = 0; cb < ND; ++cb)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-            buf[(wid * DP + 32 * cb + 8 * (r >> 2) + 4 * h + (r & 3)) * 32 + (lane & 31)] = acc[cb][r];
+            buf.set((wid * DP + 32 * cb + 8 * (r >> 2) + 4 * h + (r & 3)) * 32 + (lane & 31), acc[cb][r]);
     if (h == 0) {
         wref[wid][lane] = st.ref;
         wsum[wid][lane] = st.sum;
@@ -387,10 +398,10 @@ void attn_rows_kernel(const AttnArgs a) {
     const bool ok = oi < attn_q_len(a, b);
     float ref = -INFINITY;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) ref = fmaxf(ref, wref[x][q]);
-    float f[4], sum = 0.f;
+    for (int x = 0; x < NW; ++x) ref = fmaxf(ref, wref[x][q]);
+    float f[NW], sum = 0.f;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
+    for (int x = 0; x < NW; ++x) {
         f[x] = wref[x][q] == -INFINITY ? 0.f : ex2(wref[x][q] - ref);
         sum += wref[x][q] == -INFINITY ? 0.f : wsum[x][q] * f[x];
     }
@@ -401,23 +412,21 @@ void attn_rows_kernel(const AttnArgs a) {
     const int64_t prow = (int64_t)(b * a.H + ohead) * a.n + oi;
     const int64_t prows = (int64_t)a.B * a.H * a.n;
     T* o = (T*)a.o.p + b * a.o.sb + (int64_t)oi * a.o.sr + ohead * a.o.sh;
-    float* po = a.part_o + (split * prows + prow) * a.dv;
-    for (int x = (t >> 5) * 4; x < a.dv; x += 32) {
+    float* po = a.part_o + (split * prows + prow) * a.dv_pad;
+    for (int x = (t >> 5) * 4; x < a.dv; x += 8 * NW) {
         float y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             y[e] = 0.f;
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
+            for (int v = 0; v < NW; ++v)
                 if (wref[v][q] != -INFINITY) y[e] = fmaf(buf[(v * DP + x + e) * 32 + q], f[v], y[e]);
             y[e] = some ? y[e] * inv : 0.f;
         }
         if (last) {
             store4<OP>(o, x, a.dv, a.o.vec, y[0], y[1], y[2], y[3]);
         } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (x + e < a.dv) po[x + e] = y[e];
+            *(f32x4*)(po + x) = f32x4{y[0], y[1], y[2], y[3]};
         }
     }
     if (t < 32) {
@@ -428,35 +437,55 @@ void attn_rows_kernel(const AttnArgs a) {
     }
 }
 
-// Joins the key ranges' results of one row (32 lanes a row, a fixed order).
+// Joins the key ranges' results, in a fixed order: 32 lanes a row, four
+// elements a lane at a time.
 template <int OP>
 __global__ __launch_bounds__(256) void attn_merge_kernel(const AttnArgs a) {
     using T = typename El<OP>::T;
+    __shared__ float weight[8][kAttnMaxSplit];
     const int64_t rows = (int64_t)a.B * a.H * a.n;
-    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
+    const int grp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * 8 + grp;
     if (row >= rows) return;
+    // lane s, s + 32: the ranges' references and sums
+    float2 ml[kAttnMaxSplit / 32];
     float ref = -INFINITY;
-    for (int s = 0; s < a.n_split; ++s) ref = fmaxf(ref, a.part_ml[s * rows + row].x);
-    float sum = 0.f;
-    for (int s = 0; s < a.n_split; ++s) {
-        const float2 ml = a.part_ml[s * rows + row];
-        if (ml.x != -INFINITY) sum = fmaf(ml.y, ex2(ml.x - ref), sum);
+#pragma unroll
+    for (int x = 0; x < kAttnMaxSplit / 32; ++x) {
+        const int s = lane + 32 * x;
+        ml[x] = s < a.n_split ? a.part_ml[s * rows + row] : make_float2(-INFINITY, 0.f);
+        ref = fmaxf(ref, ml[x].x);
     }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) ref = fmaxf(ref, __shfl_xor(ref, o, 64));
+    float sum = 0.f;
+#pragma unroll
+    for (int x = 0; x < kAttnMaxSplit / 32; ++x) {
+        const float f = ml[x].x == -INFINITY ? 0.f : ex2(ml[x].x - ref);
+        weight[grp][lane + 32 * x] = f;
+        sum = fmaf(ml[x].x == -INFINITY ? 0.f : ml[x].y, f, sum);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
+    wave_fence();
     const bool some = !(sum == 0.f);
     const float inv = some ? 1.f / sum : 0.f;
     const int i = (int)(row % a.n);
     const int64_t bh = row / a.n;
     const int head = (int)(bh % a.H), b = (int)(bh / a.H);
     T* o = (T*)a.o.p + b * a.o.sb + (int64_t)i * a.o.sr + head * a.o.sh;
-    for (int x = lane; x < a.dv; x += 32) {
-        float y = 0.f;
+    const float* po = a.part_o + row * a.dv_pad;
+    for (int x = 4 * lane; x < a.dv; x += 128) {
+        f32x4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
         for (int s = 0; s < a.n_split; ++s) {
-            const float2 ml = a.part_ml[s * rows + row];
-            if (ml.x != -INFINITY)
-                y = fmaf(a.part_o[(s * rows + row) * a.dv + x], ex2(ml.x - ref), y);
+            const f32x4 p = *(const f32x4*)(po + s * rows * a.dv_pad + x);
+            const float f = weight[grp][s];
+            // a range without keys holds nothing
+            y += f == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : p * f;
         }
-        o[x] = (T)(some ? y * inv : 0.f);
+        y = some ? y * inv : f32x4{0.f, 0.f, 0.f, 0.f};
+        store4<OP>(o, x, a.dv, a.o.vec, y[0], y[1], y[2], y[3]);
     }
     if (a.lse && lane == 0) a.lse[row] = some ? (ref + lg2(sum)) * kLn2 : -INFINITY;
 }
@@ -465,10 +494,11 @@ template <int OP, int DP>
 hipError_t fwd(const AttnArgs& a, bool few, hipStream_t s) {
     if (few) {
         const int64_t g = (int64_t)a.B * a.K * a.n_split * (((int64_t)a.G * a.n + 31) / 32);
+        constexpr int nt = 64 * RowsShape<OP, DP>::kWaves;
         if (a.bias)
-            attn_rows_kernel<OP, DP, true><<<(unsigned)g, 256, 0, s>>>(a);
+            attn_rows_kernel<OP, DP, true><<<(unsigned)g, nt, 0, s>>>(a);
         else
-            attn_rows_kernel<OP, DP, false><<<(unsigned)g, 256, 0, s>>>(a);
+            attn_rows_kernel<OP, DP, false><<<(unsigned)g, nt, 0, s>>>(a);
     } else {
         const int64_t g = (int64_t)a.B * a.H * a.n_split * ((a.n + kAttnRows - 1) / kAttnRows);
         if (a.bias)

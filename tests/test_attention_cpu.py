@@ -105,8 +105,8 @@ def test_workspace_sizes(lib):
     assert size(0) == 256 and size(0, n=0) == 256 and size(1, m=0) >= 256
     # a token against a long cache is split over workgroups, never n x m
     assert 256 < size(0, n=1, m=1 << 20) < 64 * 2 * 4 * (64 + 2) * 4 + 1024
-    # the backward pass keeps a number per query row, not per pair
-    assert size(1, n=4096, m=4096, batch=8, heads=16, kv_heads=16) < 8 * 16 * 4096 * 4 + 4096
+    # the backward pass keeps two numbers per query row, none per pair
+    assert size(1, n=4096, m=4096, batch=8, heads=16, kv_heads=16) < 2 * 8 * 16 * 4096 * 4 + 4096
 
 
 def test_bucket_edges(lib):
