@@ -53,6 +53,10 @@ struct El<OP_F32> {
     }
 };
 
+// The wave's number in its workgroup, known to the compiler to be one for all
+// its lanes.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
 // Shared memory by its LDS address (the low half of a shared object's generic
 // address): loads and stores of a known address space whatever the pointer
 // went through.
@@ -84,9 +88,11 @@ __device__ __forceinline__ float half_sum(float x) {
 }
 
 // A tile of rows of DP elements in LDS, in 16-byte chunks.  Chunk c of row r
-// is stored at chunk c ^ swz(r): eight successive rows read at one c (the row
-// operands) and four successive rows read at two neighbouring c (the column
-// operands) then fall on different banks.
+// is stored at chunk c ^ swz(r).  Sixteen successive rows read at one c (the
+// row operands, 256 bytes a clock) then fall on the 64 banks once each, and so
+// do four successive rows read at two neighbouring c (the column operands).
+// Measured with four waves, cycles a wave's load: 2.9 against 4.0 for a
+// swizzle over eight rows (2.7 for addresses in order).
 template <int OP, int DP>
 struct Tile {
     using E = El<OP>;
@@ -96,52 +102,86 @@ struct Tile {
     static constexpr int kCh = DP * (int)sizeof(T) / 16;  // chunks per row
     static constexpr int kRow = DP * (int)sizeof(T);      // bytes per row
 
+    // rows of 128 bytes: two rows lie side by side in the banks
     static __device__ __forceinline__ int swz(int r) {
-        return (((r & 3) << 1) | ((r >> 2) & 1)) & (kCh - 1);
+        return kRow == 128 ? (r & 2) | ((r >> 2) & 1) | ((r >> 1) & 4)
+                           : ((r & 3) << 1) | ((r >> 2) & 1) | (r & 8);
     }
     static __device__ __forceinline__ int at(int r, int c) { return r * kRow + ((c ^ swz(r)) << 4); }
 
+    // The swizzle moves chunks within groups of sixteen (eight), so an operand's
+    // address is one of a few values of the lane plus a constant, which the
+    // load instruction holds (the values are kept opaque, or the compiler would
+    // form each address anew).
+    static constexpr int kGroup = kRow == 128 ? 8 : 16;           // chunks of a group
+    static constexpr int kRowAddrs = kGroup / 2;                  // (kk, half) of a group
+    static constexpr int kColAddrs = sizeof(T) == 2 ? kGroup / 4 : 8;
+    struct Lanes {
+        uint32_t rows[kRowAddrs], cols[kColAddrs];
+        __device__ __forceinline__ Lanes(uint32_t t, int lane) {
+            const int r = lane & 31, h = lane >> 5, i = lane & 15;
+#pragma unroll
+            for (int x = 0; x < kRowAddrs; ++x) {
+                rows[x] = t + (sizeof(T) == 2 ? at(r, 2 * x + h) : at(r, 4 * (x >> 1) + 2 * h + (x & 1)));
+                asm volatile("" : "+v"(rows[x]));
+            }
+#pragma unroll
+            for (int x = 0; x < kColAddrs; ++x) {
+                cols[x] = t + (sizeof(T) == 2 ? at(4 * h + (i >> 2), x * 4 + ((lane >> 4) & 1) * 2 + ((i & 3) >> 1)) + (i & 1) * 8
+                                              : at(4 * h + (x & 3), (x >> 2) * 8 + (r >> 2)) + (r & 3) * 4);
+                asm volatile("" : "+v"(cols[x]));
+            }
+        }
+        // the same in another buffer
+        __device__ __forceinline__ Lanes(const Lanes& l, uint32_t offset) {
+#pragma unroll
+            for (int x = 0; x < kRowAddrs; ++x) rows[x] = l.rows[x] + offset;
+#pragma unroll
+            for (int x = 0; x < kColAddrs; ++x) cols[x] = l.cols[x] + offset;
+        }
+    };
+
     // Operand whose rows (or columns) are the tile's rows r0 + (lane & 31),
-    // contraction over elements 16 kk + 8 h + 0..7.
-    static __device__ __forceinline__ Frag frag_rows(uint32_t t, int r0, int kk, int lane) {
-        const int r = r0 + (lane & 31), h = lane >> 5;
+    // contraction over elements 16 kk + 8 h + 0..7.  o: the tile's offset plus
+    // r0 * kRow, r0 a multiple of 16.
+    static __device__ __forceinline__ Frag frag_rows(const Lanes& l, int o, int kk) {
         if constexpr (sizeof(T) == 2) {
-            return lds_read<Frag>(t + at(r, 2 * kk + h));
+            return lds_read<Frag>(l.rows[kk % kRowAddrs] + o + kk / kRowAddrs * (16 * kGroup));
         } else {
-            const f32x4 lo = lds_read<f32x4>(t + at(r, 4 * kk + 2 * h));
-            const f32x4 hi = lds_read<f32x4>(t + at(r, 4 * kk + 2 * h + 1));
+            const int c = 2 * kk % kRowAddrs;
+            o += 2 * kk / kRowAddrs * (16 * kGroup);
+            const f32x4 lo = lds_read<f32x4>(l.rows[c] + o);
+            const f32x4 hi = lds_read<f32x4>(l.rows[c + 1] + o);
             return Frag{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         }
     }
 
     // Operand whose rows are the tile's elements 32 cb + (lane & 31),
-    // contraction over the tile's rows r0 + 8 (e >> 2) + 4 h + (e & 3).
-    // 16-bit types: ds_read_b64_tr_b16 hands lane i of 16 the i-th column of
-    // the 4 x 16 block whose row i >> 2, columns 4 (i & 3) + 0..3 it addresses.
-    static __device__ __forceinline__ Frag frag_cols(uint32_t t, int r0, int cb, int lane) {
-        const int h = lane >> 5;
+    // contraction over the tile's rows r0 + 8 (e >> 2) + 4 h + (e & 3); o as
+    // above.  16-bit types: ds_read_b64_tr_b16 hands lane i of 16 the i-th
+    // column of the 4 x 16 block whose row i >> 2, columns 4 (i & 3) + 0..3 it
+    // addresses.  Rows eight further on have their chunks exchanged between the
+    // halves of a group.
+    static __device__ __forceinline__ Frag frag_cols(const Lanes& l, int o, int cb) {
         if constexpr (sizeof(T) == 2) {
             typedef __attribute__((__vector_size__(8))) short s16x4;
             typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-            const int i = lane & 15;
-            const int r = r0 + 4 * h + (i >> 2);
-            const int c = cb * 4 + ((lane >> 4) & 1) * 2 + ((i & 3) >> 1);
-            const uint32_t p = t + at(r, c) + (i & 1) * 8;
+            const int c = cb % kColAddrs;
+            o += cb / kColAddrs * (16 * kGroup);
             union {
                 s16x4 q[2];
                 Frag f;
             } u;
-            u.q[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)p);
-            u.q[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(p + 8 * kRow));
+            u.q[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(l.cols[c] + o));
+            u.q[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_s16x4*)(uintptr_t)(l.cols[c ^ (kColAddrs / 2)] + o + 8 * kRow));
             return u.f;
         } else {
             Frag f;
-            const int x = cb * 32 + (lane & 31);
+            o += cb / 2 * 256;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int r = r0 + 8 * (e >> 2) + 4 * h + (e & 3);
-                f[e] = lds_read<float>(t + at(r, x >> 2) + (x & 3) * 4);
-            }
+            for (int e = 0; e < 8; ++e)
+                f[e] = lds_read<float>(l.cols[(e & 3) + 4 * ((cb & 1) ^ (e >> 2))] + o + 8 * (e >> 2) * kRow);
             return f;
         }
     }
@@ -229,6 +269,12 @@ __device__ __forceinline__ void dma_lane4(const char* src, uint32_t lds) {
 __device__ __forceinline__ void dma_wait() {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
 }
+// The same but for the wave's last N copies (loads complete in order).
+template <int N>
+__device__ __forceinline__ void dma_wait_but() {
+    static_assert(N < 64, "a six-bit counter");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
 
 // Fills a tile of ROWS rows in LDS from global memory, by NT threads (whole
 // waves; t counts within them).  Chunk positions in LDS are dealt out in
@@ -242,13 +288,14 @@ struct Loader {
     using L = Tile<OP, DP>;
     using T = typename El<OP>::T;
     static constexpr int kN = ROWS * L::kCh / NT, kStep = NT / L::kCh;
-    static_assert(ROWS * L::kCh % NT == 0 && NT % L::kCh == 0, "whole rows per step");
-    static constexpr uint64_t kAll = ROWS == 64 ? ~0ull : (1ull << ROWS) - 1;
+    static_assert(ROWS * L::kCh % NT == 0 && NT % L::kCh == 0 && ROWS <= 64,
+                  "whole rows per step, a flag each");
+    static constexpr uint64_t kAll = ROWS >= 64 ? ~0ull : (1ull << ROWS) - 1;
 
     static __device__ __forceinline__ void fill(uint32_t lds, const T* base, int64_t stride,
                                                 uint64_t seen, int w, bool vec, int t) {
         const int c0 = t % L::kCh, r0 = t / L::kCh;
-        const uint32_t dst = lds + (t & ~63) * 16;
+        const uint32_t dst = lds + (NT == 64 ? 0 : wave_id() * 1024);
         if (vec) {
             const char* src = (const char*)(base + r0 * stride);
             const int64_t step = kStep * stride * (int64_t)sizeof(T);
@@ -271,7 +318,7 @@ struct Loader {
                 T x[L::kEpc];
 #pragma unroll
                 for (int e = 0; e < L::kEpc; ++e) x[e] = (T)0.f;
-                if ((seen >> r) & 1) load_elems<OP, L::kEpc>(base + r * stride, c * L::kEpc, w, false, x);
+                if (((seen >> r) & 1)) load_elems<OP, L::kEpc>(base + r * stride, c * L::kEpc, w, false, x);
                 u32x4 v;
                 __builtin_memcpy(&v, x, 16);
                 lds_write<u32x4>(lds + (s * NT + t) * 16, v);
@@ -296,12 +343,48 @@ __device__ __forceinline__ int attn_offset(const AttnArgs& a, int b) {
     return min(max(o, -kAttnMaxOffset), kAttnMaxOffset);
 }
 
-// Bit x: key j0 + x (x < 64) exists and is not masked out.
-__device__ __forceinline__ uint64_t seen_keys(const AttnArgs& a, int b, int len, int j0, int lane) {
-    bool s = j0 + lane < len;
-    if (a.key_mask && s) s = a.key_mask[b * a.mask_stride + j0 + lane] != 0;
-    return __ballot(s);
-}
+// Which of the keys of a tile of KT (at most 64) exist and are not masked out:
+// bit x of tile u's word for key j_first + u stride + x < je.  Without a mask
+// the word follows from je; with one, words are formed 64 tiles at a time and
+// kept in LDS (one wave's work, W waves sharing it), so that no tile's fetch
+// waits for a mask byte.
+template <int KT, int W>
+struct SeenKeys {
+    const uint8_t* mask;  // of this batch entry, or NULL
+    uint32_t words;       // LDS address of 128 words
+    int j_first, stride, je;
+
+    // words of tiles u .. u + 63 (all lanes of the wave; part wid of W), eight
+    // loads at a time
+    __device__ __forceinline__ void fill(int u, int lane, int wid) const {
+        if (!mask) return;
+#pragma unroll 1
+        for (int v = u + wid * 8; v < u + 64; v += 8 * W) {
+            bool ok[8] = {};
+            if (j_first + (int64_t)v * stride < je)
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const int64_t j = j_first + (int64_t)(v + x) * stride + lane;
+                ok[x] = lane < KT && j < je && mask[j] != 0;
+            }
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const uint64_t w = __ballot(ok[x]);
+                if (lane == 0) lds_write<uint64_t>(words + 8 * ((v + x) & 127), w);
+            }
+        }
+    }
+    __device__ __forceinline__ uint64_t operator()(int u) const {
+        if (mask) {
+            const uint64_t w = lds_read<uint64_t>(words + 8 * (u & 127));
+            const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(w >> 32));
+            const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)w);
+            return ((uint64_t)hi << 32) | lo;
+        }
+        const int64_t left = je - (j_first + (int64_t)u * stride);
+        return left >= KT ? (KT == 64 ? ~0ull : (1ull << (KT & 63)) - 1) : left <= 0 ? 0 : (1ull << left) - 1;
+    }
+};
 // Bits 0 .. x (none for x < 0).
 __device__ __forceinline__ uint32_t bits_upto(int x) {
     return x < 0 ? 0u : x >= 31 ? ~0u : (2u << x) - 1u;

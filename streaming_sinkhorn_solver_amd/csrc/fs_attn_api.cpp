@@ -189,23 +189,27 @@ fs_status take_desc(const fs_attention_desc* p, AttnArgs& a) {
         krows > ((int64_t)1 << 31) || (int64_t)a.G * d.n > (1 << 30))
         return fail(FS_ERR_INVALID_ARG, "batch * heads * rows is beyond 2^31");
 
-    // Splits: enough workgroups for two rounds of the chip, no range so short
-    // that the join costs more than it gains.
-    const int64_t items = few_rows(d) ? (int64_t)d.batch * d.kv_heads * cdiv((int64_t)a.G * d.n, 32)
-                                      : (int64_t)d.batch * d.heads * cdiv(d.n, kAttnRows);
+    // Key ranges.  Few rows: enough workgroups for the chip, at least one tile
+    // for every wave, at most 32 tiles (ranges of unequal sequences then even
+    // out).  Many rows: only where whole sequences leave CUs idle.
+    const int width = std::max(d.d, d.dv), es = elem_size(d.dtype);
+    const int row = (width <= 64 ? 64 : width <= 128 ? 128 : 256) * es;  // bytes of a tile's row
+    const bool few = few_rows(d);
+    const int64_t items = few ? (int64_t)d.batch * d.kv_heads * cdiv((int64_t)a.G * d.n, 32)
+                              : (int64_t)d.batch * d.heads * cdiv(d.n, kAttnRows);
+    const int64_t turn = few ? (row <= 128 ? 8 : 4) * 32 : 256;  // keys of one turn of a workgroup
     a.n_split = 1;
     a.split_keys = d.m;
     if (items > 0 && d.m > 0) {
-        const int64_t want = cdiv(2 * kCus, items);
-        const int64_t most = std::min<int64_t>(kAttnMaxSplit, d.m / 512);
-        const int64_t s = std::max<int64_t>(1, std::min(want, most));
-        a.split_keys = (int)(cdiv(cdiv(d.m, s), 128) * 128);
+        int64_t s = cdiv(kCus, items);
+        if (few) s = std::max(s, cdiv(d.m, 32 * turn));
+        s = std::max<int64_t>(1, std::min({s, (int64_t)kAttnMaxSplit, d.m / turn}));
+        a.split_keys = (int)(cdiv(cdiv(d.m, s), turn) * turn);
         a.n_split = (int)cdiv(d.m, a.split_keys);
     }
     // Backward passes: 128 rows a workgroup where that fills the chip, else 32,
     // and then the queries in ranges if there are few keys.
-    const int width = std::max(d.d, d.dv), es = elem_size(d.dtype);
-    const bool can = (width <= 64 ? 64 : width <= 128 ? 128 : 256) * es <= 256;
+    const bool can = row <= 256;
     a.alone_q = can && (int64_t)d.batch * d.heads * cdiv(d.n, kAttnRows) < kCus;
     a.alone_k = can && (int64_t)d.batch * d.kv_heads * cdiv(d.m, kAttnRows) < kCus;
     const int64_t kblocks = cdiv(d.m, a.alone_k ? 32 : kAttnRows);
@@ -216,7 +220,7 @@ fs_status take_desc(const fs_attention_desc* p, AttnArgs& a) {
         const int64_t want = kCus / kitems;
         const int64_t most = std::min<int64_t>(16, d.n / 256);
         const int64_t s = std::max<int64_t>(1, std::min(want, most));
-        a.split_rows = (int)(cdiv(cdiv(d.n, s), 64) * 64);
+        a.split_rows = (int)(cdiv(cdiv(d.n, s), 128) * 128);
         a.q_split = (int)cdiv(d.n, a.split_rows);
     }
     a.line_blocks = (int)(a.q_split * kblocks);

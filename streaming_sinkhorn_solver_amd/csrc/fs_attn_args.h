@@ -14,7 +14,7 @@ constexpr int kAttnMaxEdge = 1024;     // the largest edge (a bias line stays wi
 constexpr int kAttnMaxOffset = 1 << 29;  // j - i - offset stays a 32-bit number
 constexpr int kAttnMaxSplit = 64;
 constexpr int kAttnRows = 128;         // query (or key) rows of a workgroup of four waves
-constexpr int kAttnRowPad = 64;       // row terms are padded to whole query tiles
+constexpr int kAttnRowPad = 128;      // row terms are padded to whole query tiles
 constexpr int kAttnFewRows = 32;       // packed rows of a workgroup of the few-row kernel
 
 // Strides are in elements: batch, row, head.

@@ -114,19 +114,28 @@ struct DsScale {
     __device__ __forceinline__ float undo() const { return 1.f / f; }
 };
 
-// Rows of a tile, and whether the waves of a workgroup share it.  Shared: four
-// waves hold 32 rows each and pass over the same tiles, fetched once for all.
-// Alone (few rows in all): they hold the same 32 rows, each passes over every
-// fourth tile, fetched for itself, and their sums are joined at the end -- four
-// times the workgroups and a quarter of the steps for four times the fetches.
-// Rows of 512 bytes leave no LDS for tiles of four waves: always shared.
-template <int OP, int DP, bool ALONE>
+// Two forms of each pass.  Shared: the four waves of a workgroup hold 32 rows
+// each and pass over the same tiles, fetched once for all.  Alone, for few rows
+// in all: the waves hold the same 32 rows, each passes over every fourth tile,
+// fetched for itself, and their sums are joined at the end -- four times the
+// workgroups and a quarter of the steps for four times the fetches.  (Rows of
+// 512 bytes leave no LDS for tiles of four waves: always shared.)
+//
+// A tile is worked on 32 rows at a time.  Where LDS allows, the next tile is
+// fetched into a second buffer meanwhile; two workgroups (or, with the
+// registers of two, one) share a CU, and one wave's products run under
+// another's exponentials.  Measured against forms whose steps are pipelined
+// within a wave (the products of the next 32 rows among the exponentials of
+// these): those need registers that cost the second wave, and were 6 to 25%
+// slower.
+template <int OP, int DP, bool ALONE, int MOST>
 struct BwdShape {
     static constexpr int kRow = Tile<OP, DP>::kRow;
-    static constexpr int kTile = !ALONE && kRow <= 256 ? 64 : 32;
+    static constexpr int kTile = ALONE || kRow > 256 ? 32 : kRow > 128 || MOST < 128 ? 64 : 128;
     static constexpr int kBufs = ALONE && kRow > 128 ? 1 : 2;
     static constexpr int kSets = ALONE ? 4 : 1;
     static constexpr int kRows = ALONE ? 32 : kAttnRows;  // rows a workgroup holds
+    static constexpr int kNt = ALONE ? 64 : 256;          // threads that fetch a tile
 };
 
 // Joins one lane-held 32-column result of four waves: adds waves 1..3 to wave 0
@@ -171,94 +180,247 @@ __device__ __forceinline__ void join_waves(f32x16 (&x)[ND], LdsFloats buf, int w
 // lanes sum a column each; positions between the last edges are added to the
 // wave's line in LDS (one lane a position), those beyond to the lane's sums.
 constexpr int kDiag = 64;
+
+// What the two forms share of the pass over queries: a lane's key, the range of
+// queries, the bias's sums and the output.
 template <int OP, int DP, bool BIAS, bool ALONE>
-__global__ __launch_bounds__(256, (Tile<OP, DP>::kRow <= 128 && !(BIAS && ALONE) ? 2 : 1)) void attn_bwd_kv_kernel(const AttnArgs a) {
+struct KvPass {
+    using S = BwdShape<OP, DP, ALONE, 64>;
+    static constexpr int ROWS = S::kRows, QT = S::kTile;
     using E = El<OP>;
     using T = typename E::T;
     using L = Tile<OP, DP>;
-    using S = BwdShape<OP, DP, ALONE>;
-    constexpr int QT = S::kTile, ND = DP / 32, NK = DP / 16;
-    using Load = Loader<OP, DP, QT, ALONE ? 64 : 256>;
-    __shared__ __attribute__((aligned(256))) char tiles[S::kSets][S::kBufs][2][QT * L::kRow];
-    __shared__ __attribute__((aligned(16))) float row_t[S::kSets][S::kBufs][2][QT];
-    __shared__ float diag[BIAS ? 4 : 1][BIAS ? 32 * kDiag : 1];
+    static constexpr int ND = DP / 32, NK = DP / 16;
+    int lane, wid, h, kb, split, kvh, b, n_line, off, j0, j, first, end, n_tiles;
+    bool key_ok;
+    LdsFloats line, gline, dg;
+    float sum_lo, sum_hi;
+
+    __device__ __forceinline__ KvPass(const AttnArgs& a, float* lines, float* diag) {
+        const int t = threadIdx.x;
+        lane = t & 63, wid = wave_id(), h = lane >> 5;
+        const int nkb = (a.m + ROWS - 1) / ROWS;
+        int w = xcd_item(blockIdx.x, gridDim.x);
+        kb = w % nkb;
+        w /= nkb;
+        split = w % a.q_split;
+        w /= a.q_split;
+        kvh = w % a.K, b = w / a.K;
+        n_line = a.r0 + a.rp + 1;
+        line.a = lds_addr(lines);
+        gline.a = line.a + 4 * (1 + wid) * n_line;
+        dg.a = lds_addr(diag) + (BIAS ? wid * 32 * kDiag * 4 : 0);
+        off = attn_offset(a, b);
+        const int len = attn_kv_len(a, b), qlen = attn_q_len(a, b);
+        j0 = kb * ROWS + (ALONE ? 0 : wid * 32), j = j0 + (lane & 31);
+        key_ok = j < len;
+        if (key_ok && a.key_mask) key_ok = a.key_mask[b * a.mask_stride + j] != 0;
+        // tiles of this workgroup's query range, from the first that sees a key
+        // of this block on
+        first = split * a.split_rows;
+        end = a.q_split == 1 ? qlen : min(qlen, first + a.split_rows);
+        if (a.causal) first = max(first, (max(0, kb * ROWS - off) / QT) * QT);
+        if (kb * ROWS >= len) first = end;
+        n_tiles = first < end ? (end - first + QT - 1) / QT : 0;
+        if (BIAS && a.gbias)
+            for (int x = lane; x < 32 * kDiag; x += 64) dg.set(x, 0.f);
+    }
+
+    // The rows of tile u of head g: q and do to LDS (lds: a tile each), and the
+    // row terms, 64 floats for every 32 rows, to terms.
+    __device__ __forceinline__ void fetch(const AttnArgs& a, int g, int u, uint32_t lds,
+                                          uint32_t terms) const {
+        using Load = Loader<OP, DP, QT, S::kNt>;
+        const int i0 = first + u * QT, head = kvh * a.G + g;
+        const uint64_t seen = ((uint64_t)bits_upto(end - 33 - i0) << 32) | bits_upto(end - 1 - i0);
+        const int t = ALONE ? lane : (int)threadIdx.x;
+        Load::fill(lds, (const T*)a.q.p + b * a.q.sb + head * a.q.sh + (int64_t)i0 * a.q.sr, a.q.sr,
+                   seen, a.d, a.q.vec, t);
+        Load::fill(lds + QT * L::kRow,
+                   (const T*)a.go.p + b * a.go.sb + head * a.go.sh + (int64_t)i0 * a.go.sr, a.go.sr,
+                   seen, a.dv, a.go.vec, t);
+        const int part = ALONE ? 0 : wid;  // 32 rows a wave
+        if (part < QT / 32) {
+            const int64_t lrow = ((int64_t)b * a.H + head) * a.n_pad + i0 + 32 * part;
+            const float* src = (lane < 32 ? a.nl2 : a.delta) + lrow + (lane & 31);
+            dma_lane4((const char*)src, terms + 256 * part);
+        }
+    }
+
+    __device__ __forceinline__ void start_head(const AttnArgs& a, int g) {
+        sum_lo = sum_hi = 0.f;
+        if (!BIAS) return;
+        __syncthreads();
+        load_line(a, kvh * a.G + g, line, threadIdx.x, 256);
+        if (a.gbias)
+            for (int x = lane; x < n_line; x += 64) gline.set(x, 0.f);
+        __syncthreads();
+    }
+
+    // Row terms of a block as the lane needs them: rl = -L (+ bias), rd = delta.
+    // Where lo or hi is set, the block lies wholly behind or before the edges.
+    __device__ __forceinline__ void row_terms(const AttnArgs& a, int i0, uint32_t terms, float (&rl)[16],
+                                              float (&rd)[16], bool& lo_far, bool& hi_far) const {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const f32x4 x = lds_read<f32x4>(terms + 4 * (8 * q + 4 * h));
+            const f32x4 y = lds_read<f32x4>(terms + 4 * (32 + 8 * q + 4 * h));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                rl[4 * q + r] = x[r];
+                rd[4 * q + r] = y[r];
+            }
+        }
+        lo_far = hi_far = false;
+        if (BIAS) {
+            lo_far = j0 + 31 - i0 - off <= -a.r0;
+            hi_far = !lo_far && j0 - i0 - 31 - off >= a.rp;
+            if (lo_far || hi_far) {
+                const float ca = line[lo_far ? 0 : n_line - 1];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) rl[r] += ca;
+            } else {
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    rl[r] += line[line_index(a, j - (i0 + 8 * (r >> 2) + 4 * h + (r & 3)) - off)];
+            }
+        }
+    }
+    // Scores of queries before j - off do not see key j.
+    __device__ __forceinline__ void hide(const AttnArgs& a, int i0, f32x16& s) const {
+        if (a.causal && j0 + 31 - off > i0) {
+            asm volatile("");  // a branch: most tiles need none of it
+            const uint32_t vis = ~bits_upto(j - off - i0 - 1) >> (4 * h);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[r] = flag(vis, r) ? s[r] : -INFINITY;
+        }
+    }
+    // Adds a block's dS to the sums of its relative positions.
+    __device__ __forceinline__ void add_bias(const AttnArgs& a, int i0, const f32x16& ds, bool lo_far,
+                                             bool hi_far) {
+        if (!BIAS || !a.gbias) return;
+        if (lo_far || hi_far) {
+            float x = 0.f;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x += ds[r];
+            x = key_ok ? x : 0.f;
+            if (lo_far) sum_lo += x;
+            else sum_hi += x;
+            return;
+        }
+        const int k = lane & 31;
+        wave_fence();
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            dg.set(k * kDiag + k - (8 * (r >> 2) + 4 * h + (r & 3)) + 31, key_ok ? ds[r] : 0.f);
+        wave_fence();
+        float x = 0.f;
+#pragma unroll
+        for (int y = 0; y < 32; ++y) x += dg[y * kDiag + lane];
+        const int r = j0 - i0 - 31 - off + lane;  // lane 63: no pair, x = 0
+        if (r <= -a.r0) sum_lo += x;
+        else if (r >= a.rp) sum_hi += x;
+        else gline.set(r + a.r0, gline[r + a.r0] + x);
+        wave_fence();
+    }
+    __device__ __forceinline__ void end_head(const AttnArgs& a, int g) {
+        if (!BIAS || !a.gbias) return;
+        sum_lo = wave_sum(sum_lo);
+        sum_hi = wave_sum(sum_hi);
+        if (lane == 0) {
+            gline.set(0, gline[0] + sum_lo);
+            gline.set(n_line - 1, gline[n_line - 1] + sum_hi);
+        }
+        __syncthreads();
+        const int nkb = (a.m + ROWS - 1) / ROWS;
+        float* part = a.line_part + ((int64_t)(kvh * a.G + g) * a.B * a.line_blocks +
+                                     (int64_t)b * a.line_blocks + split * nkb + kb) * n_line;
+        for (int x = threadIdx.x; x < n_line; x += 256)
+            part[x] = (line[n_line + x] + line[2 * n_line + x]) + (line[3 * n_line + x] + line[4 * n_line + x]);
+    }
+
+    template <bool DK, bool DV>
+    __device__ __forceinline__ void store(const AttnArgs& a, const f32x16 (&dk)[ND],
+                                          const f32x16 (&dv)[ND]) const {
+        if (j >= a.m) return;
+        if (a.q_split > 1) {
+            const int64_t row = ((int64_t)b * a.K + kvh) * a.m + j;
+            const int64_t rows = (int64_t)a.B * a.K * a.m;
+            float* pk = a.part_k + (split * rows + row) * a.d;
+            float* pv = a.part_v + (split * rows + row) * a.dv;
+#pragma unroll
+            for (int cb = 0; cb < ND; ++cb)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int x = 32 * cb + 8 * (r >> 2) + 4 * h + (r & 3);
+                    if (DK && x < a.d) pk[x] = key_ok ? dk[cb][r] : 0.f;
+                    if (DV && x < a.dv) pv[x] = key_ok ? dv[cb][r] : 0.f;
+                }
+            return;
+        }
+        T* ok = (T*)a.gk.p + b * a.gk.sb + (int64_t)j * a.gk.sr + kvh * a.gk.sh;
+        T* ov = (T*)a.gv.p + b * a.gv.sb + (int64_t)j * a.gv.sr + kvh * a.gv.sh;
+#pragma unroll
+        for (int cb = 0; cb < ND; ++cb)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float y[4], z[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    y[r] = DK && key_ok ? dk[cb][4 * q + r] : 0.f;
+                    z[r] = DV && key_ok ? dv[cb][4 * q + r] : 0.f;
+                }
+                if (DK && a.gk.p) store4<OP>(ok, 32 * cb + 8 * q + 4 * h, a.d, a.gk.vec, y[0], y[1], y[2], y[3]);
+                if (DV && a.gv.p) store4<OP>(ov, 32 * cb + 8 * q + 4 * h, a.dv, a.gv.vec, z[0], z[1], z[2], z[3]);
+            }
+    }
+};
+
+// PART: which sums this launch forms.  Both, as a rule; rows of 512 bytes leave
+// no registers for both, and they are formed by two launches.
+enum KvPart : int { PART_BOTH = 0, PART_DV = 1, PART_DK = 2 };
+template <int OP, int DP, bool BIAS, bool ALONE, int PART>
+__global__ __launch_bounds__(256, (Tile<OP, DP>::kRow <= 128 && !(BIAS && ALONE) ? 2 : 1))
+void attn_bwd_kv_kernel(const AttnArgs a) {
+    using P = KvPass<OP, DP, BIAS, ALONE>;
+    using S = typename P::S;
+    using E = typename P::E;
+    using T = typename P::T;
+    using L = typename P::L;
+    constexpr bool DK = PART != PART_DV, DV = PART != PART_DK;
+    constexpr int ND = P::ND, NK = P::NK, QT = P::QT, kBytes = QT * L::kRow;
+    __shared__ __attribute__((aligned(256))) char tiles[S::kSets][S::kBufs][2][kBytes];
+    __shared__ __attribute__((aligned(16))) float terms[S::kSets][S::kBufs][2 * QT];
+    __shared__ float diag[BIAS ? 4 * 32 * kDiag : 1];
     extern __shared__ float lines[];  // BIAS: [1 + 4][n_line], the bias and the waves' sums
     static_assert(!ALONE || sizeof(tiles) >= 3 * 32 * DP * 4, "the waves' sums fit the tiles' memory");
-
-    const int t = threadIdx.x, lane = t & 63, wid = t >> 6, h = lane >> 5;
-    const int set = ALONE ? wid : 0;
-    const int nkb = (a.m + S::kRows - 1) / S::kRows;
-    int w = xcd_item(blockIdx.x, gridDim.x);
-    const int kb = w % nkb;
-    w /= nkb;
-    const int split = w % a.q_split;
-    w /= a.q_split;
-    const int kvh = w % a.K, b = w / a.K;
-    const int n_line = a.r0 + a.rp + 1;
-    const LdsFloats line{lds_addr(lines)}, gline{line.a + 4 * (1 + wid) * n_line};
-    const LdsFloats dg{lds_addr(diag[BIAS ? wid : 0])};
-
-    const int off = attn_offset(a, b);
-    const int len = attn_kv_len(a, b);
-    const int qlen = attn_q_len(a, b);
-    const int j0 = kb * S::kRows + (ALONE ? 0 : wid * 32), j = j0 + (lane & 31);
-    bool key_ok = j < len;
-    if (key_ok && a.key_mask) key_ok = a.key_mask[b * a.mask_stride + j] != 0;
+    P p(a, lines, diag);
+    const int lane = p.lane, wid = p.wid, set = ALONE ? wid : 0;
 
     typename E::Frag kf[NK], vf[NK];
-    load_row_frags<OP, DP>((const T*)a.k.p + b * a.k.sb + (int64_t)j * a.k.sr + kvh * a.k.sh,
-                           key_ok, a.d, a.k.vec, lane, kf);
-    load_row_frags<OP, DP>((const T*)a.v.p + b * a.v.sb + (int64_t)j * a.v.sr + kvh * a.v.sh,
-                           key_ok, a.dv, a.v.vec, lane, vf);
-    f32x16 dk[ND], dvv[ND];
+    load_row_frags<OP, DP>((const T*)a.k.p + p.b * a.k.sb + (int64_t)p.j * a.k.sr + p.kvh * a.k.sh,
+                           p.key_ok, a.d, a.k.vec, lane, kf);
+    if (DK)
+        load_row_frags<OP, DP>((const T*)a.v.p + p.b * a.v.sb + (int64_t)p.j * a.v.sr + p.kvh * a.v.sh,
+                               p.key_ok, a.dv, a.v.vec, lane, vf);
+    f32x16 dk[ND], dv[ND];
 #pragma unroll
     for (int x = 0; x < ND; ++x)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) dk[x][r] = dvv[x][r] = 0.f;
+        for (int r = 0; r < 16; ++r) dk[x][r] = dv[x][r] = 0.f;
     DsScale<OP, ND> dss;
-
-    // tiles of this workgroup's query range, from the first that sees a key of
-    // this block on
-    int first = split * a.split_rows;
-    const int end = a.q_split == 1 ? qlen : min(qlen, first + a.split_rows);
-    if (a.causal) first = max(first, (max(0, kb * S::kRows - off) / QT) * QT);
-    if (kb * S::kRows >= len) first = end;
-    const int n_tiles = first < end ? (end - first + QT - 1) / QT : 0;
-    if (BIAS && a.gbias)
-        for (int x = lane; x < 32 * kDiag; x += 64) dg.set(x, 0.f);
+    const uint32_t tile0 = lds_addr(tiles[set]), term0 = lds_addr(terms[set]);
+    const typename L::Lanes lanes(tile0, lane);
 
     // With a bias the heads are taken one after the other (each has its line);
     // else the tiles of all heads are one sequence.
     const int step = ALONE ? 4 : 1;
     for (int g0 = 0; g0 < (BIAS ? a.G : 1); ++g0) {
-        const int n_all = BIAS ? n_tiles : n_tiles * a.G;
-        float sum_lo = 0.f, sum_hi = 0.f;
-        if (BIAS) {
-            __syncthreads();
-            load_line(a, kvh * a.G + g0, line, t, 256);
-            if (a.gbias)
-                for (int x = lane; x < n_line; x += 64) gline.set(x, 0.f);
-            __syncthreads();
-        }
+        const int n_all = BIAS ? p.n_tiles : p.n_tiles * a.G;
+        p.start_head(a, g0);
         const auto fetch = [&](int u, int buf) {
-            const int g = BIAS ? g0 : u / n_tiles;
-            const int i0 = first + (BIAS ? u : u - g * n_tiles) * QT, head = kvh * a.G + g;
-            const uint64_t seen = QT == 64 ? ((uint64_t)bits_upto(end - 33 - i0) << 32) | bits_upto(end - 1 - i0)
-                                           : bits_upto(end - 1 - i0);
-            const int tt = ALONE ? lane : t;
-            Load::fill(lds_addr(tiles[set][buf][0]),
-                       (const T*)a.q.p + b * a.q.sb + head * a.q.sh + (int64_t)i0 * a.q.sr, a.q.sr,
-                       seen, a.d, a.q.vec, tt);
-            Load::fill(lds_addr(tiles[set][buf][1]),
-                       (const T*)a.go.p + b * a.go.sb + head * a.go.sh + (int64_t)i0 * a.go.sr,
-                       a.go.sr, seen, a.dv, a.go.vec, tt);
-            // the row terms: 2 QT floats, by one wave (two for QT = 64)
-            const int64_t lrow = ((int64_t)b * a.H + head) * a.n_pad + i0;
-            if (ALONE || wid < 2 * QT / 64) {
-                const int x = ALONE ? lane : t;
-                const float* src = (x < QT ? a.nl2 : a.delta - QT) + lrow + x;
-                dma_lane4((const char*)src, lds_addr(row_t[set][buf]) + 4 * (x & ~63));
-            }
+            const int g = BIAS ? g0 : u / p.n_tiles;
+            p.fetch(a, g, BIAS ? u : u - g * p.n_tiles, tile0 + 2 * buf * kBytes, term0 + 8 * QT * buf);
         };
         int u = ALONE ? wid : 0, cur = 0;
         if (u < n_all) fetch(u, 0);
@@ -268,100 +430,47 @@ __global__ __launch_bounds__(256, (Tile<OP, DP>::kRow <= 128 && !(BIAS && ALONE)
                 wave_fence();
             else
                 __builtin_amdgcn_s_barrier();
-            const uint32_t qt = lds_addr(tiles[set][cur][0]);
-            const uint32_t gt = lds_addr(tiles[set][cur][1]);
-            const uint32_t row_l = lds_addr(row_t[set][cur][0]), row_d = lds_addr(row_t[set][cur][1]);
+            const typename L::Lanes now(lanes, cur * 2 * kBytes);
+            const uint32_t term = term0 + 8 * QT * cur;
             if (S::kBufs == 2) {
                 cur ^= 1;
                 if (u + step < n_all) fetch(u + step, cur);
             }
-            const int i00 = first + (BIAS ? u : u % n_tiles) * QT;
+            const int i00 = p.first + (BIAS ? u : u % p.n_tiles) * QT;
 #pragma unroll
             for (int qb = 0; qb < QT / 32; ++qb) {
-                const int i0 = i00 + 32 * qb;
+                const int i0 = i00 + 32 * qb, o = 32 * qb * L::kRow;
                 f32x16 s, dp;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.f;
 #pragma unroll
-                for (int kk = 0; kk < NK; ++kk)
-                    s = E::mfma(L::frag_rows(qt, 32 * qb, kk, lane), kf[kk], s);
+                for (int kk = 0; kk < NK; ++kk) s = E::mfma(L::frag_rows(now, o, kk), kf[kk], s);
+                if (DK) {
 #pragma unroll
-                for (int kk = 0; kk < NK; ++kk)
-                    dp = E::mfma(L::frag_rows(gt, 32 * qb, kk, lane), vf[kk], dp);
+                    for (int kk = 0; kk < NK; ++kk)
+                        dp = E::mfma(L::frag_rows(now, kBytes + o, kk), vf[kk], dp);
+                }
                 float rl[16], rd[16];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const f32x4 x = lds_read<f32x4>(row_l + 4 * (32 * qb + 8 * q + 4 * h));
-                    const f32x4 y = lds_read<f32x4>(row_d + 4 * (32 * qb + 8 * q + 4 * h));
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        rl[4 * q + r] = x[r];
-                        rd[4 * q + r] = y[r];
-                    }
-                }
-                bool lo_far = false, hi_far = false;
-                if (BIAS) {
-                    const int lo = j0 - i0 - 31 - off, hi = j0 + 31 - i0 - off;
-                    lo_far = hi <= -a.r0;
-                    hi_far = !lo_far && lo >= a.rp;
-                    if (lo_far || hi_far) {
-                        const float ca = line[lo_far ? 0 : n_line - 1];
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) rl[r] += ca;
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            rl[r] += line[line_index(a, j - (i0 + 8 * (r >> 2) + 4 * h + (r & 3)) - off)];
-                    }
-                }
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] = ex2(fmaf(s[r], a.c, rl[r]));
-                if (a.causal && j0 + 31 - off > i0) {
-                    // queries from j - off on see key j
-                    const uint32_t vis = ~bits_upto(j - off - i0 - 1) >> (4 * h);
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[r] = flag(vis, r) ? s[r] : 0.f;
-                }
-                f32x16 ds;
+                bool lo_far, hi_far;
+                p.row_terms(a, i0, term + 256 * qb, rl, rd, lo_far, hi_far);
+                p.hide(a, i0, s);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    ds[r] = s[r] * (dp[r] - rd[r]);
-                    if (kLiftP<OP> != 1.f) s[r] *= kLiftP<OP>;
+                    const float w = ex2(fmaf(s[r], a.c, rl[r]));
+                    dp[r] = w * (dp[r] - rd[r]);
+                    s[r] = w * kLiftP<OP>;
                 }
-                if (BIAS && a.gbias) {
-                    if (lo_far || hi_far) {
-                        float x = 0.f;
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) x += ds[r];
-                        x = key_ok ? x : 0.f;
-                        if (lo_far) sum_lo += x;
-                        else sum_hi += x;
-                    } else {
-                        const int k = lane & 31;
-                        wave_fence();
-#pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            dg.set(k * kDiag + k - (8 * (r >> 2) + 4 * h + (r & 3)) + 31,
-                                   key_ok ? ds[r] : 0.f);
-                        wave_fence();
-                        float x = 0.f;
-#pragma unroll
-                        for (int y = 0; y < 32; ++y) x += dg[y * kDiag + lane];
-                        const int r = j0 - i0 - 31 - off + lane;  // lane 63: no pair, x = 0
-                        if (r <= -a.r0) sum_lo += x;
-                        else if (r >= a.rp) sum_hi += x;
-                        else gline.set(r + a.r0, gline[r + a.r0] + x);
-                        wave_fence();
-                    }
+                if (DK) {
+                    p.add_bias(a, i0, dp, lo_far, hi_far);
+                    dss.apply(dp, dk);
                 }
-                dss.apply(ds, dk);
 #pragma unroll
                 for (int rc = 0; rc < 2; ++rc) {
-                    const typename E::Frag pf = L::pack(s, rc), df = L::pack(ds, rc);
+                    const typename E::Frag pf = L::pack(s, rc), df = L::pack(dp, rc);
 #pragma unroll
                     for (int cb = 0; cb < ND; ++cb) {
-                        dvv[cb] = E::mfma(L::frag_cols(gt, 32 * qb + 16 * rc, cb, lane), pf, dvv[cb]);
-                        dk[cb] = E::mfma(L::frag_cols(qt, 32 * qb + 16 * rc, cb, lane), df, dk[cb]);
+                        if (DV) dv[cb] = E::mfma(L::frag_cols(now, kBytes + o + 16 * rc * L::kRow, cb), pf, dv[cb]);
+                        if (DK) dk[cb] = E::mfma(L::frag_cols(now, o + 16 * rc * L::kRow, cb), df, dk[cb]);
                     }
                 }
             }
@@ -371,21 +480,7 @@ __global__ __launch_bounds__(256, (Tile<OP, DP>::kRow <= 128 && !(BIAS && ALONE)
                 fetch(u + step, 0);
             }
         }
-        if (BIAS && a.gbias) {
-            sum_lo = wave_sum(sum_lo);
-            sum_hi = wave_sum(sum_hi);
-            if (lane == 0) {
-                gline.set(0, gline[0] + sum_lo);
-                gline.set(n_line - 1, gline[n_line - 1] + sum_hi);
-            }
-            __syncthreads();
-            const int64_t parts = (int64_t)a.B * a.line_blocks;
-            float* part = a.line_part + ((int64_t)(kvh * a.G + g0) * parts +
-                                         (int64_t)b * a.line_blocks + split * nkb + kb) * n_line;
-            for (int x = t; x < n_line; x += 256)
-                part[x] = (line[n_line + x] + line[2 * n_line + x]) +
-                          (line[3 * n_line + x] + line[4 * n_line + x]);
-        }
+        if (DK) p.end_head(a, g0);
     }
 
     const float fk = a.scale * dss.undo(), fv = 1.f / kLiftP<OP>;
@@ -393,46 +488,16 @@ __global__ __launch_bounds__(256, (Tile<OP, DP>::kRow <= 128 && !(BIAS && ALONE)
     for (int cb = 0; cb < ND; ++cb)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            dk[cb][r] *= fk;
-            dvv[cb][r] *= fv;
+            if (DK) dk[cb][r] *= fk;
+            if (DV) dv[cb][r] *= fv;
         }
     if (ALONE) {
         const LdsFloats buf{lds_addr(tiles)};
         join_waves<DP, ND>(dk, buf, wid, lane);
-        join_waves<DP, ND>(dvv, buf, wid, lane);
+        join_waves<DP, ND>(dv, buf, wid, lane);
         if (wid > 0) return;
     }
-    if (j >= a.m) return;
-    if (a.q_split > 1) {
-        const int64_t row = ((int64_t)b * a.K + kvh) * a.m + j;
-        const int64_t rows = (int64_t)a.B * a.K * a.m;
-        float* pk = a.part_k + (split * rows + row) * a.d;
-        float* pv = a.part_v + (split * rows + row) * a.dv;
-#pragma unroll
-        for (int cb = 0; cb < ND; ++cb)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int x = 32 * cb + 8 * (r >> 2) + 4 * h + (r & 3);
-                if (x < a.d) pk[x] = key_ok ? dk[cb][r] : 0.f;
-                if (x < a.dv) pv[x] = key_ok ? dvv[cb][r] : 0.f;
-            }
-        return;
-    }
-    T* ok = (T*)a.gk.p + b * a.gk.sb + (int64_t)j * a.gk.sr + kvh * a.gk.sh;
-    T* ov = (T*)a.gv.p + b * a.gv.sb + (int64_t)j * a.gv.sr + kvh * a.gv.sh;
-#pragma unroll
-    for (int cb = 0; cb < ND; ++cb)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float y[4], z[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                y[r] = key_ok ? dk[cb][4 * q + r] : 0.f;
-                z[r] = key_ok ? dvv[cb][4 * q + r] : 0.f;
-            }
-            if (a.gk.p) store4<OP>(ok, 32 * cb + 8 * q + 4 * h, a.d, a.gk.vec, y[0], y[1], y[2], y[3]);
-            if (a.gv.p) store4<OP>(ov, 32 * cb + 8 * q + 4 * h, a.dv, a.gv.vec, z[0], z[1], z[2], z[3]);
-        }
+    p.template store<DK, DV>(a, dk, dv);
 }
 
 // Sums the query ranges' parts of dK and dV (a fixed order).
@@ -475,46 +540,107 @@ __global__ __launch_bounds__(256) void attn_kv_merge_kernel(const AttnArgs a) {
 // dL_i); the pass adds it, and the pass over the queries after it uses the
 // result.
 template <int OP, int DP, bool BIAS, bool ALONE>
-__global__ __launch_bounds__(256, (Tile<OP, DP>::kRow <= 128 ? 2 : 1)) void attn_bwd_q_kernel(const AttnArgs a) {
+struct QPass {
+    using S = BwdShape<OP, DP, ALONE, 128>;
+    static constexpr int ROWS = S::kRows;
     using E = El<OP>;
     using T = typename E::T;
     using L = Tile<OP, DP>;
-    using S = BwdShape<OP, DP, ALONE>;
-    constexpr int KT = S::kTile, NB = KT / 32, ND = DP / 32, NK = DP / 16;
-    using Load = Loader<OP, DP, KT, ALONE ? 64 : 256>;
-    __shared__ __attribute__((aligned(256))) char tiles[S::kSets][S::kBufs][2][KT * L::kRow];
+    static constexpr int ND = DP / 32, NK = DP / 16;
+    int lane, wid, h, head, b, kvh, n_line, off, i0, i, len;
+    bool row_ok, in;
+    int64_t lrow;
+    float rl, rd;
+    LdsFloats line;
+
+    __device__ __forceinline__ QPass(const AttnArgs& a, float* line_mem) {
+        const int t = threadIdx.x;
+        lane = t & 63, wid = wave_id(), h = lane >> 5;
+        const int nqb = (a.n + ROWS - 1) / ROWS;
+        int w = xcd_item(blockIdx.x, gridDim.x);
+        const int qb = w % nqb;
+        w /= nqb;
+        head = w % a.H, b = w / a.H, kvh = head / a.G;
+        n_line = a.r0 + a.rp + 1;
+        line.a = lds_addr(line_mem);
+        off = attn_offset(a, b);
+        i0 = qb * ROWS + (ALONE ? 0 : wid * 32), i = i0 + (lane & 31);
+        row_ok = i < attn_q_len(a, b);
+        in = i < a.n;
+        len = attn_kv_len(a, b);
+        if (a.causal) len = min(len, max(0, min((qb + 1) * ROWS, a.n) + off));
+        lrow = ((int64_t)b * a.H + head) * a.n_pad + i;
+        rl = in ? a.nl2[lrow] : -INFINITY;
+        rd = in ? a.delta[lrow] : 0.f;
+    }
+    // A block's scores ready for s cm + ca: masked keys at -inf, the bias in.
+    __device__ __forceinline__ void prepare(const AttnArgs& a, int j0, uint32_t vis, f32x16& s, float& cm,
+                                            float& ca) const {
+        if (a.causal) vis &= bits_upto(i + off - j0);
+        const bool all = __all(vis == ~0u);
+        vis >>= 4 * h;
+        cm = a.c, ca = rl;
+        if (BIAS) {
+            if (j0 + 31 - i0 - off <= -a.r0) {
+                ca += line[0];
+            } else if (j0 - i0 - 31 - off >= a.rp) {
+                ca += line[n_line - 1];
+            } else {
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    s[r] = fmaf(s[r], a.c, line[line_index(a, j0 + 8 * (r >> 2) + 4 * h + (r & 3) - i - off)]);
+                cm = 1.f;
+            }
+        }
+        if (!all) {
+            asm volatile("");  // a branch: most tiles need none of it
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[r] = flag(vis, r) ? s[r] : -INFINITY;
+        }
+    }
+    // delta made exact; dQ.  rest: the row's sum of dS.
+    __device__ __forceinline__ void store(const AttnArgs& a, const f32x16 (&acc)[ND], float rest) const {
+        if (!in) return;
+        if (h == 0 && rl != -INFINITY)
+            a.delta[lrow] = rd + rest - (a.glse ? a.glse[((int64_t)b * a.H + head) * a.n + i] : 0.f);
+        if (!a.gq.p) return;
+        T* o = (T*)a.gq.p + b * a.gq.sb + (int64_t)i * a.gq.sr + head * a.gq.sh;
+#pragma unroll
+        for (int cb = 0; cb < ND; ++cb)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                store4<OP>(o, 32 * cb + 8 * q + 4 * h, a.d, a.gq.vec, row_ok ? acc[cb][4 * q] : 0.f,
+                           row_ok ? acc[cb][4 * q + 1] : 0.f, row_ok ? acc[cb][4 * q + 2] : 0.f,
+                           row_ok ? acc[cb][4 * q + 3] : 0.f);
+    }
+};
+
+template <int OP, int DP, bool BIAS, bool ALONE>
+__global__ __launch_bounds__(256, (Tile<OP, DP>::kRow <= 128 ? 2 : 1))
+void attn_bwd_q_kernel(const AttnArgs a) {
+    using P = QPass<OP, DP, BIAS, ALONE>;
+    using S = typename P::S;
+    using E = typename P::E;
+    using T = typename P::T;
+    using L = typename P::L;
+    constexpr int ND = P::ND, NK = P::NK, KT = S::kTile, kBytes = KT * L::kRow;
+    constexpr int kPart = KT < 64 ? KT : 64, kParts = KT / kPart;  // keys of a word of flags
+    using Load = Loader<OP, DP, kPart, S::kNt>;
+    __shared__ __attribute__((aligned(256))) char tiles[S::kSets][S::kBufs][2][kBytes];
     __shared__ float line_mem[BIAS ? 2 * kAttnMaxEdge + 1 : 1];
-    const LdsFloats line{lds_addr(line_mem)};
     __shared__ float wsum[4][32];
-
-    const int t = threadIdx.x, lane = t & 63, wid = t >> 6, h = lane >> 5;
-    const int set = ALONE ? wid : 0;
-    const int nqb = (a.n + S::kRows - 1) / S::kRows;
-    int w = xcd_item(blockIdx.x, gridDim.x);
-    const int qb = w % nqb;
-    w /= nqb;
-    const int head = w % a.H, b = w / a.H, kvh = head / a.G;
-    const int n_line = a.r0 + a.rp + 1;
-
-    const int off = attn_offset(a, b);
-    const int i0 = qb * S::kRows + (ALONE ? 0 : wid * 32), i = i0 + (lane & 31);
-    const bool row_ok = i < attn_q_len(a, b);
-    int len = attn_kv_len(a, b);
-    if (a.causal) len = min(len, max(0, min((qb + 1) * S::kRows, a.n) + off));
-
+    __shared__ uint64_t words[S::kSets][128];
+    P p(a, line_mem);
+    const int lane = p.lane, wid = p.wid, set = ALONE ? wid : 0;
     if (BIAS) {
-        load_line(a, head, line, t, 256);
+        load_line(a, p.head, p.line, threadIdx.x, 256);
         __syncthreads();
     }
     typename E::Frag qf[NK], gf[NK];
-    load_row_frags<OP, DP>((const T*)a.q.p + b * a.q.sb + (int64_t)i * a.q.sr + head * a.q.sh,
-                           row_ok, a.d, a.q.vec, lane, qf);
-    load_row_frags<OP, DP>((const T*)a.go.p + b * a.go.sb + (int64_t)i * a.go.sr + head * a.go.sh,
-                           row_ok, a.dv, a.go.vec, lane, gf);
-    const int64_t lrow = ((int64_t)b * a.H + head) * a.n_pad + i;
-    const bool in = i < a.n;
-    const float rl = in ? a.nl2[lrow] : -INFINITY;
-    const float rd = in ? a.delta[lrow] : 0.f;
+    load_row_frags<OP, DP>((const T*)a.q.p + p.b * a.q.sb + (int64_t)p.i * a.q.sr + p.head * a.q.sh,
+                           p.row_ok, a.d, a.q.vec, lane, qf);
+    load_row_frags<OP, DP>((const T*)a.go.p + p.b * a.go.sb + (int64_t)p.i * a.go.sr + p.head * a.go.sh,
+                           p.row_ok, a.dv, a.go.vec, lane, gf);
     f32x16 acc[ND];
 #pragma unroll
     for (int x = 0; x < ND; ++x)
@@ -522,89 +648,85 @@ __global__ __launch_bounds__(256, (Tile<OP, DP>::kRow <= 128 ? 2 : 1)) void attn
         for (int r = 0; r < 16; ++r) acc[x][r] = 0.f;
     DsScale<OP, ND> dss;
     float rest = 0.f;  // sum of dS
-
-    const T* kbase = (const T*)a.k.p + b * a.k.sb + kvh * a.k.sh;
-    const T* vbase = (const T*)a.v.p + b * a.v.sb + kvh * a.v.sh;
-    uint64_t next = 0;
-    const auto fetch = [&](int j0, int buf) {
-        const int tt = ALONE ? lane : t;
-        next = seen_keys(a, b, len, j0, lane);
-        Load::fill(lds_addr(tiles[set][buf][0]), kbase + (int64_t)j0 * a.k.sr, a.k.sr, next, a.d, a.k.vec, tt);
-        Load::fill(lds_addr(tiles[set][buf][1]), vbase + (int64_t)j0 * a.v.sr, a.v.sr, next, a.dv, a.v.vec, tt);
+    const T* kbase = (const T*)a.k.p + p.b * a.k.sb + p.kvh * a.k.sh;
+    const T* vbase = (const T*)a.v.p + p.b * a.v.sb + p.kvh * a.v.sh;
+    const uint32_t tile0 = lds_addr(tiles[set]);
+    const typename L::Lanes lanes(tile0, lane);
+    // tiles u of this wave (or workgroup) start at key j_first + u stride
+    const int j_first = ALONE ? wid * KT : 0, stride = ALONE ? 4 * KT : KT;
+    const SeenKeys<kPart, ALONE ? 1 : 4> keys{a.key_mask ? a.key_mask + p.b * a.mask_stride : nullptr,
+                                              lds_addr(words[set]), j_first, stride / kParts, p.len};
+    const int n_tiles = p.len > j_first ? (p.len - j_first + stride - 1) / stride : 0;
+    const auto fetch = [&](int u, int buf) {
+        const int t = ALONE ? lane : (int)threadIdx.x;
+#pragma unroll
+        for (int x = 0; x < kParts; ++x) {
+            const int64_t j0 = j_first + (int64_t)u * stride + x * kPart;
+            const uint64_t seen = keys(u * kParts + x);
+            const uint32_t lds = tile0 + 2 * buf * kBytes + x * kPart * L::kRow;
+            Load::fill(lds, kbase + j0 * a.k.sr, a.k.sr, seen, a.d, a.k.vec, t);
+            Load::fill(lds + kBytes, vbase + j0 * a.v.sr, a.v.sr, seen, a.dv, a.v.vec, t);
+        }
     };
-    const int step = ALONE ? 4 * KT : KT;
-    int j0 = ALONE ? wid * KT : 0, cur = 0;
-    if (j0 < len) fetch(j0, 0);
-    for (; j0 < len; j0 += step) {
-        const uint64_t seen = next;
+    if (n_tiles) {
+        keys.fill(0, lane, ALONE ? 0 : wid);
+        if (ALONE)
+            wave_fence();
+        else if (a.key_mask)
+            __syncthreads();
+        fetch(0, 0);
+    }
+    int cur = 0;
+    for (int u = 0; u < n_tiles; ++u) {
         dma_wait();
         if (ALONE)
             wave_fence();
         else
             __builtin_amdgcn_s_barrier();
-        const uint32_t kt = lds_addr(tiles[set][cur][0]);
-        const uint32_t vt = lds_addr(tiles[set][cur][1]);
+        // the words of the 64 after these (the next fetch needs them at the earliest)
+        if (u * kParts % 64 == 0) {
+            keys.fill(u * kParts + 64, lane, ALONE ? 0 : wid);
+            wave_fence();
+        }
+        const typename L::Lanes now(lanes, cur * 2 * kBytes);
         if (S::kBufs == 2) {
             cur ^= 1;
-            if (j0 + step < len) fetch(j0 + step, cur);
+            if (u + 1 < n_tiles) fetch(u + 1, cur);
         }
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const int jb = j0 + 32 * nb;
-            uint32_t vis = (uint32_t)(seen >> (32 * nb));
-            if (a.causal) vis &= bits_upto(i + off - jb);
-            const bool all = __all(vis == ~0u);
-            vis >>= 4 * h;
+#pragma unroll 2
+        for (int nb = 0; nb < KT / 32; ++nb) {
+            const int j0 = j_first + u * stride + 32 * nb, o = 32 * nb * L::kRow;
+            const uint32_t vis = (uint32_t)(keys(u * kParts + nb / 2) >> (32 * (nb & 1)));
             f32x16 s, dp;
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.f;
 #pragma unroll
-            for (int kk = 0; kk < NK; ++kk) s = E::mfma(L::frag_rows(kt, 32 * nb, kk, lane), qf[kk], s);
+            for (int kk = 0; kk < NK; ++kk) s = E::mfma(L::frag_rows(now, o, kk), qf[kk], s);
 #pragma unroll
-            for (int kk = 0; kk < NK; ++kk) dp = E::mfma(L::frag_rows(vt, 32 * nb, kk, lane), gf[kk], dp);
-            bool lo_far = false, hi_far = false;
-            if (BIAS) {
-                const int lo = jb - i0 - 31 - off, hi = jb + 31 - i0 - off;
-                lo_far = hi <= -a.r0;
-                hi_far = !lo_far && lo >= a.rp;
+            for (int kk = 0; kk < NK; ++kk) dp = E::mfma(L::frag_rows(now, kBytes + o, kk), gf[kk], dp);
+            float cm, ca, x = 0.f;
+            p.prepare(a, j0, vis, s, cm, ca);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                dp[r] = ex2(fmaf(s[r], cm, ca)) * (dp[r] - p.rd);
+                x += dp[r];
             }
-            if (BIAS && !lo_far && !hi_far) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    s[r] = ex2(fmaf(s[r], a.c,
-                                    rl + line[line_index(a, jb + 8 * (r >> 2) + 4 * h + (r & 3) - i - off)]));
-            } else {
-                const float ca = rl + (BIAS ? line[lo_far ? 0 : n_line - 1] : 0.f);
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] = ex2(fmaf(s[r], a.c, ca));
-            }
-            f32x16 ds;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) ds[r] = s[r] * (dp[r] - rd);
-            if (!all) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) ds[r] = flag(vis, r) ? ds[r] : 0.f;
-            }
-            float x = 0.f;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) x += ds[r];
             rest += x;
-            dss.apply(ds, acc);
+            dss.apply(dp, acc);
 #pragma unroll
             for (int rc = 0; rc < 2; ++rc) {
-                const typename E::Frag df = L::pack(ds, rc);
+                const typename E::Frag df = L::pack(dp, rc);
 #pragma unroll
                 for (int cb = 0; cb < ND; ++cb)
-                    acc[cb] = E::mfma(L::frag_cols(kt, 32 * nb + 16 * rc, cb, lane), df, acc[cb]);
+                    acc[cb] = E::mfma(L::frag_cols(now, o + 16 * rc * L::kRow, cb), df, acc[cb]);
             }
         }
-        if (S::kBufs == 1 && j0 + step < len) {
+        if (S::kBufs == 1 && u + 1 < n_tiles) {
             dma_wait();
             wave_fence();
-            fetch(j0 + step, 0);
+            fetch(u + 1, 0);
         }
     }
-
     rest = half_sum(rest);
     const float f = a.scale * dss.undo();
 #pragma unroll
@@ -612,23 +734,12 @@ __global__ __launch_bounds__(256, (Tile<OP, DP>::kRow <= 128 ? 2 : 1)) void attn
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[cb][r] *= f;
     if (ALONE) {
-        if (h == 0) wsum[wid][lane] = rest;
+        if (p.h == 0) wsum[wid][lane] = rest;
         join_waves<DP, ND>(acc, LdsFloats{lds_addr(tiles)}, wid, lane);
         if (wid > 0) return;
         rest = (wsum[0][lane & 31] + wsum[1][lane & 31]) + (wsum[2][lane & 31] + wsum[3][lane & 31]);
     }
-    if (!in) return;
-    if (h == 0 && rl != -INFINITY)
-        a.delta[lrow] = rd + rest - (a.glse ? a.glse[((int64_t)b * a.H + head) * a.n + i] : 0.f);
-    if (!a.gq.p) return;
-    T* o = (T*)a.gq.p + b * a.gq.sb + (int64_t)i * a.gq.sr + head * a.gq.sh;
-#pragma unroll
-    for (int cb = 0; cb < ND; ++cb)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            store4<OP>(o, 32 * cb + 8 * q + 4 * h, a.d, a.gq.vec, row_ok ? acc[cb][4 * q] : 0.f,
-                       row_ok ? acc[cb][4 * q + 1] : 0.f, row_ok ? acc[cb][4 * q + 2] : 0.f,
-                       row_ok ? acc[cb][4 * q + 3] : 0.f);
+    p.store(a, acc, rest);
 }
 
 // dT[bucket, head]: the bucket's positions of every part's line, in 64 bits
@@ -668,35 +779,46 @@ __global__ __launch_bounds__(256) void attn_bias_sum_kernel(const AttnArgs a) {
     if (t == 0) a.gbias[(int64_t)bucket * a.H + head] = (float)red[0];
 }
 
-template <int OP, int DP, bool BIAS, bool ALONE>
+template <int OP, int DP, bool ALONE>
 hipError_t bwd_kv_as(const AttnArgs& a, hipStream_t s) {
-    constexpr int rows = BwdShape<OP, DP, ALONE>::kRows;
-    const int64_t g = (int64_t)a.B * a.K * a.q_split * ((a.m + rows - 1) / rows);
-    const size_t lds = BIAS ? (size_t)5 * (a.r0 + a.rp + 1) * sizeof(float) : 0;
-    attn_bwd_kv_kernel<OP, DP, BIAS, ALONE><<<(unsigned)g, 256, lds, s>>>(a);
+    constexpr int rows = BwdShape<OP, DP, ALONE, 64>::kRows;
+    const unsigned g = (unsigned)((int64_t)a.B * a.K * a.q_split * ((a.m + rows - 1) / rows));
+    const size_t lds = a.bias ? (size_t)5 * (a.r0 + a.rp + 1) * sizeof(float) : 0;
+    constexpr int one = Tile<OP, DP>::kRow <= 256 ? PART_BOTH : PART_DK;
+    if (a.bias)
+        attn_bwd_kv_kernel<OP, DP, true, ALONE, one><<<g, 256, lds, s>>>(a);
+    else
+        attn_bwd_kv_kernel<OP, DP, false, ALONE, one><<<g, 256, lds, s>>>(a);
+    if constexpr (one == PART_DK) {
+        if (a.bias)
+            attn_bwd_kv_kernel<OP, DP, true, ALONE, PART_DV><<<g, 256, lds, s>>>(a);
+        else
+            attn_bwd_kv_kernel<OP, DP, false, ALONE, PART_DV><<<g, 256, lds, s>>>(a);
+    }
     return hipGetLastError();
 }
 template <int OP, int DP>
 hipError_t bwd_kv(const AttnArgs& a, hipStream_t s) {
     if constexpr (Tile<OP, DP>::kRow <= 256)
-        if (a.alone_k)
-            return a.bias ? bwd_kv_as<OP, DP, true, true>(a, s) : bwd_kv_as<OP, DP, false, true>(a, s);
-    return a.bias ? bwd_kv_as<OP, DP, true, false>(a, s) : bwd_kv_as<OP, DP, false, false>(a, s);
+        if (a.alone_k) return bwd_kv_as<OP, DP, true>(a, s);
+    return bwd_kv_as<OP, DP, false>(a, s);
 }
 
-template <int OP, int DP, bool BIAS, bool ALONE>
+template <int OP, int DP, bool ALONE>
 hipError_t bwd_q_as(const AttnArgs& a, hipStream_t s) {
-    constexpr int rows = BwdShape<OP, DP, ALONE>::kRows;
-    const int64_t g = (int64_t)a.B * a.H * ((a.n + rows - 1) / rows);
-    attn_bwd_q_kernel<OP, DP, BIAS, ALONE><<<(unsigned)g, 256, 0, s>>>(a);
+    constexpr int rows = BwdShape<OP, DP, ALONE, 128>::kRows;
+    const unsigned g = (unsigned)((int64_t)a.B * a.H * ((a.n + rows - 1) / rows));
+    if (a.bias)
+        attn_bwd_q_kernel<OP, DP, true, ALONE><<<g, 256, 0, s>>>(a);
+    else
+        attn_bwd_q_kernel<OP, DP, false, ALONE><<<g, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 template <int OP, int DP>
 hipError_t bwd_q(const AttnArgs& a, hipStream_t s) {
     if constexpr (Tile<OP, DP>::kRow <= 256)
-        if (a.alone_q)
-            return a.bias ? bwd_q_as<OP, DP, true, true>(a, s) : bwd_q_as<OP, DP, false, true>(a, s);
-    return a.bias ? bwd_q_as<OP, DP, true, false>(a, s) : bwd_q_as<OP, DP, false, false>(a, s);
+        if (a.alone_q) return bwd_q_as<OP, DP, true>(a, s);
+    return bwd_q_as<OP, DP, false>(a, s);
 }
 
 }  // namespace

@@ -79,90 +79,55 @@ __device__ __forceinline__ void store4(typename El<OP>::T* row, int x0, int d, b
 // scores of one query row: maximum and sum need one exchange, between the
 // halves of the wave, and the weights are operands of O^T = V^T P^T as they
 // are.
-template <int OP, int DP>
-constexpr int kTileKeys = DP * (int)sizeof(typename El<OP>::T) <= 256 ? 64 : 32;
-
+//
+// What the two forms below share: a lane's query row, its range of keys, the
+// scores made ready and the output.
 template <int OP, int DP, bool BIAS>
-__global__ __launch_bounds__(256, DP * sizeof(typename El<OP>::T) <= 256 ? 2 : 1)
-void attn_fwd_kernel(const AttnArgs a) {
+struct FwdPass {
     using E = El<OP>;
     using T = typename E::T;
     using L = Tile<OP, DP>;
-    constexpr int KT = kTileKeys<OP, DP>, NB = KT / 32, ND = DP / 32, NK = DP / 16;
-    using Load = Loader<OP, DP, KT, 256>;
-    __shared__ __attribute__((aligned(256))) char tiles[2][2][KT * L::kRow];
-    __shared__ float line_mem[BIAS ? 2 * kAttnMaxEdge + 1 : 1];
-    const LdsFloats line{lds_addr(line_mem)};
+    static constexpr int ND = DP / 32, NK = DP / 16;
+    int lane, wid, h, split, head, b, kvh, off, i0, i, jb, je;
+    bool row_ok;
+    LdsFloats line;
 
-    const int t = threadIdx.x, lane = t & 63, wid = t >> 6, h = lane >> 5;
-    const int nqb = (a.n + kAttnRows - 1) / kAttnRows;
-    int w = xcd_item(blockIdx.x, gridDim.x);
-    const int qb = w % nqb;
-    w /= nqb;
-    const int split = w % a.n_split;
-    w /= a.n_split;
-    const int head = w % a.H, b = w / a.H, kvh = head / a.G;
-
-    const int off = attn_offset(a, b);
-    const int i0 = qb * kAttnRows + wid * 32, i = i0 + (lane & 31);
-    const bool row_ok = i < attn_q_len(a, b);
-    int len = attn_kv_len(a, b);
-    if (a.causal) len = min(len, max(0, min(qb * kAttnRows + kAttnRows, a.n) + off));
-    const int jb = split * a.split_keys;
-    const int je = a.n_split == 1 ? len : min(len, jb + a.split_keys);
-
-    if (BIAS) load_line(a, head, line, t, 256);
-
-    typename E::Frag qf[NK];
-    load_row_frags<OP, DP>((const T*)a.q.p + b * a.q.sb + (int64_t)i * a.q.sr + head * a.q.sh,
-                           row_ok, a.d, a.q.vec, lane, qf);
-    f32x16 acc[ND];
-#pragma unroll
-    for (int x = 0; x < ND; ++x)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[x][r] = 0.f;
-    Run st;
-
-    const T* kbase = (const T*)a.k.p + b * a.k.sb + kvh * a.k.sh;
-    const T* vbase = (const T*)a.v.p + b * a.v.sb + kvh * a.v.sh;
-    uint64_t next = 0;
-    const auto fetch = [&](int j0, int buf) {
-        next = seen_keys(a, b, je, j0, lane);
-        Load::fill(lds_addr(tiles[buf][0]), kbase + (int64_t)j0 * a.k.sr, a.k.sr, next, a.d, a.k.vec, t);
-        Load::fill(lds_addr(tiles[buf][1]), vbase + (int64_t)j0 * a.v.sr, a.v.sr, next, a.dv, a.v.vec, t);
-    };
-    if (jb < je) fetch(jb, 0);
-    int cur = 0;
-    for (int j0 = jb; j0 < je; j0 += KT, cur ^= 1) {
-        const uint64_t seen = next;
-        // this tile has landed, and no wave reads the other buffer any more
-        dma_wait();
-        __builtin_amdgcn_s_barrier();
-        if (j0 + KT < je) fetch(j0 + KT, cur ^ 1);
-        const uint32_t kt = lds_addr(tiles[cur][0]);
-        const uint32_t vt = lds_addr(tiles[cur][1]);
-        f32x16 s[NB];
+    __device__ __forceinline__ FwdPass(const AttnArgs& a, float* line_mem) {
+        lane = threadIdx.x & 63, wid = wave_id(), h = lane >> 5;
+        const int nqb = (a.n + kAttnRows - 1) / kAttnRows;
+        int w = xcd_item(blockIdx.x, gridDim.x);
+        const int qb = w % nqb;
+        w /= nqb;
+        split = w % a.n_split;
+        w /= a.n_split;
+        head = w % a.H, b = w / a.H, kvh = head / a.G;
+        line.a = lds_addr(line_mem);
+        off = attn_offset(a, b);
+        i0 = qb * kAttnRows + wid * 32, i = i0 + (lane & 31);
+        row_ok = i < attn_q_len(a, b);
+        int len = attn_kv_len(a, b);
+        if (a.causal) len = min(len, max(0, min(qb * kAttnRows + kAttnRows, a.n) + off));
+        jb = split * a.split_keys;
+        je = a.n_split == 1 ? len : min(len, jb + a.split_keys);
+    }
+    // NB blocks of 32 scores from key j0 on, ready for s cm + ca: the bias in,
+    // hidden keys at -inf.
+    template <int NB>
+    __device__ __forceinline__ void prepare(const AttnArgs& a, int j0, uint64_t word, f32x16 (&s)[NB],
+                                            float& cm, float& ca) const {
         uint32_t vis[NB];
         bool all = true;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            vis[nb] = (uint32_t)(seen >> (32 * nb));
+            vis[nb] = (uint32_t)(word >> (32 * nb));
             if (a.causal) vis[nb] &= bits_upto(i + off - (j0 + 32 * nb));
             all = all && vis[nb] == ~0u;
             vis[nb] >>= 4 * h;
         }
         all = __all(all);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) s[nb][r] = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < NK; ++kk)
-                s[nb] = E::mfma(L::frag_rows(kt, 32 * nb, kk, lane), qf[kk], s[nb]);
-        }
-        float cm = a.c, ca = 0.f;
+        cm = a.c, ca = 0.f;
         if (BIAS) {
-            const int lo = j0 - i0 - 31 - off, hi = j0 + KT - 1 - i0 - off;
+            const int lo = j0 - i0 - 31 - off, hi = j0 + 32 * NB - 1 - i0 - off;
             if (hi <= -a.r0) {
                 ca = line[0];
             } else if (lo >= a.rp) {
@@ -179,66 +144,295 @@ void attn_fwd_kernel(const AttnArgs a) {
             }
         }
         if (!all) {
+            asm volatile("");  // a branch: most tiles need none of it
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[nb][r] = flag(vis[nb], r) ? s[nb][r] : -INFINITY;
         }
+    }
+    // Moves the reference up to the scores' maximum where it has to.
+    template <int NB>
+    __device__ __forceinline__ void raise(const f32x16 (&s)[NB], float cm, float ca, Run& st,
+                                          f32x16 (&acc)[ND]) const {
         float mx = -INFINITY;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[nb][r]);
-        mx = half_max(mx);
-        mx = fmaf(mx, cm, ca);
+        mx = fmaf(half_max(mx), cm, ca);
         raise_ref<OP, ND>(st, mx, acc);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            st.sum += weights(s[nb], cm, ca, st);
-#pragma unroll
-            for (int rc = 0; rc < 2; ++rc) {
-                const typename E::Frag pf = L::pack(s[nb], rc);
-#pragma unroll
-                for (int cb = 0; cb < ND; ++cb)
-                    acc[cb] = E::mfma(L::frag_cols(vt, 32 * nb + 16 * rc, cb, lane), pf, acc[cb]);
-            }
-        }
     }
-
-    st.sum = half_sum(st.sum);
-    if (i >= a.n) return;
-    if (!row_ok) st.sum = 0.f;
-    if (a.n_split > 1) {
-        const int64_t row = (int64_t)(b * a.H + head) * a.n + i;
-        const int64_t rows = (int64_t)a.B * a.H * a.n;
-        if (h == 0) a.part_ml[split * rows + row] = make_float2(st.sum == 0.f ? -INFINITY : st.ref, st.sum);
-        float* po = a.part_o + (split * rows + row) * a.dv_pad;
+    __device__ __forceinline__ void store(const AttnArgs& a, Run st, const f32x16 (&acc)[ND]) const {
+        st.sum = half_sum(st.sum);
+        if (i >= a.n) return;
+        if (!row_ok) st.sum = 0.f;
+        if (a.n_split > 1) {
+            const int64_t row = (int64_t)(b * a.H + head) * a.n + i;
+            const int64_t rows = (int64_t)a.B * a.H * a.n;
+            if (h == 0) a.part_ml[split * rows + row] = make_float2(st.sum == 0.f ? -INFINITY : st.ref, st.sum);
+            float* po = a.part_o + (split * rows + row) * a.dv_pad;
+#pragma unroll
+            for (int cb = 0; cb < ND; ++cb)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int x = 32 * cb + 8 * q + 4 * h;
+                    if (x < a.dv)
+                        *(f32x4*)(po + x) = f32x4{acc[cb][4 * q], acc[cb][4 * q + 1], acc[cb][4 * q + 2],
+                                                  acc[cb][4 * q + 3]};
+                }
+            return;
+        }
+        const bool some = !(st.sum == 0.f);
+        const float inv = some ? 1.f / st.sum : 0.f;
+        T* o = (T*)a.o.p + b * a.o.sb + (int64_t)i * a.o.sr + head * a.o.sh;
 #pragma unroll
         for (int cb = 0; cb < ND; ++cb)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int x = 32 * cb + 8 * q + 4 * h;
-                if (x < a.dv)
-                    *(f32x4*)(po + x) = f32x4{acc[cb][4 * q], acc[cb][4 * q + 1], acc[cb][4 * q + 2],
-                                              acc[cb][4 * q + 3]};
+                float y[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) y[r] = some ? acc[cb][4 * q + r] * inv : 0.f;
+                store4<OP>(o, 32 * cb + 8 * q + 4 * h, a.dv, a.o.vec, y[0], y[1], y[2], y[3]);
             }
-        return;
+        if (a.lse && h == 0)
+            a.lse[(int64_t)(b * a.H + head) * a.n + i] =
+                some ? (st.ref + lg2(st.sum)) * kLn2 : -INFINITY;
     }
-    const bool some = !(st.sum == 0.f);
-    const float inv = some ? 1.f / st.sum : 0.f;
-    T* o = (T*)a.o.p + b * a.o.sb + (int64_t)i * a.o.sr + head * a.o.sh;
+};
+
+// Tiles of 128 keys (rows of 128 bytes), worked on 64 at a time, the next tile
+// fetched meanwhile.  Few registers leave two waves a SIMD, and with little
+// work per key one barrier for 128 keys costs less than the pipelining of the
+// form below gains (2048 x 2048, 16 heads of 64, batch 4, with a bias: 116
+// against 132 us).
+template <int OP, int DP, bool BIAS>
+__global__ __launch_bounds__(256, 2) void attn_fwd_narrow_kernel(const AttnArgs a) {
+    using P = FwdPass<OP, DP, BIAS>;
+    using E = typename P::E;
+    using T = typename P::T;
+    using L = typename P::L;
+    constexpr int TK = 128, KT = 64, NB = 2, ND = P::ND, NK = P::NK, kBytes = TK * L::kRow;
+    using Load = Loader<OP, DP, KT, 256>;
+    __shared__ __attribute__((aligned(256))) char tiles[2][2][kBytes];  // keys, values
+    __shared__ uint64_t words[128];
+    __shared__ float line_mem[BIAS ? 2 * kAttnMaxEdge + 1 : 1];
+    const P p(a, line_mem);
+    const int t = threadIdx.x, lane = p.lane;
+    const T* kbase = (const T*)a.k.p + p.b * a.k.sb + p.kvh * a.k.sh;
+    const T* vbase = (const T*)a.v.p + p.b * a.v.sb + p.kvh * a.v.sh;
+    const uint32_t tile0 = lds_addr(tiles);
+    const SeenKeys<KT, 4> seen{a.key_mask ? a.key_mask + p.b * a.mask_stride : nullptr, lds_addr(words),
+                               p.jb, KT, p.je};
+    const auto fetch = [&](int jt, int buf) {
 #pragma unroll
-    for (int cb = 0; cb < ND; ++cb)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float y[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) y[r] = some ? acc[cb][4 * q + r] * inv : 0.f;
-            store4<OP>(o, 32 * cb + 8 * q + 4 * h, a.dv, a.o.vec, y[0], y[1], y[2], y[3]);
+        for (int x = 0; x < 2; ++x) {
+            const int64_t j = jt + x * KT;
+            const uint64_t word = seen((jt - p.jb) / KT + x);
+            const uint32_t lds = tile0 + 2 * buf * kBytes + x * KT * L::kRow;
+            Load::fill(lds, kbase + j * a.k.sr, a.k.sr, word, a.d, a.k.vec, t);
+            Load::fill(lds + kBytes, vbase + j * a.v.sr, a.v.sr, word, a.dv, a.v.vec, t);
         }
-    if (a.lse && h == 0)
-        a.lse[(int64_t)(b * a.H + head) * a.n + i] =
-            some ? (st.ref + lg2(st.sum)) * kLn2 : -INFINITY;
+    };
+    if (p.jb < p.je) {
+        seen.fill(0, lane, p.wid);
+        if (a.key_mask) __syncthreads();
+        fetch(p.jb, 0);
+    }
+    if (BIAS) load_line(a, p.head, p.line, t, 256);
+    typename E::Frag qf[NK];
+    load_row_frags<OP, DP>((const T*)a.q.p + p.b * a.q.sb + (int64_t)p.i * a.q.sr + p.head * a.q.sh,
+                           p.row_ok, a.d, a.q.vec, lane, qf);
+    f32x16 acc[ND];
+#pragma unroll
+    for (int x = 0; x < ND; ++x)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[x][r] = 0.f;
+    Run st;
+    const typename L::Lanes lanes(tile0, lane);
+    int cur = 0;
+    for (int jt = p.jb; jt < p.je; jt += TK) {
+        dma_wait();
+        __builtin_amdgcn_s_barrier();
+        const int u = (jt - p.jb) / KT;
+        if (u % 64 == 0) seen.fill(u + 64, lane, p.wid);
+        const typename L::Lanes now(lanes, cur * 2 * kBytes);
+        cur ^= 1;
+        if (jt + TK < p.je) fetch(jt + TK, cur);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int j0 = jt + x * KT, o = x * KT * L::kRow;
+            f32x16 s[NB];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[nb][r] = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < NK; ++kk)
+                    s[nb] = E::mfma(L::frag_rows(now, o + 32 * nb * L::kRow, kk), qf[kk], s[nb]);
+            }
+            float cm, ca;
+            p.prepare(a, j0, seen(u + x), s, cm, ca);
+            p.raise(s, cm, ca, st, acc);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                st.sum += weights(s[nb], cm, ca, st);
+#pragma unroll
+                for (int rc = 0; rc < 2; ++rc) {
+                    const typename E::Frag pf = L::pack(s[nb], rc);
+#pragma unroll
+                    for (int cb = 0; cb < ND; ++cb)
+                        acc[cb] = E::mfma(L::frag_cols(now, kBytes + o + (32 * nb + 16 * rc) * L::kRow, cb),
+                                          pf, acc[cb]);
+                }
+            }
+        }
+    }
+    p.store(a, st, acc);
+}
+
+// Rows of 256 and 512 bytes: tiles of KT keys, and the steps are pipelined by
+// one: the scores of tile u + 1 are issued to the
+// matrix cores among the exponentials of tile u, so that both units have work
+// of the same wave.  Keys and values stand in rings of R tiles.  At the barrier
+// of step u every wave has formed the scores of u and used the values of u - 1,
+// so the keys of u + R and the values of u + R - 1 are fetched into those
+// places; behind the last tile the fetches go on, of zeros, so that the number
+// of copies in flight is always the same.  (4096 x 8192, 32 heads of 128 over 8,
+// batch 2: 1125 us, 977 TFLOP/s; 1220 with the products' operands loaded where
+// the compiler puts them.)
+template <int OP, int DP>
+constexpr int kStepKeys = Tile<OP, DP>::kRow <= 256 ? 64 : 32;
+
+template <int OP, int DP, bool BIAS>
+__global__ __launch_bounds__(256, (Tile<OP, DP>::kRow <= 256 ? 2 : 1))
+void attn_fwd_kernel(const AttnArgs a) {
+    using P = FwdPass<OP, DP, BIAS>;
+    using E = typename P::E;
+    using T = typename P::T;
+    using L = typename P::L;
+    constexpr int KT = kStepKeys<OP, DP>, NB = KT / 32, ND = P::ND, NK = P::NK;
+    using Load = Loader<OP, DP, KT, 256>;
+    constexpr int R = 2, kTileBytes = KT * L::kRow;
+    __shared__ __attribute__((aligned(256))) char tiles[2 * R][kTileBytes];  // keys, values
+    __shared__ uint64_t words[128];
+    __shared__ float line_mem[BIAS ? 2 * kAttnMaxEdge + 1 : 1];
+    const P p(a, line_mem);
+    const int t = threadIdx.x, lane = p.lane, jb = p.jb, je = p.je;
+    const T* kbase = (const T*)a.k.p + p.b * a.k.sb + p.kvh * a.k.sh;
+    const T* vbase = (const T*)a.v.p + p.b * a.v.sb + p.kvh * a.v.sh;
+    const uint32_t tile0 = lds_addr(tiles);
+    const SeenKeys<KT, 4> seen{a.key_mask ? a.key_mask + p.b * a.mask_stride : nullptr, lds_addr(words),
+                               jb, KT, je};
+    const int n_tiles = jb < je ? (je - jb + KT - 1) / KT : 0;
+    const auto fetch_k = [&](int u, int place) {
+        Load::fill(tile0 + place * kTileBytes, kbase + (jb + (int64_t)u * KT) * a.k.sr, a.k.sr,
+                   seen(u), a.d, a.k.vec, t);
+    };
+    const auto fetch_v = [&](int u, int place) {
+        Load::fill(tile0 + (R + place) * kTileBytes, vbase + (jb + (int64_t)u * KT) * a.v.sr, a.v.sr,
+                   seen(u), a.dv, a.v.vec, t);
+    };
+    if (n_tiles) {
+        seen.fill(0, lane, p.wid);
+        seen.fill(64, lane, p.wid);
+        if (a.key_mask) __syncthreads();
+        fetch_k(0, 0);
+#pragma unroll
+        for (int u = 0; u < R - 1; ++u) {
+            fetch_v(u, u);
+            fetch_k(u + 1, u + 1);
+        }
+    }
+    if (BIAS) load_line(a, p.head, p.line, t, 256);
+    typename E::Frag qf[NK];
+    load_row_frags<OP, DP>((const T*)a.q.p + p.b * a.q.sb + (int64_t)p.i * a.q.sr + p.head * a.q.sh,
+                           p.row_ok, a.d, a.q.vec, lane, qf);
+    f32x16 acc[ND];
+#pragma unroll
+    for (int x = 0; x < ND; ++x)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[x][r] = 0.f;
+    Run st;
+
+    const typename L::Lanes lanes(tile0, lane);
+    // one tile: s its scores, sn those of the next tile; place: its place
+    const auto step = [&](int u, f32x16 (&s)[NB], f32x16 (&sn)[NB], int place) {
+        const int j0 = jb + u * KT;
+        float cm, ca;
+        p.prepare(a, j0, seen(u), s, cm, ca);
+        p.raise(s, cm, ca, st, acc);
+
+        dma_wait_but<(R - 2) * 2 * Load::kN>();
+        __builtin_amdgcn_s_barrier();
+        if (a.key_mask && u % 64 == 0 && u > 0) seen.fill(u + 64, lane, p.wid);
+        fetch_v(u + R - 1, (place + R - 1) % R);
+        fetch_k(u + R, place);
+        // The next tile's scores (behind the last tile: scores that no one
+        // uses), this tile's weights and their products with the values, in an
+        // order that is written out: operands are read kAhead products ahead,
+        // and the sixteen weights of an operand pair are formed between the
+        // products, two at a time, each in time for its own.
+        const int kt = (place + 1) % R * kTileBytes, vt = (R + place) * kTileBytes;
+        constexpr int kAhead = BIAS && DP > 64 ? 2 : 4, kScores = NB * NK, kAll = kScores + 2 * NB * ND, kPairs = 8 * NB;
+        typename E::Frag f[kAhead], pf[2 * NB];
+        const float sub = ca - (st.ref == -INFINITY ? 0.f : st.ref);
+        float part[2] = {0.f, 0.f};
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) sn[nb][r] = 0.f;
+        const auto operand = [&](int x) {
+            if (x < kScores) return L::frag_rows(lanes, kt + 32 * (x % NB) * L::kRow, x / NB);
+            const int y = x - kScores;
+            return L::frag_cols(lanes, vt + 16 * (y / ND) * L::kRow, y % ND);
+        };
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) f[x] = operand(x);
+#pragma unroll
+        for (int x = 0; x < kAll; ++x) {
+            __builtin_amdgcn_sched_barrier(0);
+            const typename E::Frag op = f[x % kAhead];
+            if (x + kAhead < kAll) f[x % kAhead] = operand(x + kAhead);
+            if (x < kScores)
+                sn[x % NB] = E::mfma(op, qf[x / NB], sn[x % NB]);
+            else
+                acc[(x - kScores) % ND] = E::mfma(op, pf[(x - kScores) / ND], acc[(x - kScores) % ND]);
+#pragma unroll
+            for (int y = 0; y < kPairs; ++y)
+                if (y * (kAll - ND) / kPairs == x) {
+                    const int nb = y / 8, r = 2 * (y % 8);
+                    const float u = ex2(fmaf(s[nb][r], cm, sub)), v = ex2(fmaf(s[nb][r + 1], cm, sub));
+                    part[0] += u;
+                    part[1] += v;
+                    pf[y / 4][r % 8] = (T)u;
+                    pf[y / 4][r % 8 + 1] = (T)v;
+                }
+        }
+        st.sum += part[0] + part[1];
+    };
+    if (n_tiles) {
+        f32x16 sa[NB], sb[NB];
+        dma_wait();
+        __syncthreads();
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) sa[nb][r] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < NK; ++kk)
+                sa[nb] = E::mfma(L::frag_rows(lanes, 32 * nb * L::kRow, kk), qf[kk], sa[nb]);
+        }
+        for (int u = 0;;) {
+            step(u, sa, sb, 0);
+            if (++u == n_tiles) break;
+            step(u, sb, sa, 1);
+            if (++u == n_tiles) break;
+        }
+        dma_wait();
+    }
+
+    p.store(a, st, acc);
 }
 
 // ---- few query rows -------------------------------------------------------
@@ -267,8 +461,9 @@ void attn_rows_kernel(const AttnArgs a) {
     static_assert(sizeof(tiles) >= NW * 32 * DP * 4, "the waves' results fit the tiles' memory");
     __shared__ short bucket[BIAS ? 2 * kAttnMaxEdge + 1 : 1];
     __shared__ float wref[NW][32], wsum[NW][32];
+    __shared__ uint64_t words[NW][128];
 
-    const int t = threadIdx.x, lane = t & 63, wid = t >> 6, h = lane >> 5;
+    const int t = threadIdx.x, lane = t & 63, wid = wave_id(), h = lane >> 5;
     const int rows = a.G * a.n;
     const int nrb = (rows + 31) / 32;
     int w = xcd_item(blockIdx.x, gridDim.x);
@@ -288,6 +483,27 @@ void attn_rows_kernel(const AttnArgs a) {
     const int jb = split * a.split_keys;
     const int je = a.n_split == 1 ? len : min(len, jb + a.split_keys);
 
+    const T* kbase = (const T*)a.k.p + b * a.k.sb + kvh * a.k.sh;
+    const T* vbase = (const T*)a.v.p + b * a.v.sb + kvh * a.v.sh;
+    const int j_first = jb + wid * KT;
+    const SeenKeys<KT, 1> keys{a.key_mask ? a.key_mask + b * a.mask_stride : nullptr,
+                               lds_addr(words[wid]), j_first, NW * KT, je};
+    const int n_tiles = j_first < je ? (je - j_first + NW * KT - 1) / (NW * KT) : 0;
+    constexpr int kTileBytes = KT * L::kRow;
+    const uint32_t tile0 = lds_addr(tiles[wid]);
+    const auto fetch = [&](int u, int buf) {
+        const int64_t j0 = j_first + (int64_t)u * NW * KT;
+        const uint64_t seen = keys(u);
+        Load::fill(tile0 + 2 * buf * kTileBytes, kbase + j0 * a.k.sr, a.k.sr, seen, a.d, a.k.vec, lane);
+        Load::fill(tile0 + (2 * buf + 1) * kTileBytes, vbase + j0 * a.v.sr, a.v.sr, seen, a.dv,
+                   a.v.vec, lane);
+    };
+    if (n_tiles) {
+        keys.fill(0, lane, 0);
+        wave_fence();
+        fetch(0, 0);
+    }
+    const typename L::Lanes lanes(tile0, lane);
     float bias_lo = 0.f, bias_hi = 0.f;
     if (BIAS) {
         for (int x = t; x < a.r0 + a.rp + 1; x += 64 * NW) bucket[x] = (short)bucket_of(a, x - a.r0);
@@ -306,29 +522,20 @@ void attn_rows_kernel(const AttnArgs a) {
         for (int r = 0; r < 16; ++r) acc[x][r] = 0.f;
     Run st;
 
-    const T* kbase = (const T*)a.k.p + b * a.k.sb + kvh * a.k.sh;
-    const T* vbase = (const T*)a.v.p + b * a.v.sb + kvh * a.v.sh;
-    uint32_t next = 0;
-    const auto fetch = [&](int j0, int buf) {
-        next = (uint32_t)seen_keys(a, b, je, j0, lane);
-        Load::fill(lds_addr(tiles[wid][buf][0]), kbase + (int64_t)j0 * a.k.sr, a.k.sr, next, a.d, a.k.vec, lane);
-        Load::fill(lds_addr(tiles[wid][buf][1]), vbase + (int64_t)j0 * a.v.sr, a.v.sr, next, a.dv, a.v.vec, lane);
-    };
-    const int j_first = jb + wid * KT;
-    if (j_first < je) fetch(j_first, 0);
     int cur = 0;
-    for (int j0 = j_first; j0 < je; j0 += NW * KT) {
-        const uint32_t seen = next;
+    for (int u = 0; u < n_tiles; ++u) {
+        const int j0 = j_first + u * NW * KT;
+        uint32_t vis = (uint32_t)keys(u);
         // the wave's own buffers: no barrier
         dma_wait();
         wave_fence();
-        const uint32_t kt = lds_addr(tiles[wid][cur][0]);
-        const uint32_t vt = lds_addr(tiles[wid][cur][1]);
+        const typename L::Lanes now(lanes, cur * 2 * kTileBytes);
+        if (u % 64 == 0) keys.fill(u + 64, lane, 0);
+        wave_fence();
         if (NB == 2) {
             cur ^= 1;
-            if (j0 + NW * KT < je) fetch(j0 + NW * KT, cur);
+            if (u + 1 < n_tiles) fetch(u + 1, cur);
         }
-        uint32_t vis = seen;
         if (a.causal) vis &= bits_upto(i + off - j0);
         const bool all = __all(vis == ~0u);
         vis >>= 4 * h;
@@ -336,7 +543,7 @@ void attn_rows_kernel(const AttnArgs a) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[r] = 0.f;
 #pragma unroll
-        for (int kk = 0; kk < NK; ++kk) s = E::mfma(L::frag_rows(kt, 0, kk, lane), qf[kk], s);
+        for (int kk = 0; kk < NK; ++kk) s = E::mfma(L::frag_rows(now, 0, kk), qf[kk], s);
         float cm = a.c, ca = 0.f;
         if (BIAS) {
             const int lo = j0 - (a.n - 1) - off, hi = j0 + KT - 1 - off;
@@ -354,6 +561,7 @@ void attn_rows_kernel(const AttnArgs a) {
             }
         }
         if (!all) {
+            asm volatile("");  // a branch: most tiles need none of it
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = flag(vis, r) ? s[r] : -INFINITY;
         }
@@ -368,12 +576,12 @@ void attn_rows_kernel(const AttnArgs a) {
             const typename E::Frag pf = L::pack(s, rc);
 #pragma unroll
             for (int cb = 0; cb < ND; ++cb)
-                acc[cb] = E::mfma(L::frag_cols(vt, 16 * rc, cb, lane), pf, acc[cb]);
+                acc[cb] = E::mfma(L::frag_cols(now, kTileBytes + 16 * rc * L::kRow, cb), pf, acc[cb]);
         }
-        if (NB == 1 && j0 + NW * KT < je) {
+        if (NB == 1 && u + 1 < n_tiles) {
             dma_wait();
             wave_fence();
-            fetch(j0 + NW * KT, 0);
+            fetch(u + 1, 0);
         }
     }
 
@@ -475,14 +683,20 @@ __global__ __launch_bounds__(256) void attn_merge_kernel(const AttnArgs a) {
     const int head = (int)(bh % a.H), b = (int)(bh / a.H);
     T* o = (T*)a.o.p + b * a.o.sb + (int64_t)i * a.o.sr + head * a.o.sh;
     const float* po = a.part_o + row * a.dv_pad;
+    const int64_t next = rows * a.dv_pad;
     for (int x = 4 * lane; x < a.dv; x += 128) {
         f32x4 y = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-        for (int s = 0; s < a.n_split; ++s) {
-            const f32x4 p = *(const f32x4*)(po + s * rows * a.dv_pad + x);
-            const float f = weight[grp][s];
-            // a range without keys holds nothing
-            y += f == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : p * f;
+        for (int s0 = 0; s0 < a.n_split; s0 += 8) {
+            f32x4 p[8];
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                p[s] = *(const f32x4*)(po + min(s0 + s, a.n_split - 1) * next + x);
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const float f = s0 + s < a.n_split ? weight[grp][s0 + s] : 0.f;
+                // a range without keys holds nothing
+                y += f == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : p[s] * f;
+            }
         }
         y = some ? y * inv : f32x4{0.f, 0.f, 0.f, 0.f};
         store4<OP>(o, x, a.dv, a.o.vec, y[0], y[1], y[2], y[3]);
@@ -501,10 +715,17 @@ hipError_t fwd(const AttnArgs& a, bool few, hipStream_t s) {
             attn_rows_kernel<OP, DP, false><<<(unsigned)g, nt, 0, s>>>(a);
     } else {
         const int64_t g = (int64_t)a.B * a.H * a.n_split * ((a.n + kAttnRows - 1) / kAttnRows);
-        if (a.bias)
-            attn_fwd_kernel<OP, DP, true><<<(unsigned)g, 256, 0, s>>>(a);
-        else
-            attn_fwd_kernel<OP, DP, false><<<(unsigned)g, 256, 0, s>>>(a);
+        if constexpr (Tile<OP, DP>::kRow <= 128) {
+            if (a.bias)
+                attn_fwd_narrow_kernel<OP, DP, true><<<(unsigned)g, 256, 0, s>>>(a);
+            else
+                attn_fwd_narrow_kernel<OP, DP, false><<<(unsigned)g, 256, 0, s>>>(a);
+        } else {
+            if (a.bias)
+                attn_fwd_kernel<OP, DP, true><<<(unsigned)g, 256, 0, s>>>(a);
+            else
+                attn_fwd_kernel<OP, DP, false><<<(unsigned)g, 256, 0, s>>>(a);
+        }
     }
     return hipGetLastError();
 }
