@@ -738,33 +738,34 @@ def fs_bucket_edges(side_buckets: int, max_distance: int) -> list:
     return list(out[:side_buckets - 1])
 
 
-def _on(t: torch.Tensor, name: str, like: torch.Tensor):
+def _on(t: torch.Tensor, name: str, dev: int):
+    """t is a tensor on device number dev (negative: the host)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a device tensor")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, q on {like.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on device {t.get_device()}, not on {dev} as the others")
 
 
-def _rows(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape) -> Rows:
-    """A [batch, rows, heads, width] tensor of q's type as fs_rows."""
+def _rows(t: Optional[torch.Tensor], name: str, like: torch.Tensor, dev: int, shape) -> Rows:
+    """A [batch, rows, heads, width] tensor of like's type as fs_rows."""
     if t is None:
         return _NO_ROWS
-    _on(t, name, like)
+    _on(t, name, dev)
     if t.dtype != like.dtype:
-        raise TypeError(f"{name} is {t.dtype}, q is {like.dtype}")
+        raise TypeError(f"{name} is {t.dtype}, not {like.dtype} as the others")
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)} (is {tuple(t.shape)})")
-    s = t.stride()
-    if s[3] != 1 and shape[3] != 1:
+    b, r, h, w = t.stride()
+    if w != 1 and shape[3] != 1:
         raise ValueError(f"{name}'s last axis must be contiguous")
-    return Rows(t.data_ptr(), s[0], s[1], s[2])
+    return Rows(t.data_ptr(), b, r, h)
 
 
-def _flat(t: Optional[torch.Tensor], name: str, like: torch.Tensor, dtype, shape) -> Optional[int]:
+def _flat(t: Optional[torch.Tensor], name: str, dev: int, dtype, shape) -> Optional[int]:
     """A contiguous tensor of this type and shape, as its address."""
     if t is None:
         return None
-    _on(t, name, like)
+    _on(t, name, dev)
     if t.dtype != dtype or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous {dtype} tensor")
     if t.shape != shape:
@@ -772,55 +773,71 @@ def _flat(t: Optional[torch.Tensor], name: str, like: torch.Tensor, dtype, shape
     return t.data_ptr()
 
 
-def _work(workspace: Optional[torch.Tensor], need: int, like: torch.Tensor, stream):
+def _work(workspace: Optional[torch.Tensor], size, like: torch.Tensor, dev: int, stream):
     """Aligned address and size of the workspace, and the tensor to keep: the
-    caller's, or one of `need` bytes that the stream holds until it is done."""
+    caller's, or one of size() bytes that the stream holds until it is done."""
     if workspace is None:
-        workspace = torch.empty(need + 256, dtype=torch.uint8, device=like.device)
+        workspace = torch.empty(size() + 256, dtype=torch.uint8, device=like.device)
         if stream is not None:
             s = stream if isinstance(stream, torch.cuda.Stream) else \
                 torch.cuda.ExternalStream(int(stream), device=like.device)
             workspace.record_stream(s)
     else:
-        _on(workspace, "workspace", like)
+        _on(workspace, "workspace", dev)
         if not workspace.is_contiguous():
             raise TypeError("workspace must be contiguous")
     base = workspace.data_ptr()
     aligned = (base + 255) // 256 * 256
-    return aligned, max(0, workspace.numel() * workspace.element_size() - (aligned - base)), workspace
+    return aligned, max(0, workspace.nbytes - (aligned - base)), workspace
 
 
-def _run_on(like: torch.Tensor, stream, call):
-    """call(stream handle) with q's device current."""
-    if torch.cuda.current_device() == like.device.index:
-        return call(_stream(stream))
-    with torch.cuda.device(like.device):
-        return call(_stream(stream))
+# the current stream's handle without the objects around it, where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call(fn, where: str, dev: int, stream, *args):
+    """fn(*args, stream handle) with device dev current."""
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, _raw_stream(dev) if stream is None and _raw_stream else _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(stream))
+    return st if st == FS_OK else _check(st, where)
+
+
+def _needed(fn, where: str, *args):
+    need = int(fn(*args))
+    if need == 0:
+        _check(FS_ERR_INVALID_ARG, where)
+    return need
 
 
 def _attention_desc(q, k, v, scale, causal, offset, offsets, q_len, kv_len, key_mask, bias, edges,
-                    two_sided) -> AttentionDesc:
+                    two_sided):
+    """The description, and q's device number."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda:
         raise TypeError("q must be a device tensor")
-    if q.dtype not in _DTYPES:
+    dtype = _DTYPES.get(q.dtype)
+    if dtype is None:
         raise TypeError(f"q must be float32, bfloat16 or float16 (is {q.dtype})")
     if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k and v must be [batch, rows, heads, width]")
+    dev = q.get_device()
     batch, n, heads, d = q.shape
-    m, kv_heads = k.shape[1], k.shape[2]
+    _, m, kv_heads, _ = k.shape
     dv = v.shape[3]
     lens = (batch,)
     i32 = torch.int32
-    a = AttentionDesc(_DTYPES[q.dtype], batch, n, m, heads, kv_heads, d, dv,
-                      scale if scale is not None else d ** -0.5, bool(causal), offset)
+    a = AttentionDesc(dtype, batch, n, m, heads, kv_heads, d, dv,
+                      d ** -0.5 if scale is None else scale, 1 if causal else 0, offset)
     if offsets is not None:
-        a.offsets = _flat(offsets, "offsets", q, i32, lens)
+        a.offsets = _flat(offsets, "offsets", dev, i32, lens)
     if q_len is not None:
-        a.q_len = _flat(q_len, "q_len", q, i32, lens)
+        a.q_len = _flat(q_len, "q_len", dev, i32, lens)
     if kv_len is not None:
-        a.kv_len = _flat(kv_len, "kv_len", q, i32, lens)
+        a.kv_len = _flat(kv_len, "kv_len", dev, i32, lens)
     if key_mask is not None:
-        _on(key_mask, "key_mask", q)
+        _on(key_mask, "key_mask", dev)
         if key_mask.dtype not in (torch.uint8, torch.bool):
             raise TypeError("key_mask must be uint8 or bool")
         if key_mask.shape != (batch, m) or (m > 1 and key_mask.stride(1) != 1):
@@ -830,11 +847,11 @@ def _attention_desc(q, k, v, scale, causal, offset, offsets, q_len, kv_len, key_
     if bias is not None:
         e = [] if edges is None else edges
         buckets = (len(e) + 1) * (2 if two_sided else 1)
-        a.bias = _flat(bias, "bias", q, torch.float32, (buckets, heads))
+        a.bias = _flat(bias, "bias", dev, torch.float32, (buckets, heads))
         a.edges = (ctypes.c_int32 * max(len(e), 1))(*e)
         a.n_edges = len(e)
         a.two_sided = bool(two_sided)
-    return a
+    return a, dev
 
 
 def fs_attention_workspace_bytes(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, edges=None,
@@ -865,21 +882,18 @@ def fs_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: t
     log-sum-exps.  q, o: [batch, n, heads, d or dv]; k, v: [batch, m, kv_heads,
     d or dv]; lse: [batch, heads, n] float32; scale: 1/sqrt(d) unless given."""
     lib = load()
-    a = _attention_desc(q, k, v, scale, causal, offset, offsets, q_len, kv_len, key_mask, bias,
-                        edges, two_sided)
-    need = 0
-    if workspace is None:
-        need = lib.fs_attention_workspace_bytes(ctypes.byref(a), 0)
-        if need == 0:
-            _check(FS_ERR_INVALID_ARG, "fs_attention_forward")
-    ws, size, _keep = _work(workspace, need, q, stream)
-    args = (ctypes.byref(a), _rows(q, "q", q, q.shape),
-            _rows(k, "k", q, (a.batch, a.m, a.kv_heads, a.d)),
-            _rows(v, "v", q, (a.batch, a.m, a.kv_heads, a.dv)),
-            _rows(o, "o", q, (a.batch, a.n, a.heads, a.dv)),
-            _flat(lse, "lse", q, torch.float32, (a.batch, a.heads, a.n)), ws, size)
-    return _check(_run_on(q, stream, lambda s: lib.fs_attention_forward(*args, s)),
-                  "fs_attention_forward")
+    a, dev = _attention_desc(q, k, v, scale, causal, offset, offsets, q_len, kv_len, key_mask, bias,
+                             edges, two_sided)
+    pa = ctypes.byref(a)
+    ws, size, _keep = _work(workspace, lambda: _needed(lib.fs_attention_workspace_bytes,
+                                                       "fs_attention_forward", pa, 0), q, dev, stream)
+    batch, n, heads, _ = q.shape
+    m, kv_heads, dv = a.m, a.kv_heads, a.dv
+    return _call(lib.fs_attention_forward, "fs_attention_forward", dev, stream, pa,
+                 _rows(q, "q", q, dev, q.shape), _rows(k, "k", q, dev, (batch, m, kv_heads, a.d)),
+                 _rows(v, "v", q, dev, (batch, m, kv_heads, dv)),
+                 _rows(o, "o", q, dev, (batch, n, heads, dv)),
+                 _flat(lse, "lse", dev, torch.float32, (batch, heads, n)), ws, size)
 
 
 def fs_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
@@ -893,69 +907,64 @@ def fs_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: 
     optional): writes d_q, d_k, d_v and d_bias, each of its input's shape;
     None: not wanted."""
     lib = load()
-    a = _attention_desc(q, k, v, scale, causal, offset, offsets, q_len, kv_len, key_mask, bias,
-                        edges, two_sided)
-    need = 0
-    if workspace is None:
-        need = lib.fs_attention_workspace_bytes(ctypes.byref(a), 1)
-        if need == 0:
-            _check(FS_ERR_INVALID_ARG, "fs_attention_backward")
-    ws, size, _keep = _work(workspace, need, q, stream)
-    f32, lses = torch.float32, (a.batch, a.heads, a.n)
+    a, dev = _attention_desc(q, k, v, scale, causal, offset, offsets, q_len, kv_len, key_mask, bias,
+                             edges, two_sided)
+    pa = ctypes.byref(a)
+    ws, size, _keep = _work(workspace, lambda: _needed(lib.fs_attention_workspace_bytes,
+                                                       "fs_attention_backward", pa, 1), q, dev, stream)
     if lse is None or o is None or d_o is None:
         raise TypeError("o, lse and d_o must be given")
-    ks, vs = (a.batch, a.m, a.kv_heads, a.d), (a.batch, a.m, a.kv_heads, a.dv)
-    os_ = (a.batch, a.n, a.heads, a.dv)
-    args = (ctypes.byref(a), _rows(q, "q", q, q.shape), _rows(k, "k", q, ks),
-            _rows(v, "v", q, vs), _rows(o, "o", q, os_), _flat(lse, "lse", q, f32, lses),
-            _rows(d_o, "d_o", q, os_), _flat(d_lse, "d_lse", q, f32, lses),
-            _rows(d_q, "d_q", q, q.shape), _rows(d_k, "d_k", q, ks), _rows(d_v, "d_v", q, vs),
-            _flat(d_bias, "d_bias", q, f32, bias.shape if bias is not None else ()), ws, size)
-    return _check(_run_on(q, stream, lambda s: lib.fs_attention_backward(*args, s)),
-                  "fs_attention_backward")
+    f32 = torch.float32
+    batch, n, heads, _ = qs = q.shape
+    ks, vs = (batch, a.m, a.kv_heads, a.d), (batch, a.m, a.kv_heads, a.dv)
+    outs, lses = (batch, n, heads, a.dv), (batch, heads, n)
+    return _call(lib.fs_attention_backward, "fs_attention_backward", dev, stream, pa,
+                 _rows(q, "q", q, dev, qs), _rows(k, "k", q, dev, ks), _rows(v, "v", q, dev, vs),
+                 _rows(o, "o", q, dev, outs), _flat(lse, "lse", dev, f32, lses),
+                 _rows(d_o, "d_o", q, dev, outs), _flat(d_lse, "d_lse", dev, f32, lses),
+                 _rows(d_q, "d_q", q, dev, qs), _rows(d_k, "d_k", q, dev, ks),
+                 _rows(d_v, "d_v", q, dev, vs),
+                 _flat(d_bias, "d_bias", dev, f32, bias.shape if bias is not None else ()), ws, size)
 
 
 def _norm_desc(q, k, eps, cos, sin, positions, offset, interleaved):
+    """The description, the tensor whose type and device count, its device number."""
     like = q if q is not None else k
     if not isinstance(like, torch.Tensor) or not like.is_cuda:
         raise TypeError("q or k must be a device tensor")
-    if like.dtype not in _DTYPES:
+    dtype = _DTYPES.get(like.dtype)
+    if dtype is None:
         raise TypeError(f"q and k must be float32, bfloat16 or float16 (is {like.dtype})")
-    if like.dim() != 4:
+    if like.dim() != 4 or (k is not None and k.dim() != 4):
         raise ValueError("q and k must be [batch, rows, heads, d]")
+    dev = like.get_device()
     batch, n, _, d = like.shape
-    a = QkNormDesc(_DTYPES[like.dtype], batch, n, q.shape[2] if q is not None else 0,
-                   k.shape[2] if k is not None else 0, d, 0, bool(interleaved), eps)
+    a = QkNormDesc(dtype, batch, n, 0 if q is None else q.shape[2], 0 if k is None else k.shape[2],
+                   d, 0, 1 if interleaved else 0, eps)
     if (cos is None) != (sin is None):
         raise TypeError("cos and sin must both be given or both be None")
     if cos is not None:
         if cos.dim() != 2:
             raise ValueError("cos and sin must be [positions, rot / 2]")
-        a.rot, a.n_pos = 2 * cos.shape[1], cos.shape[0]
-        a.cos_table = _flat(cos, "cos", like, torch.float32, cos.shape)
-        a.sin_table = _flat(sin, "sin", like, torch.float32, cos.shape)
+        table = cos.shape
+        a.rot, a.n_pos = 2 * table[1], table[0]
+        a.cos_table = _flat(cos, "cos", dev, torch.float32, table)
+        a.sin_table = _flat(sin, "sin", dev, torch.float32, table)
     if positions is not None:
-        _on(positions, "positions", like)
+        _on(positions, "positions", dev)
         if positions.dtype != torch.int32 or positions.shape != (batch, n) or \
                 (n > 1 and positions.stride(1) != 1):
             raise TypeError(f"positions must be int32 ({batch}, {n}) with a contiguous last axis")
         a.positions = positions.data_ptr()
         a.positions_stride = positions.stride(0) if batch > 1 else 0
     a.offset = offset
-    return a, like
-
-
-def _norm_shapes(a):
-    return (a.batch, a.n, a.heads_q, a.d), (a.batch, a.n, a.heads_k, a.d)
+    return a, like, dev
 
 
 def fs_qk_norm_workspace_bytes(q, k) -> int:
     """Bytes of workspace of fs_qk_norm_rotate_backward on tensors of these shapes."""
-    a, _ = _norm_desc(q, k, 0.0, None, None, None, 0, False)
-    need = int(load().fs_qk_norm_workspace_bytes(ctypes.byref(a)))
-    if need == 0:
-        _check(FS_ERR_INVALID_ARG, "fs_qk_norm_workspace_bytes")
-    return need
+    a, _, _ = _norm_desc(q, k, 0.0, None, None, None, 0, False)
+    return _needed(load().fs_qk_norm_workspace_bytes, "fs_qk_norm_workspace_bytes", ctypes.byref(a))
 
 
 def fs_qk_norm_rotate(q, k, q_weight, k_weight, q_out, k_out, *, eps: float = 1e-6, cos=None,
@@ -965,14 +974,14 @@ def fs_qk_norm_rotate(q, k, q_weight, k_weight, q_out, k_out, *, eps: float = 1e
     None) times its weight, and the rotation of the first 2 * cos.shape[1]
     elements by the position's row of cos and sin ([positions, rot / 2])."""
     lib = load()
-    a, like = _norm_desc(q, k, eps, cos, sin, positions, offset, interleaved)
-    qs, ks = _norm_shapes(a)
-    f32, w = torch.float32, (a.d,)
-    args = (ctypes.byref(a), _rows(q, "q", like, qs), _rows(k, "k", like, ks),
-            _flat(q_weight, "q_weight", like, f32, w), _flat(k_weight, "k_weight", like, f32, w),
-            _rows(q_out, "q_out", like, qs), _rows(k_out, "k_out", like, ks))
-    return _check(_run_on(like, stream, lambda s: lib.fs_qk_norm_rotate(*args, s)),
-                  "fs_qk_norm_rotate")
+    a, like, dev = _norm_desc(q, k, eps, cos, sin, positions, offset, interleaved)
+    batch, n, _, d = like.shape
+    qs, ks = (batch, n, a.heads_q, d), (batch, n, a.heads_k, d)
+    f32, w = torch.float32, (d,)
+    return _call(lib.fs_qk_norm_rotate, "fs_qk_norm_rotate", dev, stream, ctypes.byref(a),
+                 _rows(q, "q", like, dev, qs), _rows(k, "k", like, dev, ks),
+                 _flat(q_weight, "q_weight", dev, f32, w), _flat(k_weight, "k_weight", dev, f32, w),
+                 _rows(q_out, "q_out", like, dev, qs), _rows(k_out, "k_out", like, dev, ks))
 
 
 def fs_qk_norm_rotate_backward(q, k, q_weight, k_weight, d_q_out, d_k_out, d_q, d_k,
@@ -983,20 +992,18 @@ def fs_qk_norm_rotate_backward(q, k, q_weight, k_weight, d_q_out, d_k_out, d_q, 
     """Gradients of fs_qk_norm_rotate: writes d_q, d_k and, where given, the
     weights' gradients."""
     lib = load()
-    a, like = _norm_desc(q, k, eps, cos, sin, positions, offset, interleaved)
-    need = 0
-    if workspace is None:
-        need = lib.fs_qk_norm_workspace_bytes(ctypes.byref(a))
-        if need == 0:
-            _check(FS_ERR_INVALID_ARG, "fs_qk_norm_rotate_backward")
-    ws, size, _keep = _work(workspace, need, like, stream)
-    qs, ks = _norm_shapes(a)
-    f32, w = torch.float32, (a.d,)
-    args = (ctypes.byref(a), _rows(q, "q", like, qs), _rows(k, "k", like, ks),
-            _flat(q_weight, "q_weight", like, f32, w), _flat(k_weight, "k_weight", like, f32, w),
-            _rows(d_q_out, "d_q_out", like, qs), _rows(d_k_out, "d_k_out", like, ks),
-            _rows(d_q, "d_q", like, qs), _rows(d_k, "d_k", like, ks),
-            _flat(d_q_weight, "d_q_weight", like, f32, w),
-            _flat(d_k_weight, "d_k_weight", like, f32, w), ws, size)
-    return _check(_run_on(like, stream, lambda s: lib.fs_qk_norm_rotate_backward(*args, s)),
-                  "fs_qk_norm_rotate_backward")
+    a, like, dev = _norm_desc(q, k, eps, cos, sin, positions, offset, interleaved)
+    pa = ctypes.byref(a)
+    ws, size, _keep = _work(workspace, lambda: _needed(lib.fs_qk_norm_workspace_bytes,
+                                                       "fs_qk_norm_rotate_backward", pa), like, dev,
+                            stream)
+    batch, n, _, d = like.shape
+    qs, ks = (batch, n, a.heads_q, d), (batch, n, a.heads_k, d)
+    f32, w = torch.float32, (d,)
+    return _call(lib.fs_qk_norm_rotate_backward, "fs_qk_norm_rotate_backward", dev, stream, pa,
+                 _rows(q, "q", like, dev, qs), _rows(k, "k", like, dev, ks),
+                 _flat(q_weight, "q_weight", dev, f32, w), _flat(k_weight, "k_weight", dev, f32, w),
+                 _rows(d_q_out, "d_q_out", like, dev, qs), _rows(d_k_out, "d_k_out", like, dev, ks),
+                 _rows(d_q, "d_q", like, dev, qs), _rows(d_k, "d_k", like, dev, ks),
+                 _flat(d_q_weight, "d_q_weight", dev, f32, w),
+                 _flat(d_k_weight, "d_k_weight", dev, f32, w), ws, size)

@@ -195,6 +195,40 @@ struct Tile {
     }
 };
 
+// Two runs of products whose operands come from LDS, with vector work between
+// them.  Operands are read A products ahead, across the gap (the order is
+// pinned: left to itself the compiler reads each operand right before its
+// product and waits out the latency of LDS every time).
+template <int A, int N1, int N2, typename Frag, typename Operand>
+struct Products {
+    Frag f[A];
+    Operand operand;
+    __device__ __forceinline__ Products(Operand o) : operand(o) {
+#pragma unroll
+        for (int x = 0; x < A; ++x)
+            if (x < N1 + N2) f[x] = operand(x);
+    }
+    template <int FROM, int TO, typename Product>
+    __device__ __forceinline__ void run(Product product) {
+#pragma unroll
+        for (int x = FROM; x < TO; ++x) {
+            __builtin_amdgcn_sched_barrier(0);
+            const Frag op = f[x % A];
+            if (x + A < N1 + N2) f[x % A] = operand(x + A);
+            product(x - FROM, op);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    template <typename Product>
+    __device__ __forceinline__ void first(Product product) { run<0, N1>(product); }
+    template <typename Product>
+    __device__ __forceinline__ void second(Product product) { run<N1, N1 + N2>(product); }
+};
+template <int A, int N1, int N2, typename Frag, typename Operand>
+__device__ __forceinline__ Products<A, N1, N2, Frag, Operand> products(Operand o) {
+    return Products<A, N1, N2, Frag, Operand>(o);
+}
+
 // Eight elements of a row in global memory from element x0 on, zero behind
 // width d.  vec: the row is 16-byte aligned and d a multiple of a chunk.
 template <int OP, int N>
@@ -417,11 +451,16 @@ __device__ __forceinline__ void load_line(const AttnArgs& a, int head, LdsFloats
         line.set(i, bias2(a.bias[(int64_t)bucket_of(a, i - a.r0) * a.H + head]));
 }
 
-// Work item of a 1-D grid, consecutive ones on the same XCD: workgroups go to
-// the 8 XCDs round-robin, and those that read the same keys then share an L2.
-__device__ __forceinline__ int xcd_item(int id, int total) {
-    const int x = id & 7, q = total >> 3, r = total & 7;
-    return x * q + min(x, r) + (id >> 3);
+// Work item of a 1-D grid whose items come in groups of `group` that read the
+// same keys.  Workgroups go to the 8 XCDs round-robin and each XCD has its own
+// L2, so a group's items are given to one XCD, and the groups to the XCDs in
+// turn (sequences of unequal length then spread over them); where the groups
+// are not a multiple of 8, each XCD takes an equal run of items instead.
+__device__ __forceinline__ int xcd_item(int id, int total, int group) {
+    const int x = id & 7, k = id >> 3;
+    if (total / group % 8 == 0) return (k / group * 8 + x) * group + k % group;
+    const int q = total >> 3, r = total & 7;
+    return x * q + min(x, r) + k;
 }
 
 }  // namespace fs

@@ -203,6 +203,7 @@ fs_status take_desc(const fs_attention_desc* p, AttnArgs& a) {
     if (items > 0 && d.m > 0) {
         int64_t s = cdiv(kCus, items);
         if (few) s = std::max(s, cdiv(d.m, 32 * turn));
+        if (few && d.m <= 2 * turn) s = 1;  // the second launch costs more than two tiles
         s = std::max<int64_t>(1, std::min({s, (int64_t)kAttnMaxSplit, d.m / turn}));
         a.split_keys = (int)(cdiv(cdiv(d.m, s), turn) * turn);
         a.n_split = (int)cdiv(d.m, a.split_keys);

@@ -128,6 +128,7 @@ struct DsScale {
 // within a wave (the products of the next 32 rows among the exponentials of
 // these): those need registers that cost the second wave, and were 6 to 25%
 // slower.
+constexpr int kAhead = 4;  // products ahead of which operands are read
 template <int OP, int DP, bool ALONE, int MOST>
 struct BwdShape {
     static constexpr int kRow = Tile<OP, DP>::kRow;
@@ -200,7 +201,7 @@ struct KvPass {
         const int t = threadIdx.x;
         lane = t & 63, wid = wave_id(), h = lane >> 5;
         const int nkb = (a.m + ROWS - 1) / ROWS;
-        int w = xcd_item(blockIdx.x, gridDim.x);
+        int w = xcd_item(blockIdx.x, gridDim.x, a.q_split * nkb);
         kb = w % nkb;
         w /= nkb;
         split = w % a.q_split;
@@ -443,13 +444,22 @@ void attn_bwd_kv_kernel(const AttnArgs a) {
                 f32x16 s, dp;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.f;
-#pragma unroll
-                for (int kk = 0; kk < NK; ++kk) s = E::mfma(L::frag_rows(now, o, kk), kf[kk], s);
-                if (DK) {
-#pragma unroll
-                    for (int kk = 0; kk < NK; ++kk)
-                        dp = E::mfma(L::frag_rows(now, kBytes + o, kk), vf[kk], dp);
-                }
+                // q and do rows in turn, then their columns (rc, cb; dV, dK)
+                constexpr int kFirst = DK ? 2 * NK : NK, kSecond = DK && DV ? 4 * ND : 2 * ND;
+                auto prod = products<kAhead, kFirst, kSecond, typename E::Frag>([&](int y) {
+                    if (y < kFirst)
+                        return DK ? L::frag_rows(now, y % 2 * kBytes + o, y / 2) : L::frag_rows(now, o, y);
+                    y -= kFirst;
+                    const int of = DK && DV ? (y % 2 ? 0 : kBytes) : DK ? 0 : kBytes;
+                    if (DK && DV) y /= 2;
+                    return L::frag_cols(now, of + o + 16 * (y / ND) * L::kRow, y % ND);
+                });
+                prod.first([&](int y, typename E::Frag op) {
+                    if (DK && y % 2)
+                        dp = E::mfma(op, vf[y / 2], dp);
+                    else
+                        s = E::mfma(op, kf[DK ? y / 2 : y], s);
+                });
                 float rl[16], rd[16];
                 bool lo_far, hi_far;
                 p.row_terms(a, i0, term + 256 * qb, rl, rd, lo_far, hi_far);
@@ -464,15 +474,16 @@ void attn_bwd_kv_kernel(const AttnArgs a) {
                     p.add_bias(a, i0, dp, lo_far, hi_far);
                     dss.apply(dp, dk);
                 }
-#pragma unroll
-                for (int rc = 0; rc < 2; ++rc) {
-                    const typename E::Frag pf = L::pack(s, rc), df = L::pack(dp, rc);
-#pragma unroll
-                    for (int cb = 0; cb < ND; ++cb) {
-                        if (DV) dv[cb] = E::mfma(L::frag_cols(now, kBytes + o + 16 * rc * L::kRow, cb), pf, dv[cb]);
-                        if (DK) dk[cb] = E::mfma(L::frag_cols(now, o + 16 * rc * L::kRow, cb), df, dk[cb]);
-                    }
-                }
+                const typename E::Frag pf[2] = {L::pack(s, 0), L::pack(s, 1)};
+                const typename E::Frag df[2] = {L::pack(dp, 0), L::pack(dp, 1)};
+                prod.second([&](int y, typename E::Frag op) {
+                    const bool k = DK && (!DV || y % 2);
+                    if (DK && DV) y /= 2;
+                    if (k)
+                        dk[y % ND] = E::mfma(op, df[y / ND], dk[y % ND]);
+                    else
+                        dv[y % ND] = E::mfma(op, pf[y / ND], dv[y % ND]);
+                });
             }
             if (S::kBufs == 1 && u + step < n_all) {
                 dma_wait();
@@ -557,7 +568,7 @@ struct QPass {
         const int t = threadIdx.x;
         lane = t & 63, wid = wave_id(), h = lane >> 5;
         const int nqb = (a.n + ROWS - 1) / ROWS;
-        int w = xcd_item(blockIdx.x, gridDim.x);
+        int w = xcd_item(blockIdx.x, gridDim.x, a.G * nqb);
         const int qb = w % nqb;
         w /= nqb;
         head = w % a.H, b = w / a.H, kvh = head / a.G;
@@ -700,10 +711,17 @@ void attn_bwd_q_kernel(const AttnArgs a) {
             f32x16 s, dp;
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < NK; ++kk) s = E::mfma(L::frag_rows(now, o, kk), qf[kk], s);
-#pragma unroll
-            for (int kk = 0; kk < NK; ++kk) dp = E::mfma(L::frag_rows(now, kBytes + o, kk), gf[kk], dp);
+            auto prod = products<kAhead, 2 * NK, 2 * ND, typename E::Frag>([&](int y) {
+                if (y < 2 * NK) return L::frag_rows(now, y % 2 * kBytes + o, y / 2);
+                y -= 2 * NK;
+                return L::frag_cols(now, o + 16 * (y / ND) * L::kRow, y % ND);
+            });
+            prod.first([&](int y, typename E::Frag op) {
+                if (y % 2)
+                    dp = E::mfma(op, gf[y / 2], dp);
+                else
+                    s = E::mfma(op, qf[y / 2], s);
+            });
             float cm, ca, x = 0.f;
             p.prepare(a, j0, vis, s, cm, ca);
 #pragma unroll
@@ -713,13 +731,8 @@ void attn_bwd_q_kernel(const AttnArgs a) {
             }
             rest += x;
             dss.apply(dp, acc);
-#pragma unroll
-            for (int rc = 0; rc < 2; ++rc) {
-                const typename E::Frag df = L::pack(dp, rc);
-#pragma unroll
-                for (int cb = 0; cb < ND; ++cb)
-                    acc[cb] = E::mfma(L::frag_cols(now, o + 16 * rc * L::kRow, cb), df, acc[cb]);
-            }
+            const typename E::Frag df[2] = {L::pack(dp, 0), L::pack(dp, 1)};
+            prod.second([&](int y, typename E::Frag op) { acc[y % ND] = E::mfma(op, df[y / ND], acc[y % ND]); });
         }
         if (S::kBufs == 1 && u + 1 < n_tiles) {
             dma_wait();

@@ -95,7 +95,7 @@ struct FwdPass {
     __device__ __forceinline__ FwdPass(const AttnArgs& a, float* line_mem) {
         lane = threadIdx.x & 63, wid = wave_id(), h = lane >> 5;
         const int nqb = (a.n + kAttnRows - 1) / kAttnRows;
-        int w = xcd_item(blockIdx.x, gridDim.x);
+        int w = xcd_item(blockIdx.x, gridDim.x, a.G * a.n_split * nqb);
         const int qb = w % nqb;
         w /= nqb;
         split = w % a.n_split;
@@ -206,6 +206,7 @@ struct FwdPass {
 // work per key one barrier for 128 keys costs less than the pipelining of the
 // form below gains (2048 x 2048, 16 heads of 64, batch 4, with a bias: 116
 // against 132 us).
+constexpr int kNarrowAhead = 8;
 template <int OP, int DP, bool BIAS>
 __global__ __launch_bounds__(256, 2) void attn_fwd_narrow_kernel(const AttnArgs a) {
     using P = FwdPass<OP, DP, BIAS>;
@@ -264,28 +265,27 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_narrow_kernel(const AttnArgs 
             const int j0 = jt + x * KT, o = x * KT * L::kRow;
             f32x16 s[NB];
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[nb][r] = 0.f;
-#pragma unroll
-                for (int kk = 0; kk < NK; ++kk)
-                    s[nb] = E::mfma(L::frag_rows(now, o + 32 * nb * L::kRow, kk), qf[kk], s[nb]);
-            }
+            constexpr int kScores = NB * NK, kValues = 2 * NB * ND;
+            auto prod = products<kNarrowAhead, kScores, kValues, typename E::Frag>([&](int y) {
+                if (y < kScores) return L::frag_rows(now, o + 32 * (y % NB) * L::kRow, y / NB);
+                y -= kScores;
+                return L::frag_cols(now, kBytes + o + 16 * (y / ND) * L::kRow, y % ND);
+            });
+            prod.first([&](int y, typename E::Frag op) { s[y % NB] = E::mfma(op, qf[y / NB], s[y % NB]); });
             float cm, ca;
             p.prepare(a, j0, seen(u + x), s, cm, ca);
             p.raise(s, cm, ca, st, acc);
+            typename E::Frag pf[2 * NB];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 st.sum += weights(s[nb], cm, ca, st);
-#pragma unroll
-                for (int rc = 0; rc < 2; ++rc) {
-                    const typename E::Frag pf = L::pack(s[nb], rc);
-#pragma unroll
-                    for (int cb = 0; cb < ND; ++cb)
-                        acc[cb] = E::mfma(L::frag_cols(now, kBytes + o + (32 * nb + 16 * rc) * L::kRow, cb),
-                                          pf, acc[cb]);
-                }
+                pf[2 * nb] = L::pack(s[nb], 0);
+                pf[2 * nb + 1] = L::pack(s[nb], 1);
             }
+            prod.second([&](int y, typename E::Frag op) { acc[y % ND] = E::mfma(op, pf[y / ND], acc[y % ND]); });
         }
     }
     p.store(a, st, acc);
@@ -466,7 +466,7 @@ void attn_rows_kernel(const AttnArgs a) {
     const int t = threadIdx.x, lane = t & 63, wid = wave_id(), h = lane >> 5;
     const int rows = a.G * a.n;
     const int nrb = (rows + 31) / 32;
-    int w = xcd_item(blockIdx.x, gridDim.x);
+    int w = xcd_item(blockIdx.x, gridDim.x, a.n_split * nrb);
     const int rb = w % nrb;
     w /= nrb;
     const int split = w % a.n_split;
@@ -542,8 +542,12 @@ void attn_rows_kernel(const AttnArgs a) {
         f32x16 s;
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[r] = 0.f;
-#pragma unroll
-        for (int kk = 0; kk < NK; ++kk) s = E::mfma(L::frag_rows(now, 0, kk), qf[kk], s);
+        auto prod = products<4, NK, 2 * ND, typename E::Frag>([&](int y) {
+            if (y < NK) return L::frag_rows(now, 0, y);
+            y -= NK;
+            return L::frag_cols(now, kTileBytes + 16 * (y / ND) * L::kRow, y % ND);
+        });
+        prod.first([&](int y, typename E::Frag op) { s = E::mfma(op, qf[y], s); });
         float cm = a.c, ca = 0.f;
         if (BIAS) {
             const int lo = j0 - (a.n - 1) - off, hi = j0 + KT - 1 - off;
@@ -571,13 +575,8 @@ void attn_rows_kernel(const AttnArgs a) {
         mx = fmaf(half_max(mx), cm, ca);
         raise_ref<OP, ND>(st, mx, acc);
         st.sum += weights(s, cm, ca, st);
-#pragma unroll
-        for (int rc = 0; rc < 2; ++rc) {
-            const typename E::Frag pf = L::pack(s, rc);
-#pragma unroll
-            for (int cb = 0; cb < ND; ++cb)
-                acc[cb] = E::mfma(L::frag_cols(now, kTileBytes + 16 * rc * L::kRow, cb), pf, acc[cb]);
-        }
+        const typename E::Frag pf[2] = {L::pack(s, 0), L::pack(s, 1)};
+        prod.second([&](int y, typename E::Frag op) { acc[y % ND] = E::mfma(op, pf[y / ND], acc[y % ND]); });
         if (NB == 1 && u + 1 < n_tiles) {
             dma_wait();
             wave_fence();

@@ -112,92 +112,129 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
-template <int OP, int LPR>
+// A wave takes U rows a lane group, heads h0, h0 + 64 / LPR, ... of one token:
+// the angles, the weights and the token's place are formed once, and U rows'
+// loads are in flight together.
+template <int LPR, int U>
+struct NormItem {
+    static constexpr int kGroups = 64 / LPR, kHeads = kGroups * U;
+    int b, i, h0;
+    bool any;
+    __device__ __forceinline__ NormItem(const NormArgs& a, int heads, uint32_t item) {
+        const uint32_t per = (uint32_t)(heads + kHeads - 1) / kHeads;  // items of a token
+        const uint32_t tok = item / per;
+        any = tok < (uint32_t)a.B * a.n;
+        b = (int)(tok / a.n), i = (int)(tok - b * (uint32_t)a.n);
+        h0 = (int)(item - tok * per) * kHeads + (threadIdx.x & 63) / LPR;
+    }
+};
+
+template <int OP, int LPR, int U>
 __global__ __launch_bounds__(256) void norm_rotate_kernel(const NormArgs a) {
     using T = typename El<OP>::T;
+    using Item = NormItem<LPR, U>;
     const NormRows& R = a.r[blockIdx.y];
-    const uint32_t rows = (uint32_t)a.B * a.n * R.heads;
-    const uint32_t r = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+    if (R.heads == 0) return;
+    const Item it(a, R.heads, blockIdx.x * 4 + wave_id());
+    if (!it.any) return;
     const int p0 = 4 * (threadIdx.x % LPR);
-    if (r >= rows) return;
-    const uint32_t tok = r / R.heads;
-    const int head = (int)(r - tok * R.heads), b = (int)(tok / a.n), i = (int)(tok - b * (uint32_t)a.n);
     const bool wide = R.x.vec && R.y.vec && a.rot % 8 == 0 && a.d % 8 == 0;
     const bool in = p0 < a.d / 2;
-    const T* x = (const T*)R.x.p + b * R.x.sb + (int64_t)i * R.x.sr + head * R.x.sh;
-    float u[4] = {0, 0, 0, 0}, v[4] = {0, 0, 0, 0};
-    if (in) load_pairs(a, x, p0, wide, u, v);
-    float c[4], s[4], wu[4], wv[4];
-    load_angles(a, b, i, p0, c, s);
-    load_weights(a, R.w, p0, wu, wv);
-    float q = 0.f;
+    const T* x = (const T*)R.x.p + it.b * R.x.sb + (int64_t)it.i * R.x.sr;
+    float u[U][4], v[U][4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) q = fmaf(u[k], u[k], fmaf(v[k], v[k], q));
-    q = row_sum<LPR>(q);
-    const float inv = 1.f / sqrtf(q / (float)a.d + a.eps);
-    if (!in) return;
+    for (int k = 0; k < U; ++k) {
+        const int head = it.h0 + k * Item::kGroups;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float zu = u[k] * inv * wu[k], zv = v[k] * inv * wv[k];
-        u[k] = fmaf(zu, c[k], -zv * s[k]);
-        v[k] = fmaf(zv, c[k], zu * s[k]);
+        for (int e = 0; e < 4; ++e) u[k][e] = v[k][e] = 0.f;
+        if (in && head < R.heads) load_pairs(a, x + head * R.x.sh, p0, wide, u[k], v[k]);
     }
-    store_pairs(a, (T*)R.y.p + b * R.y.sb + (int64_t)i * R.y.sr + head * R.y.sh, p0, wide, u, v);
+    float c[4], s[4], wu[4], wv[4];
+    load_angles(a, it.b, it.i, p0, c, s);
+    load_weights(a, R.w, p0, wu, wv);
+    T* y = (T*)R.y.p + it.b * R.y.sb + (int64_t)it.i * R.y.sr;
+    const float dinv = 1.f / (float)a.d;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        float q = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q = fmaf(u[k][e], u[k][e], fmaf(v[k][e], v[k][e], q));
+        q = row_sum<LPR>(q);
+        const float inv = 1.f / sqrtf(fmaf(q, dinv, a.eps));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float zu = u[k][e] * inv * wu[e], zv = v[k][e] * inv * wv[e];
+            u[k][e] = fmaf(zu, c[e], -zv * s[e]);
+            v[k][e] = fmaf(zv, c[e], zu * s[e]);
+        }
+        const int head = it.h0 + k * Item::kGroups;
+        if (in && head < R.heads) store_pairs(a, y + head * R.y.sh, p0, wide, u[k], v[k]);
+    }
 }
 
-// Backward: a workgroup takes rows blockIdx.x, + gridDim.x, ... in groups of
-// 256 / LPR; a lane's pairs are the same in every row, so the weights'
-// gradient is summed in registers, over the workgroup in LDS and over
-// workgroups by norm_weight_kernel, in a fixed order.
-template <int OP, int LPR>
+// Backward: a workgroup takes items blockIdx.x * 4 + wave, in steps of the grid;
+// a lane's pairs are the same in every row, so the weights' gradient is summed
+// in registers, over the workgroup in LDS and over workgroups by
+// norm_weight_kernel, in a fixed order.
+template <int OP, int LPR, int U>
 __global__ __launch_bounds__(256) void norm_rotate_bwd_kernel(const NormArgs a) {
     using T = typename El<OP>::T;
-    constexpr int RPB = 256 / LPR;
-    __shared__ float red[RPB][8 * LPR];
+    using Item = NormItem<LPR, U>;
+    constexpr int GRP = 256 / LPR;
+    __shared__ float red[GRP][8 * LPR];
     const NormRows& R = a.r[blockIdx.y];
-    const uint32_t rows = (uint32_t)a.B * a.n * R.heads;
+    if (R.heads == 0) return;
     const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR, p0 = 4 * lane;
     const bool wide = R.x.vec && R.y.vec && R.g.vec && a.rot % 8 == 0 && a.d % 8 == 0;
     const bool in = p0 < a.d / 2;
     float wu[4], wv[4], du[4] = {0, 0, 0, 0}, dv[4] = {0, 0, 0, 0};
     load_weights(a, R.w, p0, wu, wv);
     const float dinv = 1.f / (float)a.d;
-    for (uint32_t r = blockIdx.x * RPB + grp; r < rows; r += gridDim.x * RPB) {
-        const uint32_t tok = r / R.heads;
-        const int head = (int)(r - tok * R.heads), b = (int)(tok / a.n),
-                  i = (int)(tok - b * (uint32_t)a.n);
-        const T* x = (const T*)R.x.p + b * R.x.sb + (int64_t)i * R.x.sr + head * R.x.sh;
-        const T* g = (const T*)R.g.p + b * R.g.sb + (int64_t)i * R.g.sr + head * R.g.sh;
-        float u[4] = {0, 0, 0, 0}, v[4] = {0, 0, 0, 0}, gu[4] = {0, 0, 0, 0}, gv[4] = {0, 0, 0, 0};
-        if (in) {
-            load_pairs(a, x, p0, wide, u, v);
-            load_pairs(a, g, p0, wide, gu, gv);
+    for (uint32_t item = blockIdx.x * 4 + wave_id();; item += gridDim.x * 4) {
+        const Item it(a, R.heads, item);
+        if (!it.any) break;
+        const T* x = (const T*)R.x.p + it.b * R.x.sb + (int64_t)it.i * R.x.sr;
+        const T* g = (const T*)R.g.p + it.b * R.g.sb + (int64_t)it.i * R.g.sr;
+        T* y = (T*)R.y.p + it.b * R.y.sb + (int64_t)it.i * R.y.sr;
+        float u[U][4], v[U][4], gu[U][4], gv[U][4];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int head = it.h0 + k * Item::kGroups;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[k][e] = v[k][e] = gu[k][e] = gv[k][e] = 0.f;
+            if (in && head < R.heads) {
+                load_pairs(a, x + head * R.x.sh, p0, wide, u[k], v[k]);
+                load_pairs(a, g + head * R.g.sh, p0, wide, gu[k], gv[k]);
+            }
         }
         float c[4], s[4];
-        load_angles(a, b, i, p0, c, s);
-        float q = 0.f, m = 0.f;
+        load_angles(a, it.b, it.i, p0, c, s);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float tu = fmaf(gu[k], c[k], gv[k] * s[k]), tv = fmaf(gv[k], c[k], -gu[k] * s[k]);
-            gu[k] = tu;
-            gv[k] = tv;
-            q = fmaf(u[k], u[k], fmaf(v[k], v[k], q));
-            m = fmaf(u[k] * wu[k], tu, fmaf(v[k] * wv[k], tv, m));
-        }
-        q = row_sum<LPR>(q);
-        m = row_sum<LPR>(m);
-        const float inv = 1.f / sqrtf(q * dinv + a.eps);
-        const float k2 = inv * inv * m * dinv;
+        for (int k = 0; k < U; ++k) {
+            float q = 0.f, m = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            du[k] = fmaf(u[k] * inv, gu[k], du[k]);
-            dv[k] = fmaf(v[k] * inv, gv[k], dv[k]);
-            u[k] = inv * fmaf(wu[k], gu[k], -u[k] * k2);
-            v[k] = inv * fmaf(wv[k], gv[k], -v[k] * k2);
+            for (int e = 0; e < 4; ++e) {
+                const float tu = fmaf(gu[k][e], c[e], gv[k][e] * s[e]);
+                const float tv = fmaf(gv[k][e], c[e], -gu[k][e] * s[e]);
+                gu[k][e] = tu;
+                gv[k][e] = tv;
+                q = fmaf(u[k][e], u[k][e], fmaf(v[k][e], v[k][e], q));
+                m = fmaf(u[k][e] * wu[e], tu, fmaf(v[k][e] * wv[e], tv, m));
+            }
+            q = row_sum<LPR>(q);
+            m = row_sum<LPR>(m);
+            const float inv = 1.f / sqrtf(fmaf(q, dinv, a.eps));
+            const float k2 = inv * inv * m * dinv;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                du[e] = fmaf(u[k][e] * inv, gu[k][e], du[e]);
+                dv[e] = fmaf(v[k][e] * inv, gv[k][e], dv[e]);
+                u[k][e] = inv * fmaf(wu[e], gu[k][e], -u[k][e] * k2);
+                v[k][e] = inv * fmaf(wv[e], gv[k][e], -v[k][e] * k2);
+            }
+            const int head = it.h0 + k * Item::kGroups;
+            if (in && head < R.heads) store_pairs(a, y + head * R.y.sh, p0, wide, u[k], v[k]);
         }
-        if (in)
-            store_pairs(a, (T*)R.y.p + b * R.y.sb + (int64_t)i * R.y.sr + head * R.y.sh, p0, wide, u,
-                        v);
     }
     if (!R.gw) return;
 #pragma unroll
@@ -211,58 +248,76 @@ __global__ __launch_bounds__(256) void norm_rotate_bwd_kernel(const NormArgs a) 
         if (p >= a.d / 2) continue;
         float t = 0.f;
 #pragma unroll
-        for (int y = 0; y < RPB; ++y) t += red[y][x];
+        for (int y = 0; y < GRP; ++y) t += red[y][x];
         a.part[((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * a.d + pair_at(a, p, (x >> 2) & 1)] = t;
     }
 }
 
-// dw[x]: the workgroups' parts, in 64 bits and a fixed order; 32 elements a
-// workgroup, 8 lanes an element.
+// dw[x]: the workgroups' parts, in 64 bits and a fixed order; 8 elements a
+// workgroup, 32 lanes an element.
 __global__ __launch_bounds__(256) void norm_weight_kernel(const NormArgs a, int blocks) {
-    __shared__ double red[8][32];
+    __shared__ double red[32][8];
     const NormRows& R = a.r[blockIdx.y];
     if (!R.gw) return;
-    const int x = blockIdx.x * 32 + (threadIdx.x & 31), y = threadIdx.x >> 5;
+    const int e = threadIdx.x & 7, x = blockIdx.x * 8 + e, y = threadIdx.x >> 3;
     double s = 0.0;
-    if (x < a.d && R.heads > 0)
-        for (int k = y; k < blocks; k += 8)
+    if (x < a.d && R.heads > 0) {
+#pragma unroll 8
+        for (int k = y; k < blocks; k += 32)
             s += (double)a.part[((int64_t)blockIdx.y * blocks + k) * a.d + x];
-    red[y][threadIdx.x & 31] = s;
-    __syncthreads();
-    if (y == 0 && x < a.d) {
-        for (int k = 1; k < 8; ++k) s += red[k][threadIdx.x & 31];
-        R.gw[x] = (float)s;
     }
+    red[y][e] = s;
+    __syncthreads();
+    for (int o = 16; o >= 1; o >>= 1) {
+        if (y < o) red[y][e] += red[y + o][e];
+        __syncthreads();
+    }
+    if (y == 0 && x < a.d) R.gw[x] = (float)red[0][e];
 }
 
-int64_t most_rows(const NormArgs& a) {
-    const int h = a.r[0].heads > a.r[1].heads ? a.r[0].heads : a.r[1].heads;
-    return (int64_t)a.B * a.n * h;
+// Rows a lane group: four where that still leaves every SIMD several waves,
+// else one (the latency of a single token's rows is then one load's).
+constexpr int64_t kManyRows = 131072;
+int64_t items(const NormArgs& a, int lpr, int u) {
+    const int per = 64 / lpr * u;
+    const int64_t q = (a.r[0].heads + per - 1) / per, k = (a.r[1].heads + per - 1) / per;
+    return (int64_t)a.B * a.n * (q > k ? q : k);
 }
 
-template <int OP>
+template <int OP, int LPR>
 hipError_t fwd(const NormArgs& a, hipStream_t s) {
-    const int64_t rows = most_rows(a);
-    if (rows == 0) return hipSuccess;
-    if (a.d <= 64)
-        norm_rotate_kernel<OP, 8><<<dim3((unsigned)((rows + 31) / 32), 2), 256, 0, s>>>(a);
-    else if (a.d <= 128)
-        norm_rotate_kernel<OP, 16><<<dim3((unsigned)((rows + 15) / 16), 2), 256, 0, s>>>(a);
+    const bool many = (int64_t)a.B * a.n * (a.r[0].heads + a.r[1].heads) >= kManyRows;
+    const int64_t n = items(a, LPR, many ? 4 : 1);
+    if (n == 0) return hipSuccess;
+    const dim3 g((unsigned)((n + 3) / 4), 2);
+    if (many)
+        norm_rotate_kernel<OP, LPR, 4><<<g, 256, 0, s>>>(a);
     else
-        norm_rotate_kernel<OP, 32><<<dim3((unsigned)((rows + 7) / 8), 2), 256, 0, s>>>(a);
+        norm_rotate_kernel<OP, LPR, 1><<<g, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <int OP, int LPR>
+hipError_t bwd(const NormArgs& a, hipStream_t s) {
+    const bool many = (int64_t)a.B * a.n * (a.r[0].heads + a.r[1].heads) >= kManyRows;
+    const dim3 g((unsigned)a.blocks, 2);
+    if (many)
+        norm_rotate_bwd_kernel<OP, LPR, 2><<<g, 256, 0, s>>>(a);
+    else
+        norm_rotate_bwd_kernel<OP, LPR, 1><<<g, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 
 template <int OP>
-hipError_t bwd(const NormArgs& a, hipStream_t s) {
-    const dim3 g((unsigned)a.blocks, 2);
-    if (a.d <= 64)
-        norm_rotate_bwd_kernel<OP, 8><<<g, 256, 0, s>>>(a);
-    else if (a.d <= 128)
-        norm_rotate_bwd_kernel<OP, 16><<<g, 256, 0, s>>>(a);
-    else
-        norm_rotate_bwd_kernel<OP, 32><<<g, 256, 0, s>>>(a);
-    return hipGetLastError();
+hipError_t launch(const NormArgs& a, bool back, hipStream_t s) {
+    if (a.d <= 64) return back ? bwd<OP, 8>(a, s) : fwd<OP, 8>(a, s);
+    if (a.d <= 128) return back ? bwd<OP, 16>(a, s) : fwd<OP, 16>(a, s);
+    return back ? bwd<OP, 32>(a, s) : fwd<OP, 32>(a, s);
+}
+hipError_t launch(const NormArgs& a, bool back, hipStream_t s) {
+    return a.op == OP_BF16 ? launch<OP_BF16>(a, back, s)
+           : a.op == OP_F16 ? launch<OP_F16>(a, back, s)
+                            : launch<OP_F32>(a, back, s);
 }
 
 }  // namespace
@@ -272,16 +327,12 @@ int norm_bwd_blocks(int64_t rows) {
     return b < 1 ? 1 : b > 1024 ? 1024 : (int)b;
 }
 
-hipError_t launch_norm_rotate(const NormArgs& a, hipStream_t s) {
-    return a.op == OP_BF16 ? fwd<OP_BF16>(a, s) : a.op == OP_F16 ? fwd<OP_F16>(a, s)
-                                                                : fwd<OP_F32>(a, s);
-}
+hipError_t launch_norm_rotate(const NormArgs& a, hipStream_t s) { return launch(a, false, s); }
 
 hipError_t launch_norm_rotate_bwd(const NormArgs& a, hipStream_t s) {
-    hipError_t e = a.op == OP_BF16 ? bwd<OP_BF16>(a, s) : a.op == OP_F16 ? bwd<OP_F16>(a, s)
-                                                                        : bwd<OP_F32>(a, s);
+    const hipError_t e = launch(a, true, s);
     if (e != hipSuccess || (!a.r[0].gw && !a.r[1].gw)) return e;
-    norm_weight_kernel<<<dim3((unsigned)((a.d + 31) / 32), 2), 256, 0, s>>>(a, a.blocks);
+    norm_weight_kernel<<<dim3((unsigned)((a.d + 7) / 8), 2), 256, 0, s>>>(a, a.blocks);
     return hipGetLastError();
 }
 
