@@ -112,10 +112,23 @@ Extent flat(const void* p, size_t bytes) {
 
 // ---- attention ------------------------------------------------------------
 
-// The few-row kernel packs the rows of a key head's queries into blocks of 32
-// and reads the keys once per block; the other reads them once per head for
-// up to 128 rows.
-bool few_rows(const fs_attention_desc& d) { return d.n <= kAttnFewRows; }
+// Bytes of a tile's row in LDS.
+int tile_row(const fs_attention_desc& d) {
+    const int width = std::max(d.d, d.dv);
+    return (width <= 64 ? 64 : width <= 128 ? 128 : 256) * elem_size(d.dtype);
+}
+
+// The few-row kernel packs the rows of a key head's queries into blocks of 32,
+// its waves divide the keys; the other reads the keys once per head for 128
+// rows, its waves divide the rows.  The first for single tokens, and for more
+// rows if they are narrow and fill few workgroups of the other (measured, us,
+// few-row against the other: 8 x 1024 rows of 64, 1024 keys, 11.6 / 16.8; 2 x 8
+// x 500 fp32 rows of 48, 700 keys, 25.7 / 48.5; but 8 x 4 x 512 rows of 128,
+// 2048 keys, 62.5 / 38.4 and 16 x 48 rows of 128, 8192 keys, 35.0 / 22.3).
+bool few_rows(const fs_attention_desc& d) {
+    if (d.n <= kAttnFewRows) return true;
+    return d.d <= 64 && d.dv <= 64 && (int64_t)d.batch * d.heads * cdiv(d.n, kAttnRows) <= 64;
+}
 
 int buckets_of(const fs_attention_desc& d) { return (d.n_edges + 1) * (d.two_sided ? 2 : 1); }
 
@@ -192,8 +205,7 @@ fs_status take_desc(const fs_attention_desc* p, AttnArgs& a) {
     // Key ranges.  Few rows: enough workgroups for the chip, at least one tile
     // for every wave, at most 32 tiles (ranges of unequal sequences then even
     // out).  Many rows: only where whole sequences leave CUs idle.
-    const int width = std::max(d.d, d.dv), es = elem_size(d.dtype);
-    const int row = (width <= 64 ? 64 : width <= 128 ? 128 : 256) * es;  // bytes of a tile's row
+    const int row = tile_row(d);
     const bool few = few_rows(d);
     const int64_t items = few ? (int64_t)d.batch * d.kv_heads * cdiv((int64_t)a.G * d.n, 32)
                               : (int64_t)d.batch * d.heads * cdiv(d.n, kAttnRows);
@@ -208,11 +220,16 @@ fs_status take_desc(const fs_attention_desc* p, AttnArgs& a) {
         a.split_keys = (int)(cdiv(cdiv(d.m, s), turn) * turn);
         a.n_split = (int)cdiv(d.m, a.split_keys);
     }
-    // Backward passes: 128 rows a workgroup where that fills the chip, else 32,
-    // and then the queries in ranges if there are few keys.
+    // Backward passes: 128 rows a workgroup where that fills the chip, else 32
+    // (with the waves dividing the other side), and then the queries in ranges
+    // if there are few keys.  The gradients of keys in rows of 256 bytes have one
+    // buffer a wave and pay only where 128 rows leave most CUs idle (us, 32 /
+    // 128 rows: 2 x 2 x 1024 keys of 128, 256 queries, 30.5 / 48.2, but 8 x 2048
+    // keys, 128 queries, 29.3 / 16.6; 4 x 8 x 2048 keys, 512 queries, 151 / 64).
     const bool can = row <= 256;
     a.alone_q = can && (int64_t)d.batch * d.heads * cdiv(d.n, kAttnRows) < kCus;
-    a.alone_k = can && (int64_t)d.batch * d.kv_heads * cdiv(d.m, kAttnRows) < kCus;
+    a.alone_k = can && (int64_t)d.batch * d.kv_heads * cdiv(d.m, kAttnRows) <
+                           (row <= 128 || d.dtype == FS_DTYPE_F32 ? kCus : kCus / 4);
     const int64_t kblocks = cdiv(d.m, a.alone_k ? 32 : kAttnRows);
     const int64_t kitems = (int64_t)d.batch * d.kv_heads * kblocks;
     a.q_split = 1;

@@ -627,7 +627,7 @@ struct QPass {
 };
 
 template <int OP, int DP, bool BIAS, bool ALONE>
-__global__ __launch_bounds__(256, (Tile<OP, DP>::kRow <= 128 ? 2 : 1))
+__global__ __launch_bounds__(256, (Tile<OP, DP>::kRow <= 256 ? 2 : 1))
 void attn_bwd_q_kernel(const AttnArgs a) {
     using P = QPass<OP, DP, BIAS, ALONE>;
     using S = typename P::S;
@@ -711,7 +711,7 @@ void attn_bwd_q_kernel(const AttnArgs a) {
             f32x16 s, dp;
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.f;
-            auto prod = products<kAhead, 2 * NK, 2 * ND, typename E::Frag>([&](int y) {
+            auto prod = products<L::kRow == 256 ? 3 : kAhead, 2 * NK, 2 * ND, typename E::Frag>([&](int y) {
                 if (y < 2 * NK) return L::frag_rows(now, y % 2 * kBytes + o, y / 2);
                 y -= 2 * NK;
                 return L::frag_cols(now, o + 16 * (y / ND) * L::kRow, y % ND);

@@ -72,6 +72,15 @@ CASES = [
     (HF, 1, 300, 310, 2, 1, 128, 128, {"buckets": (4, 7), "two_sided": False}),
     (BF, 1, 1100, 130, 2, 1, 64, 64, {"ragged": True}),  # query ranges split
     (BF, 1, 140, 2100, 2, 2, 64, 64, {"mask": True}),    # key ranges split
+    # each form of every pass at each width of tile (workgroups of 128 rows)
+    (BF, 3, 257, 300, 16, 16, 64, 64, {"ragged": True, "mask": True}),
+    (HF, 2, 390, 390, 11, 11, 64, 64, {"causal": True, "buckets": (16, 50)}),
+    (F4, 2, 250, 270, 33, 33, 20, 20, {"mask": True}),
+    (BF, 1, 520, 1030, 8, 8, 128, 128, {"mask": True, "buckets": (16, 50), "two_sided": True}),
+    (HF, 1, 1030, 1030, 8, 4, 96, 96, {"causal": True}),
+    (BF, 1, 300, 4600, 2, 1, 128, 128, {"mask": True, "ragged": True}),  # masks of 64 tiles and more
+    (HF, 1, 3, 20000, 2, 2, 64, 64, {"mask": True}),
+    (F4, 1, 200, 210, 6, 6, 100, 100, {"causal": True, "buckets": (8, 20), "two_sided": True}),
 ]
 
 
