@@ -393,9 +393,8 @@ struct SeenKeys {
     __device__ __forceinline__ void fill(int u, int lane, int wid) const {
         if (!mask) return;
 #pragma unroll 1
-        for (int v = u + wid * 8; v < u + 64; v += 8 * W) {
-            bool ok[8] = {};
-            if (j_first + (int64_t)v * stride < je)
+        for (int v = u + wid * 8; v < u + 64 && j_first + (int64_t)v * stride < je; v += 8 * W) {
+            bool ok[8];
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
                 const int64_t j = j_first + (int64_t)(v + x) * stride + lane;
@@ -409,14 +408,15 @@ struct SeenKeys {
         }
     }
     __device__ __forceinline__ uint64_t operator()(int u) const {
+        const int64_t left = je - (j_first + (int64_t)u * stride);
+        if (left <= 0) return 0;
         if (mask) {
             const uint64_t w = lds_read<uint64_t>(words + 8 * (u & 127));
             const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(w >> 32));
             const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)w);
             return ((uint64_t)hi << 32) | lo;
         }
-        const int64_t left = je - (j_first + (int64_t)u * stride);
-        return left >= KT ? (KT == 64 ? ~0ull : (1ull << (KT & 63)) - 1) : left <= 0 ? 0 : (1ull << left) - 1;
+        return left >= KT ? (KT == 64 ? ~0ull : (1ull << (KT & 63)) - 1) : (1ull << left) - 1;
     }
 };
 // Bits 0 .. x (none for x < 0).

@@ -503,6 +503,7 @@ fs_status take_norm_desc(const fs_qk_norm_desc* p, NormArgs& a) {
     a.cos_t = d.cos_table;
     a.sin_t = d.sin_table;
     a.n_pos = d.n_pos;
+    a.table_vec = d.rot % 8 == 0 && (uintptr_t)d.cos_table % 16 == 0 && (uintptr_t)d.sin_table % 16 == 0;
     a.positions = d.positions;
     a.pos_stride = d.positions_stride;
     a.offset = d.offset;

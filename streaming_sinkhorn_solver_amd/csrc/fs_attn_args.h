@@ -81,6 +81,7 @@ struct NormArgs {
     const float* cos_t;
     const float* sin_t;  // [positions][rot / 2]
     int n_pos;
+    int table_vec;         // tables 16-byte aligned, their rows whole 16-byte chunks
     const int* positions;  // [B][n] (row stride pos_stride) or NULL
     int64_t pos_stride;
     int offset;

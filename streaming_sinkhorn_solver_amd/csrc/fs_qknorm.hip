@@ -91,6 +91,11 @@ __device__ __forceinline__ void load_angles(const NormArgs& a, int b, int i, int
     const int64_t pos = min(max(given, (int64_t)0), (int64_t)a.n_pos - 1);
     const float* ct = a.cos_t + pos * half + p0;
     const float* st = a.sin_t + pos * half + p0;
+    if (a.table_vec) {
+        load4(ct, 0, c);
+        load4(st, 0, s);
+        return;
+    }
 #pragma unroll
     for (int x = 0; x < 4; ++x)
         if (p0 + x < half) c[x] = ct[x], s[x] = st[x];
@@ -98,6 +103,10 @@ __device__ __forceinline__ void load_angles(const NormArgs& a, int b, int i, int
 // Weights of a lane's pairs.
 __device__ __forceinline__ void load_weights(const NormArgs& a, const float* w, int p0,
                                              float (&u)[4], float (&v)[4]) {
+    if (w && (uintptr_t)w % 16 == 0 && a.rot % 8 == 0 && a.d % 8 == 0 && p0 < a.d / 2) {
+        load_pairs(a, w, p0, true, u, v);
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const bool in = p0 + i < a.d / 2;
