@@ -95,9 +95,10 @@ size_t fs_attention_workspace_bytes(const fs_attention_desc* desc, int32_t backw
 
 /* o (written) and, unless NULL, lse (written, [batch][heads][n] contiguous).
  * Work: with many query rows, workgroups of 128 rows stream the keys once per
- * head; with at most 32 rows per head (single tokens) the rows of all heads of
- * a key head share one pass over the keys, which is split over workgroups and
- * joined in a fixed order.  workspace: 256-byte aligned. */
+ * head; with few (single tokens, or a small problem) the rows of all heads of
+ * a key head share a pass over the keys.  Where workgroups are few, the keys
+ * are split over them and joined in a fixed order.  workspace: 256-byte
+ * aligned. */
 fs_status fs_attention_forward(const fs_attention_desc* desc, fs_rows q, fs_rows k, fs_rows v,
                                fs_rows o, float* lse, void* workspace, size_t workspace_bytes,
                                void* stream);
@@ -108,7 +109,9 @@ fs_status fs_attention_forward(const fs_attention_desc* desc, fs_rows q, fs_rows
  * [buckets][heads]; NULL: not wanted) are written, not added to.  d_k and d_v
  * are summed over the query heads that share a key head.  For an input that
  * was broadcast by a stride of 0 each copy's gradient is written (the
- * caller's to sum). */
+ * caller's to sum).  The rows' sums of P dP are formed in fp32 by the pass that
+ * writes d_q (run for d_bias too); d_k and d_v asked for without either take
+ * them from the stored, rounded o. */
 fs_status fs_attention_backward(const fs_attention_desc* desc, fs_rows q, fs_rows k, fs_rows v,
                                 fs_rows o, const float* lse, fs_rows d_o, const float* d_lse,
                                 fs_rows d_q, fs_rows d_k, fs_rows d_v, float* d_bias,

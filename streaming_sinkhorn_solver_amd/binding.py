@@ -858,6 +858,8 @@ def fs_attention_workspace_bytes(q: torch.Tensor, k: torch.Tensor, v: torch.Tens
                                  two_sided: bool = True, backward: bool = False) -> int:
     """Bytes that serve the forward call, and the backward call if asked, on
     tensors of these shapes; edges: the bias's (None without a bias)."""
+    if q.dtype not in _DTYPES:
+        raise TypeError(f"q must be float32, bfloat16 or float16 (is {q.dtype})")
     a = AttentionDesc(_DTYPES[q.dtype], q.shape[0], q.shape[1], k.shape[1], q.shape[2],
                       k.shape[2], q.shape[3], v.shape[3], 1.0)
     if edges is not None:

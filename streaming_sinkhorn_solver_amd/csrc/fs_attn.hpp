@@ -250,6 +250,24 @@ __device__ __forceinline__ void load_elems(const typename El<OP>::T* row, int x0
     }
 }
 
+// Four results of a lane as four elements of a row (x0 a multiple of 4).
+template <int OP>
+__device__ __forceinline__ void store4(typename El<OP>::T* row, int x0, int d, bool vec, float a,
+                                       float b, float c, float e) {
+    using T = typename El<OP>::T;
+    const float y[4] = {a, b, c, e};
+    T o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = (T)y[i];
+    if (vec) {
+        if (x0 < d) __builtin_memcpy(__builtin_assume_aligned(row + x0, sizeof(o)), o, sizeof(o));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (x0 + i < d) row[x0 + i] = o[i];
+    }
+}
+
 // Operand fragments of one row held for a whole kernel: elements 16 kk + 8 h.
 template <int OP, int DP>
 __device__ __forceinline__ void load_row_frags(const typename El<OP>::T* row, bool valid, int d,

@@ -54,24 +54,6 @@ __device__ __forceinline__ float weights(f32x16& s, float cm, float ca, const Ru
     return t;
 }
 
-// Four results of a lane as four elements of a row (x0 a multiple of 4).
-template <int OP>
-__device__ __forceinline__ void store4(typename El<OP>::T* row, int x0, int d, bool vec, float a,
-                                       float b, float c, float e) {
-    using T = typename El<OP>::T;
-    const float y[4] = {a, b, c, e};
-    T o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = (T)y[i];
-    if (vec) {
-        if (x0 < d) __builtin_memcpy(__builtin_assume_aligned(row + x0, sizeof(o)), o, sizeof(o));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (x0 + i < d) row[x0 + i] = o[i];
-    }
-}
-
 // ---- many query rows ------------------------------------------------------
 // A workgroup of four waves takes 128 query rows of one head, 32 a wave, and
 // a range of keys in tiles of KT staged through LDS and shared by the waves.

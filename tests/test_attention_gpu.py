@@ -337,6 +337,67 @@ def test_graph_replays(fs, case):
             assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("case", [CASES[1], CASES[16], CASES[20], CASES[21], CASES[25]],
+                         ids=lambda c: "-".join(str(x) for x in c[:8]))
+def test_workspace_contents_do_not_matter(fs, case):
+    """Whatever the workspace held, and with no bytes to spare."""
+    q, k, v, d_o, kw = inputs(case)
+    first = run_case(fs, q, k, v, d_o, **kw)
+    need = fs.fs_attention_workspace_bytes(q, k, v, edges=kw.get("edges"), backward=True)
+    ws = torch.full((need + 512,), 0xFF, dtype=torch.uint8, device="cuda")  # NaN in every type
+    again = run_case(fs, q, k, v, d_o, workspace=ws[:need], **kw)
+    for x in first:
+        assert torch.equal(first[x], again[x]), x
+    assert torch.all(ws[need:] == 0xFF)
+
+
+def test_single_gradients(fs):
+    """Each gradient alone is the one that comes with the others; keys' and
+    values' without the queries' stay within the bounds."""
+    q, k, v, d_o, kw = inputs(CASES[13])
+    dev = {x: gpu(y) for x, y in kw.items()}
+    Q, K, V, G = (t.cuda() for t in (q, k, v, d_o))
+    full = run_case(fs, q, k, v, d_o, **kw)
+    o, lse = full["o"].cuda(), full["lse"].cuda()
+    ref = reference(q, k, v, d_o=d_o, **kw)
+    for name, like in (("d_q", Q), ("d_k", K), ("d_v", V), ("d_bias", dev["bias"])):
+        out = torch.full_like(like, math.nan)
+        fs.fs_attention_backward(Q, K, V, o, lse, G, **{name: out}, **dev)
+        torch.cuda.synchronize()
+        check(name, out, ref[name])
+        if name in ("d_q", "d_bias"):
+            assert torch.equal(out.cpu(), full[name])
+
+
+def test_binding_refuses(fs):
+    q = torch.zeros(1, 4, 2, 32, device="cuda", dtype=BF)
+    o, lse = torch.empty_like(q), torch.empty(1, 2, 4, device="cuda")
+    ok = lambda **kw: fs.fs_attention_forward(q, q, q, o, lse, **kw)
+    ok()
+    i32 = torch.int32
+    for bad, error in ((dict(kv_len=torch.tensor([4], dtype=i32)), TypeError),       # on the host
+                       (dict(kv_len=torch.tensor([4], device="cuda")), TypeError),   # int64
+                       (dict(kv_len=torch.zeros(2, dtype=i32, device="cuda")), ValueError),
+                       (dict(key_mask=torch.ones(1, 4, device="cuda")), TypeError),
+                       (dict(key_mask=torch.ones(1, 5, dtype=torch.bool, device="cuda")), ValueError),
+                       (dict(bias=torch.zeros(3, 2, device="cuda"), edges=[1, 2]), ValueError),
+                       (dict(scale=-1.0), fs.FsError), (dict(offset=1 << 30), fs.FsError),
+                       (dict(workspace=torch.empty(8, dtype=torch.uint8, device="cuda")), fs.FsError)):
+        with pytest.raises(error):
+            ok(**bad)
+    for args in ((q.float(), q, q, o), (q.double(), q, q, o), (q[0], q, q, o), (q, q[:, :3], q, o),
+                 (q, q, q, o[..., :31]), (q, q, q, q), (q, q.cpu(), q, o),
+                 (q, q, q, o[:, :1].expand(-1, 4, -1, -1)), (q.transpose(2, 3), q, q, o)):
+        with pytest.raises((TypeError, ValueError, fs.FsError)):
+            fs.fs_attention_forward(*args)
+    with pytest.raises(fs.FsError):
+        fs.fs_qk_norm_rotate(q, None, None, None, q, None)
+    with pytest.raises(TypeError):
+        fs.fs_qk_norm_rotate(q, None, None, None, o, None, cos=torch.ones(4, 16, device="cuda"))
+    with pytest.raises(TypeError):
+        fs.fs_qk_norm_rotate(None, None, None, None, None, None)
+
+
 def test_offsets_beyond_32_bits(fs):
     """Keys of 2^32 bytes and more behind one another: the last heads against
     the same rows in a small tensor, bit for bit."""
