@@ -103,6 +103,44 @@ __device__ __forceinline__ void load_angles(const NormArgs& a, int b, int i, int
     for (int x = 0; x < 4; ++x)
         if (p0 + x < half) c[x] = ct[x], s[x] = st[x];
 }
+
+// A lane's two groups of four elements of U rows of whole, aligned groups.
+// The loads ask nothing first (a lane without pairs reads the row's first ones,
+// a head behind the last the last one's), so that all are in flight before the
+// first is waited for; what was read in another's place counts as zero.
+template <typename T, int U>
+struct WideRows {
+    T lo[U][4], hi[U][4];
+    __device__ __forceinline__ void load(const NormArgs& a, const T* x, int64_t sh, int h0, int step,
+                                         int heads, int p0) {
+        const bool next = 2 * p0 >= a.rot || a.interleaved;  // the pairs' elements are neighbours
+        const int at = p0 < a.d / 2 ? p0 : 0;
+        const int xl = at == p0 && next ? 2 * at : at;
+        const int xh = at != p0 ? 4 : next ? xl + 4 : at + a.rot / 2;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int head = h0 + k * step;
+            const T* row = x + (head < heads ? head : heads - 1) * sh;
+            __builtin_memcpy(lo[k], __builtin_assume_aligned(row + xl, sizeof(lo[k])), sizeof(lo[k]));
+            __builtin_memcpy(hi[k], __builtin_assume_aligned(row + xh, sizeof(hi[k])), sizeof(hi[k]));
+        }
+    }
+    __device__ __forceinline__ void pairs(const NormArgs& a, int k, bool in, int p0, float (&u)[4],
+                                          float (&v)[4]) const {
+        const bool next = 2 * p0 >= a.rot || a.interleaved;
+        float l[4], h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            l[e] = in ? (float)lo[k][e] : 0.f;
+            h[e] = in ? (float)hi[k][e] : 0.f;
+        }
+        u[0] = l[0], v[0] = next ? l[1] : h[0];
+        u[1] = next ? l[2] : l[1], v[1] = next ? l[3] : h[1];
+        u[2] = next ? h[0] : l[2], v[2] = next ? h[1] : h[2];
+        u[3] = next ? h[2] : l[3], v[3] = h[3];
+    }
+};
+
 // Weights of a lane's pairs.
 __device__ __forceinline__ void load_weights(const NormArgs& a, const float* w, int p0,
                                              float (&u)[4], float (&v)[4]) {
@@ -154,16 +192,23 @@ __global__ __launch_bounds__(256) void norm_rotate_kernel(const NormArgs a) {
     const bool in = p0 < a.d / 2;
     const T* x = (const T*)R.x.p + it.b * R.x.sb + (int64_t)it.i * R.x.sr;
     float u[U][4], v[U][4];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-        const int head = it.h0 + k * Item::kGroups;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) u[k][e] = v[k][e] = 0.f;
-        if (in && head < R.heads) load_pairs(a, x + head * R.x.sh, p0, wide, u[k], v[k]);
-    }
+    WideRows<T, U> rows;
+    if (wide) rows.load(a, x, R.x.sh, it.h0, Item::kGroups, R.heads, p0);
     float c[4], s[4], wu[4], wv[4];
     load_angles(a, it.b, it.i, p0, c, s);
     load_weights(a, R.w, p0, wu, wv);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        const int head = it.h0 + k * Item::kGroups;
+        const bool live = in && head < R.heads;
+        if (wide) {
+            rows.pairs(a, k, live, p0, u[k], v[k]);
+            continue;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[k][e] = v[k][e] = 0.f;
+        if (live) load_pairs(a, x + head * R.x.sh, p0, false, u[k], v[k]);
+    }
     T* y = (T*)R.y.p + it.b * R.y.sb + (int64_t)it.i * R.y.sr;
     const float dinv = 1.f / (float)a.d;
 #pragma unroll
@@ -209,18 +254,29 @@ __global__ __launch_bounds__(256) void norm_rotate_bwd_kernel(const NormArgs a) 
         const T* g = (const T*)R.g.p + it.b * R.g.sb + (int64_t)it.i * R.g.sr;
         T* y = (T*)R.y.p + it.b * R.y.sb + (int64_t)it.i * R.y.sr;
         float u[U][4], v[U][4], gu[U][4], gv[U][4];
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int head = it.h0 + k * Item::kGroups;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) u[k][e] = v[k][e] = gu[k][e] = gv[k][e] = 0.f;
-            if (in && head < R.heads) {
-                load_pairs(a, x + head * R.x.sh, p0, wide, u[k], v[k]);
-                load_pairs(a, g + head * R.g.sh, p0, wide, gu[k], gv[k]);
-            }
+        WideRows<T, U> xs, gs;
+        if (wide) {
+            xs.load(a, x, R.x.sh, it.h0, Item::kGroups, R.heads, p0);
+            gs.load(a, g, R.g.sh, it.h0, Item::kGroups, R.heads, p0);
         }
         float c[4], s[4];
         load_angles(a, it.b, it.i, p0, c, s);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int head = it.h0 + k * Item::kGroups;
+            const bool live = in && head < R.heads;
+            if (wide) {
+                xs.pairs(a, k, live, p0, u[k], v[k]);
+                gs.pairs(a, k, live, p0, gu[k], gv[k]);
+                continue;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[k][e] = v[k][e] = gu[k][e] = gv[k][e] = 0.f;
+            if (live) {
+                load_pairs(a, x + head * R.x.sh, p0, false, u[k], v[k]);
+                load_pairs(a, g + head * R.g.sh, p0, false, gu[k], gv[k]);
+            }
+        }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             float q = 0.f, m = 0.f;
