@@ -11,6 +11,8 @@
 // half as many a row, took 122 and 172 us against 93 and 137.)
 #include "fs_attn.hpp"
 
+#include <type_traits>
+
 namespace fs {
 
 namespace {
@@ -247,63 +249,71 @@ __global__ __launch_bounds__(256) void norm_rotate_bwd_kernel(const NormArgs a) 
     float wu[4], wv[4], du[4] = {0, 0, 0, 0}, dv[4] = {0, 0, 0, 0};
     load_weights(a, R.w, p0, wu, wv);
     const float dinv = 1.f / (float)a.d;
-    for (uint32_t item = blockIdx.x * 4 + wave_id();; item += gridDim.x * 4) {
-        const Item it(a, R.heads, item);
-        if (!it.any) break;
-        const T* x = (const T*)R.x.p + it.b * R.x.sb + (int64_t)it.i * R.x.sr;
-        const T* g = (const T*)R.g.p + it.b * R.g.sb + (int64_t)it.i * R.g.sr;
-        T* y = (T*)R.y.p + it.b * R.y.sb + (int64_t)it.i * R.y.sr;
-        float u[U][4], v[U][4], gu[U][4], gv[U][4];
-        WideRows<T, U> xs, gs;
-        if (wide) {
-            xs.load(a, x, R.x.sh, it.h0, Item::kGroups, R.heads, p0);
-            gs.load(a, g, R.g.sh, it.h0, Item::kGroups, R.heads, p0);
+    // Two loops, so that the usual one does not hold the other's registers.
+    const auto work = [&](auto form) {
+        constexpr bool WIDE = decltype(form)::value;
+        for (uint32_t item = blockIdx.x * 4 + wave_id();; item += gridDim.x * 4) {
+            const Item it(a, R.heads, item);
+            if (!it.any) break;
+            const T* x = (const T*)R.x.p + it.b * R.x.sb + (int64_t)it.i * R.x.sr;
+            const T* g = (const T*)R.g.p + it.b * R.g.sb + (int64_t)it.i * R.g.sr;
+            T* y = (T*)R.y.p + it.b * R.y.sb + (int64_t)it.i * R.y.sr;
+            float u[U][4], v[U][4], gu[U][4], gv[U][4];
+            WideRows<T, U> xs, gs;
+            if constexpr (WIDE) {
+                xs.load(a, x, R.x.sh, it.h0, Item::kGroups, R.heads, p0);
+                gs.load(a, g, R.g.sh, it.h0, Item::kGroups, R.heads, p0);
+            }
+            float c[4], s[4];
+            load_angles(a, it.b, it.i, p0, c, s);
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int head = it.h0 + k * Item::kGroups;
+                const bool live = in && head < R.heads;
+                if constexpr (WIDE) {
+                    xs.pairs(a, k, live, p0, u[k], v[k]);
+                    gs.pairs(a, k, live, p0, gu[k], gv[k]);
+                    continue;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) u[k][e] = v[k][e] = gu[k][e] = gv[k][e] = 0.f;
+                if (live) {
+                    load_pairs(a, x + head * R.x.sh, p0, false, u[k], v[k]);
+                    load_pairs(a, g + head * R.g.sh, p0, false, gu[k], gv[k]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                float q = 0.f, m = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float tu = fmaf(gu[k][e], c[e], gv[k][e] * s[e]);
+                    const float tv = fmaf(gv[k][e], c[e], -gu[k][e] * s[e]);
+                    gu[k][e] = tu;
+                    gv[k][e] = tv;
+                    q = fmaf(u[k][e], u[k][e], fmaf(v[k][e], v[k][e], q));
+                    m = fmaf(u[k][e] * wu[e], tu, fmaf(v[k][e] * wv[e], tv, m));
+                }
+                q = row_sum<LPR>(q);
+                m = row_sum<LPR>(m);
+                const float inv = 1.f / sqrtf(fmaf(q, dinv, a.eps));
+                const float k2 = inv * inv * m * dinv;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    du[e] = fmaf(u[k][e] * inv, gu[k][e], du[e]);
+                    dv[e] = fmaf(v[k][e] * inv, gv[k][e], dv[e]);
+                    u[k][e] = inv * fmaf(wu[e], gu[k][e], -u[k][e] * k2);
+                    v[k][e] = inv * fmaf(wv[e], gv[k][e], -v[k][e] * k2);
+                }
+                const int head = it.h0 + k * Item::kGroups;
+                if (in && head < R.heads) store_pairs(a, y + head * R.y.sh, p0, WIDE, u[k], v[k]);
+            }
         }
-        float c[4], s[4];
-        load_angles(a, it.b, it.i, p0, c, s);
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int head = it.h0 + k * Item::kGroups;
-            const bool live = in && head < R.heads;
-            if (wide) {
-                xs.pairs(a, k, live, p0, u[k], v[k]);
-                gs.pairs(a, k, live, p0, gu[k], gv[k]);
-                continue;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) u[k][e] = v[k][e] = gu[k][e] = gv[k][e] = 0.f;
-            if (live) {
-                load_pairs(a, x + head * R.x.sh, p0, false, u[k], v[k]);
-                load_pairs(a, g + head * R.g.sh, p0, false, gu[k], gv[k]);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            float q = 0.f, m = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float tu = fmaf(gu[k][e], c[e], gv[k][e] * s[e]);
-                const float tv = fmaf(gv[k][e], c[e], -gu[k][e] * s[e]);
-                gu[k][e] = tu;
-                gv[k][e] = tv;
-                q = fmaf(u[k][e], u[k][e], fmaf(v[k][e], v[k][e], q));
-                m = fmaf(u[k][e] * wu[e], tu, fmaf(v[k][e] * wv[e], tv, m));
-            }
-            q = row_sum<LPR>(q);
-            m = row_sum<LPR>(m);
-            const float inv = 1.f / sqrtf(fmaf(q, dinv, a.eps));
-            const float k2 = inv * inv * m * dinv;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                du[e] = fmaf(u[k][e] * inv, gu[k][e], du[e]);
-                dv[e] = fmaf(v[k][e] * inv, gv[k][e], dv[e]);
-                u[k][e] = inv * fmaf(wu[e], gu[k][e], -u[k][e] * k2);
-                v[k][e] = inv * fmaf(wv[e], gv[k][e], -v[k][e] * k2);
-            }
-            const int head = it.h0 + k * Item::kGroups;
-            if (in && head < R.heads) store_pairs(a, y + head * R.y.sh, p0, wide, u[k], v[k]);
-        }
-    }
+    };
+    if (wide)
+        work(std::true_type{});
+    else
+        work(std::false_type{});
     if (!R.gw) return;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
