@@ -6,9 +6,9 @@
 // angles' cosines and sines are shared by the heads of a token.  A lane holds
 // four pairs (8 elements), d / 8 lanes (rounded up to a power of two) a row,
 // so a row's sums are butterflies within those lanes.  (4 x 4096 tokens, 32 + 8
-// heads of 128, bf16: forward 82 us for 335 MB, 4.1 TB/s; backward 132 us for
-// 503 MB, 3.8 TB/s, and 5 us for the weights' sums.  Lanes of 16-byte loads,
-// half as many a row, took 122 and 172 us against 93 and 137.)
+// heads of 128, bf16: forward 73 us for 335 MB, 4.6 TB/s; backward 102 us for
+// 503 MB, 4.9 TB/s, and 5 us for the weights' sums.  Lanes of 16-byte loads,
+// half as many a row, were slower, 122 and 172 us against 93 and 137 at the time.)
 #include "fs_attn.hpp"
 
 #include <type_traits>
@@ -193,42 +193,49 @@ __global__ __launch_bounds__(256) void norm_rotate_kernel(const NormArgs a) {
     const bool wide = R.x.vec && R.y.vec && a.rot % 8 == 0 && a.d % 8 == 0;
     const bool in = p0 < a.d / 2;
     const T* x = (const T*)R.x.p + it.b * R.x.sb + (int64_t)it.i * R.x.sr;
-    float u[U][4], v[U][4];
-    WideRows<T, U> rows;
-    if (wide) rows.load(a, x, R.x.sh, it.h0, Item::kGroups, R.heads, p0);
-    float c[4], s[4], wu[4], wv[4];
-    load_angles(a, it.b, it.i, p0, c, s);
-    load_weights(a, R.w, p0, wu, wv);
+    const auto work = [&](auto form) {
+        constexpr bool WIDE = decltype(form)::value;
+        float u[U][4], v[U][4];
+        WideRows<T, U> rows;
+        if constexpr (WIDE) rows.load(a, x, R.x.sh, it.h0, Item::kGroups, R.heads, p0);
+        float c[4], s[4], wu[4], wv[4];
+        load_angles(a, it.b, it.i, p0, c, s);
+        load_weights(a, R.w, p0, wu, wv);
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-        const int head = it.h0 + k * Item::kGroups;
-        const bool live = in && head < R.heads;
-        if (wide) {
-            rows.pairs(a, k, live, p0, u[k], v[k]);
-            continue;
+        for (int k = 0; k < U; ++k) {
+            const int head = it.h0 + k * Item::kGroups;
+            const bool live = in && head < R.heads;
+            if constexpr (WIDE) {
+                rows.pairs(a, k, live, p0, u[k], v[k]);
+                continue;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[k][e] = v[k][e] = 0.f;
+            if (live) load_pairs(a, x + head * R.x.sh, p0, false, u[k], v[k]);
         }
+        T* y = (T*)R.y.p + it.b * R.y.sb + (int64_t)it.i * R.y.sr;
+        const float dinv = 1.f / (float)a.d;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) u[k][e] = v[k][e] = 0.f;
-        if (live) load_pairs(a, x + head * R.x.sh, p0, false, u[k], v[k]);
-    }
-    T* y = (T*)R.y.p + it.b * R.y.sb + (int64_t)it.i * R.y.sr;
-    const float dinv = 1.f / (float)a.d;
+        for (int k = 0; k < U; ++k) {
+            float q = 0.f;
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-        float q = 0.f;
+            for (int e = 0; e < 4; ++e) q = fmaf(u[k][e], u[k][e], fmaf(v[k][e], v[k][e], q));
+            q = row_sum<LPR>(q);
+            const float inv = 1.f / sqrtf(fmaf(q, dinv, a.eps));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) q = fmaf(u[k][e], u[k][e], fmaf(v[k][e], v[k][e], q));
-        q = row_sum<LPR>(q);
-        const float inv = 1.f / sqrtf(fmaf(q, dinv, a.eps));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float zu = u[k][e] * inv * wu[e], zv = v[k][e] * inv * wv[e];
-            u[k][e] = fmaf(zu, c[e], -zv * s[e]);
-            v[k][e] = fmaf(zv, c[e], zu * s[e]);
+            for (int e = 0; e < 4; ++e) {
+                const float zu = u[k][e] * inv * wu[e], zv = v[k][e] * inv * wv[e];
+                u[k][e] = fmaf(zu, c[e], -zv * s[e]);
+                v[k][e] = fmaf(zv, c[e], zu * s[e]);
+            }
+            const int head = it.h0 + k * Item::kGroups;
+            if (in && head < R.heads) store_pairs(a, y + head * R.y.sh, p0, WIDE, u[k], v[k]);
         }
-        const int head = it.h0 + k * Item::kGroups;
-        if (in && head < R.heads) store_pairs(a, y + head * R.y.sh, p0, wide, u[k], v[k]);
-    }
+    };
+    if (wide)
+        work(std::true_type{});
+    else
+        work(std::false_type{});
 }
 
 // Backward: a workgroup takes items blockIdx.x * 4 + wave, in steps of the grid;
@@ -249,7 +256,8 @@ __global__ __launch_bounds__(256) void norm_rotate_bwd_kernel(const NormArgs a) 
     float wu[4], wv[4], du[4] = {0, 0, 0, 0}, dv[4] = {0, 0, 0, 0};
     load_weights(a, R.w, p0, wu, wv);
     const float dinv = 1.f / (float)a.d;
-    // Two loops, so that the usual one does not hold the other's registers.
+    // Two loops, so that the usual one does not hold the other's registers (150
+    // for one with both, three waves a SIMD, 129 us; 108, four, 102 us).
     const auto work = [&](auto form) {
         constexpr bool WIDE = decltype(form)::value;
         for (uint32_t item = blockIdx.x * 4 + wave_id();; item += gridDim.x * 4) {
