@@ -448,6 +448,9 @@ NORM = [  # dtype, B, n, Hq, Hk, d, rot, interleaved, weights, offset or positio
     (F4, 1, 3, 0, 2, 2, 2, True, False, 0),
     (BF, 1, 600, 8, 2, 96, 0, False, True, 0),
     (F4, 1, 1, 1, 1, 256, 250, False, True, -4),
+    # enough rows for the forms of several rows a lane group, heads not a multiple of them
+    (BF, 2, 4700, 11, 3, 80, 32, False, True, "positions"),
+    (HF, 1, 33000, 3, 1, 64, 48, True, True, "positions"),
 ]
 
 
