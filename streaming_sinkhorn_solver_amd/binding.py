@@ -281,6 +281,18 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """torch.empty for a call on `stream`.  The memory comes from that stream's
+    pool: a block of the current stream's may still be in use there when it is
+    handed out, and only work of the current stream waits for that."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 class Problem:
     """A problem handle plus the workspace tensor it lives in."""
 
@@ -775,13 +787,9 @@ def _flat(t: Optional[torch.Tensor], name: str, dev: int, dtype, shape) -> Optio
 
 def _work(workspace: Optional[torch.Tensor], size, like: torch.Tensor, dev: int, stream):
     """Aligned address and size of the workspace, and the tensor to keep: the
-    caller's, or one of size() bytes that the stream holds until it is done."""
+    caller's, or one of size() bytes from the memory of the call's stream."""
     if workspace is None:
-        workspace = torch.empty(size() + 256, dtype=torch.uint8, device=like.device)
-        if stream is not None:
-            s = stream if isinstance(stream, torch.cuda.Stream) else \
-                torch.cuda.ExternalStream(int(stream), device=like.device)
-            workspace.record_stream(s)
+        workspace = _empty(size() + 256, torch.uint8, like.device, stream)
     else:
         _on(workspace, "workspace", dev)
         if not workspace.is_contiguous():
