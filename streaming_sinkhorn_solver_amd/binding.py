@@ -329,7 +329,7 @@ def fs_potentials_init(X: torch.Tensor, Y: torch.Tensor, a: torch.Tensor, b: tor
     if need == 0:
         _check(FS_ERR_INVALID_ARG, "fs_workspace_bytes")
     if workspace is None:
-        workspace = torch.empty(need + 256, dtype=torch.uint8, device=X.device)
+        workspace = _empty(need + 256, torch.uint8, X.device, stream)
     base = workspace.data_ptr()
     aligned = (base + 255) // 256 * 256
     avail = workspace.numel() - (aligned - base)
@@ -431,7 +431,7 @@ def fs_hvp(p: Problem, eps: float, f, g, X, Y, V, HV, cg_tol: float = 1e-4,
     rows = p.n if wrt == "x" else p.m
     need = fs_hvp_workspace_bytes(p)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=V.device)
+        workspace = _empty(max(need, 1), torch.uint8, V.device, stream)
     if not workspace.is_cuda:
         raise TypeError("workspace must be a device tensor")
     info = HvpInfo()
@@ -448,7 +448,7 @@ def fs_hvp(p: Problem, eps: float, f, g, X, Y, V, HV, cg_tol: float = 1e-4,
 def fs_dual_value(p: Problem, f, g, out=None, stream=None) -> torch.Tensor:
     """<a,f> + <b,g> into a one-element float64 device tensor (returned)."""
     if out is None:
-        out = torch.empty(1, dtype=torch.float64, device=f.device)
+        out = _empty(1, torch.float64, f.device, stream)
     if out.dtype != torch.float64 or not out.is_cuda or out.numel() < 1:
         raise TypeError("out must be a float64 device tensor")
     _check(load().fs_dual_value(p.handle, _dev(f, "f", p.n), _dev(g, "g", p.m), out.data_ptr(),
@@ -495,16 +495,16 @@ def fs_morton_sort(X, w=None, X_sorted=None, w_sorted=None, perm=None, workspace
     n, d = X.shape
     dev = X.device
     if X_sorted is None:
-        X_sorted = torch.empty_like(X)
+        X_sorted = _empty(X.shape, X.dtype, dev, stream)
     if w is not None and w_sorted is None:
-        w_sorted = torch.empty_like(w)
+        w_sorted = _empty(w.shape, w.dtype, dev, stream)
     if perm is None:
-        perm = torch.empty(n, dtype=torch.int32, device=dev)
+        perm = _empty(n, torch.int32, dev, stream)
     need = fs_morton_workspace_bytes(n, d)
     if need == 0:
         _check(FS_ERR_INVALID_ARG, "fs_morton_workspace_bytes")
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _empty(need, torch.uint8, dev, stream)
     _check(load().fs_morton_sort(_dev(X, "X", n * d), _dev(w, "w", n), n, d,
                                  _dev(X_sorted, "X_sorted", n * d), _dev(w_sorted, "w_sorted", n),
                                  _idev(perm, "perm", n), workspace.data_ptr(),
@@ -518,7 +518,7 @@ def fs_unpermute(src, perm, dst=None, stream=None):
     n = perm.numel()
     width = src.numel() // n
     if dst is None:
-        dst = torch.empty_like(src)
+        dst = _empty(src.shape, src.dtype, src.device, stream)
     _check(load().fs_unpermute(_dev(src, "src", n * width), _idev(perm, "perm", n), n, width,
                                _dev(dst, "dst", n * width), _stream(stream)), "fs_unpermute")
     return dst
@@ -534,7 +534,7 @@ def fs_bs_attach(p: Problem, workspace=None, stream=None):
     if need == 0:
         _check(FS_ERR_INVALID_ARG, "fs_bs_workspace_bytes")
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=p.workspace.device)
+        workspace = _empty(need, torch.uint8, p.workspace.device, stream)
     _check(load().fs_bs_attach(p.handle, workspace.data_ptr(),
                                workspace.numel() * workspace.element_size(), _stream(stream)),
            "fs_bs_attach")
@@ -633,8 +633,8 @@ def fs_centroids(P, w, cell: int, C=None, W=None, stream=None):
     """Centroids and weights of runs of `cell` points; returns (C, W)."""
     n, d = P.shape
     nc = (n + cell - 1) // cell if cell >= 1 else 1  # (the library rejects cell < 1)
-    C = torch.empty((nc, d), device=P.device) if C is None else C
-    W = torch.empty(nc, device=P.device) if W is None else W
+    C = _empty((nc, d), P.dtype, P.device, stream) if C is None else C
+    W = _empty(nc, P.dtype, P.device, stream) if W is None else W
     _check(load().fs_centroids(_dev(P, "P", n * d), _dev(w, "w", n), n, d, int(cell),
                                _dev(C, "C", nc * d), _dev(W, "W", nc), _stream(stream)),
            "fs_centroids")
@@ -642,7 +642,7 @@ def fs_centroids(P, w, cell: int, C=None, W=None, stream=None):
 
 
 def fs_lift(F, n: int, cell: int, f=None, stream=None):
-    f = torch.empty(n, device=F.device) if f is None else f
+    f = _empty(n, F.dtype, F.device, stream) if f is None else f
     _check(load().fs_lift(_dev(F, "F", (n + cell - 1) // cell), n, int(cell), _dev(f, "f", n),
                           _stream(stream)), "fs_lift")
     return f
@@ -655,9 +655,9 @@ def fs_sampled_marginal_error(X, Y, a, b, f, g, eps: float, rows, cols, out2=Non
     n, d = X.shape
     m = Y.shape[0]
     nr, nc = rows.numel(), cols.numel()
-    out2 = torch.empty(2, device=X.device) if out2 is None else out2
+    out2 = _empty(2, X.dtype, X.device, stream) if out2 is None else out2
     need = lib.fs_sampled_workspace_bytes(nr, nc)
-    workspace = torch.empty(need, dtype=torch.uint8, device=X.device) if workspace is None \
+    workspace = _empty(need, torch.uint8, X.device, stream) if workspace is None \
         else workspace
     _check(lib.fs_sampled_marginal_error(
         _dev(X, "X", n * d), _dev(Y, "Y", m * d), _dev(a, "a", n), _dev(b, "b", m), n, m, d,
@@ -680,7 +680,7 @@ def fs_bs_coarse_start(coarse: Problem, X, Y, a, b, cell: int, f, g, F, G, rows,
     m = Y.shape[0]
     nr, nc = rows.numel(), cols.numel()
     need = lib.fs_sampled_workspace_bytes(nr, nc) + 256
-    ws = torch.empty(need, dtype=torch.uint8, device=X.device)
+    ws = _empty(need, torch.uint8, X.device, stream)
     opts = SolveOpts(int(n_stages), float(eps_start if eps_start is not None else eps_end),
                      float(eps_end), int(iters_per_stage), 0.0, 1, 0, 0)
     info = CoarseInfo()

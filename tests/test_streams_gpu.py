@@ -66,7 +66,31 @@ def norm(fs, stream=None, order=lambda: None):
     return dx, dw
 
 
-@pytest.mark.parametrize("work", [attention, norm])
+def solver(fs, stream=None, order=lambda: None):
+    """Every solver call that allocates something for itself."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    n, m, d, eps = 300, 260, 3, 0.5
+    X, V = (torch.rand(n, d, generator=g, device="cuda") for _ in range(2))
+    Y = torch.rand(m, d, generator=g, device="cuda")
+    a, b = torch.full((n,), 1 / n, device="cuda"), torch.full((m,), 1 / m, device="cuda")
+    f, gp, HV = (torch.zeros(s, device="cuda") for s in (n, m, (n, d)))
+    pick = torch.arange(20, dtype=torch.int32, device="cuda")
+    order()
+    kw = {"stream": stream}
+    Xs, ws, perm = fs.fs_morton_sort(X, a, **kw)
+    back = fs.fs_unpermute(Xs, perm, **kw)
+    C, W = fs.fs_centroids(Xs, ws, 8, **kw)
+    lifted = fs.fs_lift(W, n, 8, **kw)
+    p = fs.fs_potentials_init(X, Y, a, b, dv_max=d + 2, f=f, g=gp, **kw)
+    fs.fs_bs_attach(p, **kw)
+    fs.fs_sinkhorn_solve(p, f, gp, eps_end=eps, iters_per_stage=20, **kw)
+    value = fs.fs_dual_value(p, f, gp, **kw)
+    errs = fs.fs_sampled_marginal_error(X, Y, a, b, f, gp, eps, pick, pick, **kw)
+    fs.fs_hvp(p, eps, f, gp, X, Y, V, HV, **kw)
+    return Xs, ws, perm, back, C, W, lifted, f, gp, value, errs, HV
+
+
+@pytest.mark.parametrize("work", [attention, norm, solver])
 def test_temporary_memory_is_the_streams_own(fs, monkeypatch, side, work):
     """Each workspace that a call allocates for itself comes from the pool of the
     stream that it runs on, given as a stream or as its handle."""
@@ -91,7 +115,7 @@ def test_temporary_memory_is_the_streams_own(fs, monkeypatch, side, work):
             assert torch.equal(x, y)
 
 
-@pytest.mark.parametrize("work", [attention, norm])
+@pytest.mark.parametrize("work", [attention, norm, solver])
 def test_other_stream_in_order(fs, side, work):
     """The side stream waits for the fills and the current one for the side
     stream, with no wait of the host between: equal bits."""
