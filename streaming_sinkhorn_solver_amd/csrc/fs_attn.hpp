@@ -139,6 +139,13 @@ struct Tile {
 #pragma unroll
             for (int x = 0; x < kColAddrs; ++x) cols[x] = l.cols[x] + offset;
         }
+        // the same, in place of these: half the registers where they are scarce
+        __device__ __forceinline__ void move(uint32_t offset) {
+#pragma unroll
+            for (int x = 0; x < kRowAddrs; ++x) rows[x] += offset;
+#pragma unroll
+            for (int x = 0; x < kColAddrs; ++x) cols[x] += offset;
+        }
     };
 
     // Operand whose rows (or columns) are the tile's rows r0 + (lane & 31),
@@ -334,8 +341,11 @@ __device__ __forceinline__ void dma_wait_but() {
 // bit in `seen` is clear are filled with zeros and never read: what stands
 // there (NaN in padding, memory behind the tensor) cannot enter a product.
 // Aligned rows (vec) go straight to LDS and are complete after dma_wait();
-// others are loaded element by element and stored at once.
-template <int OP, int DP, int ROWS, int NT>
+// others are loaded element by element and stored at once.  ANEW: the places of a
+// thread are formed at every fill, for kernels without registers to keep them
+// (put into memory, they are read again between the copies, and each time that
+// waits for the copies before).
+template <int OP, int DP, int ROWS, int NT, bool ANEW = false>
 struct Loader {
     using L = Tile<OP, DP>;
     using T = typename El<OP>::T;
@@ -346,6 +356,7 @@ struct Loader {
 
     static __device__ __forceinline__ void fill(uint32_t lds, const T* base, int64_t stride,
                                                 uint64_t seen, int w, bool vec, int t) {
+        if (ANEW) asm volatile("" : "+v"(t));
         const int c0 = t % L::kCh, r0 = t / L::kCh;
         const uint32_t dst = lds + (NT == 64 ? 0 : wave_id() * 1024);
         if (vec) {
@@ -383,16 +394,21 @@ struct Loader {
 // keeps the compiler from exchanging them).
 __device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
-// The keys of a batch entry that exist, and the position of query row 0.
+// The keys and queries of a batch entry that exist, and the position of query
+// row 0.  The entry is the whole wave's: said so, what follows from them stays
+// in scalar registers, and with it the tiles' addresses.
+__device__ __forceinline__ int row_len(const int* len, int b, int n) {
+    return len ? min(max(len[b], 0), n) : n;
+}
 __device__ __forceinline__ int attn_kv_len(const AttnArgs& a, int b) {
-    return a.kv_len ? min(max(a.kv_len[b], 0), a.m) : a.m;
+    return __builtin_amdgcn_readfirstlane(row_len(a.kv_len, b, a.m));
 }
 __device__ __forceinline__ int attn_q_len(const AttnArgs& a, int b) {
-    return a.q_len ? min(max(a.q_len[b], 0), a.n) : a.n;
+    return __builtin_amdgcn_readfirstlane(row_len(a.q_len, b, a.n));
 }
 __device__ __forceinline__ int attn_offset(const AttnArgs& a, int b) {
     const int o = a.offsets ? a.offsets[b] : a.offset;
-    return min(max(o, -kAttnMaxOffset), kAttnMaxOffset);
+    return __builtin_amdgcn_readfirstlane(min(max(o, -kAttnMaxOffset), kAttnMaxOffset));
 }
 
 // Which of the keys of a tile of KT (at most 64) exist and are not masked out:

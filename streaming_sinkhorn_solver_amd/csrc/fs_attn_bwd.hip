@@ -30,7 +30,7 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(const AttnArgs a) {
     const int head = (int)(r % a.H);
     const int64_t bi = r / a.H;
     const int i = (int)(bi % a.n_pad), b = (int)(bi / a.n_pad);
-    const bool ok = i < attn_q_len(a, b);
+    const bool ok = i < row_len(a.q_len, b, a.n);
     float s = 0.f;
     if (ok) {
         const T* o = (const T*)a.o.p + b * a.o.sb + (int64_t)i * a.o.sr + head * a.o.sh;
@@ -212,25 +212,46 @@ struct KvPass {
             for (int x = lane; x < 32 * kDiag; x += 64) dg.set(x, 0.f);
     }
 
-    // The rows of tile u of head g: q and do to LDS (lds: a tile each), and the
-    // row terms, 64 floats for every 32 rows, to terms.
-    __device__ __forceinline__ void fetch(const AttnArgs& a, int g, int u, uint32_t lds,
+    // Tile u of head g of the group.
+    struct Place {
+        int g, u;
+    };
+    // `step` tiles on; without a bias the tiles of all heads are one sequence.
+    __device__ __forceinline__ Place advance(Place x, int step) const {
+        x.u += step;
+        if (!BIAS && n_tiles > 0)
+            while (x.u >= n_tiles) x.u -= n_tiles, ++x.g;
+        return x;
+    }
+    // -L of the lane's row of a tile (rows are padded to whole tiles), read a tile
+    // before the tile's fetch asks which rows take part.  A row that takes none
+    // has -inf and weight 0; it is fetched as zeros, or what it holds (the loss of
+    // an empty row may well have no derivative) would enter sums as 0 * NaN.
+    __device__ __forceinline__ float row_term(const AttnArgs& a, Place x) const {
+        const int64_t lrow = ((int64_t)b * a.H + kvh * a.G + x.g) * a.n_pad + first + x.u * QT;
+        return lane < QT ? a.nl2[lrow + lane] : -INFINITY;
+    }
+    static __device__ __forceinline__ uint64_t live(float term) { return __ballot(term != -INFINITY); }
+    // A tile's rows in `seen`: q and do to LDS (lds: a tile each), and the row
+    // terms, 64 floats for every 32 rows, to terms (these first: an address that
+    // had to be put into memory is read again, and that waits for the copies
+    // before it).
+    __device__ __forceinline__ void fetch(const AttnArgs& a, Place x, uint64_t seen, uint32_t lds,
                                           uint32_t terms) const {
-        using Load = Loader<OP, DP, QT, S::kNt>;
-        const int i0 = first + u * QT, head = kvh * a.G + g;
-        const uint64_t seen = ((uint64_t)bits_upto(end - 33 - i0) << 32) | bits_upto(end - 1 - i0);
-        const int t = ALONE ? lane : (int)threadIdx.x;
-        Load::fill(lds, (const T*)a.q.p + b * a.q.sb + head * a.q.sh + (int64_t)i0 * a.q.sr, a.q.sr,
-                   seen, a.d, a.q.vec, t);
-        Load::fill(lds + QT * L::kRow,
-                   (const T*)a.go.p + b * a.go.sb + head * a.go.sh + (int64_t)i0 * a.go.sr, a.go.sr,
-                   seen, a.dv, a.go.vec, t);
+        using Load = Loader<OP, DP, QT, S::kNt, true>;
+        const int i0 = first + x.u * QT, head = kvh * a.G + x.g;
         const int part = ALONE ? 0 : wid;  // 32 rows a wave
         if (part < QT / 32) {
             const int64_t lrow = ((int64_t)b * a.H + head) * a.n_pad + i0 + 32 * part;
             const float* src = (lane < 32 ? a.nl2 : a.delta) + lrow + (lane & 31);
             dma_lane4((const char*)src, terms + 256 * part);
         }
+        const int t = ALONE ? lane : (int)threadIdx.x;
+        Load::fill(lds, (const T*)a.q.p + b * a.q.sb + head * a.q.sh + (int64_t)i0 * a.q.sr, a.q.sr,
+                   seen, a.d, a.q.vec, t);
+        Load::fill(lds + QT * L::kRow,
+                   (const T*)a.go.p + b * a.go.sb + head * a.go.sh + (int64_t)i0 * a.go.sr, a.go.sr,
+                   seen, a.dv, a.go.vec, t);
     }
 
     __device__ __forceinline__ void start_head(const AttnArgs& a, int g) {
@@ -388,6 +409,17 @@ void attn_bwd_kv_kernel(const AttnArgs a) {
     P p(a, lines, diag);
     const int lane = p.lane, wid = p.wid, set = ALONE ? wid : 0;
 
+    // With a bias the heads are taken one after the other (each has its line);
+    // else the tiles of all heads are one sequence.
+    const int step = ALONE ? 4 : 1, u_first = ALONE ? wid : 0;
+    const int n_all = BIAS ? p.n_tiles : p.n_tiles * a.G;
+    typename P::Place here{0, 0};
+    float term = -INFINITY;
+    if (u_first < n_all) {
+        here = p.advance(here, u_first);
+        term = p.row_term(a, here);
+    }
+
     typename E::Frag kf[NK], vf[NK];
     load_row_frags<OP, DP>((const T*)a.k.p + p.b * a.k.sb + (int64_t)p.j * a.k.sr + p.kvh * a.k.sh,
                            p.key_ok, a.d, a.k.vec, lane, kf);
@@ -401,33 +433,36 @@ void attn_bwd_kv_kernel(const AttnArgs a) {
         for (int r = 0; r < 16; ++r) dk[x][r] = dv[x][r] = 0.f;
     DsScale<OP, ND> dss;
     const uint32_t tile0 = lds_addr(tiles[set]), term0 = lds_addr(terms[set]);
-    const typename L::Lanes lanes(tile0, lane);
+    typename L::Lanes now(tile0, lane);
+    int cur = 0;
 
-    // With a bias the heads are taken one after the other (each has its line);
-    // else the tiles of all heads are one sequence.
-    const int step = ALONE ? 4 : 1;
     for (int g0 = 0; g0 < (BIAS ? a.G : 1); ++g0) {
-        const int n_all = BIAS ? p.n_tiles : p.n_tiles * a.G;
+        int u = u_first;
+        if (g0 > 0) here = {g0, u}, term = u < n_all ? p.row_term(a, here) : -INFINITY;
         p.start_head(a, g0);
-        const auto fetch = [&](int u, int buf) {
-            const int g = BIAS ? g0 : u / p.n_tiles;
-            p.fetch(a, g, BIAS ? u : u - g * p.n_tiles, tile0 + 2 * buf * kBytes, term0 + 8 * QT * buf);
+        const auto fetch = [&](typename P::Place x, uint64_t seen, int buf) {
+            p.fetch(a, x, seen, tile0 + 2 * buf * kBytes, term0 + 8 * QT * buf);
         };
-        int u = ALONE ? wid : 0, cur = 0;
-        if (u < n_all) fetch(u, 0);
+        typename P::Place next = p.advance(here, step);
+        if (u < n_all) {
+            fetch(here, P::live(term), cur);
+            if (u + step < n_all) term = p.row_term(a, next);
+        }
         for (; u < n_all; u += step) {
             dma_wait();
             if (ALONE)
                 wave_fence();
             else
                 __builtin_amdgcn_s_barrier();
-            const typename L::Lanes now(lanes, cur * 2 * kBytes);
-            const uint32_t term = term0 + 8 * QT * cur;
+            const uint32_t term_lds = term0 + 8 * QT * cur;
+            const uint64_t seen = P::live(term);
             if (S::kBufs == 2) {
                 cur ^= 1;
-                if (u + step < n_all) fetch(u + step, cur);
+                if (u + step < n_all) fetch(next, seen, cur);
             }
-            const int i00 = p.first + (BIAS ? u : u % p.n_tiles) * QT;
+            const typename P::Place after = p.advance(next, step);
+            if (u + 2 * step < n_all) term = p.row_term(a, after);
+            const int i00 = p.first + here.u * QT;
 #pragma unroll
             for (int qb = 0; qb < QT / 32; ++qb) {
                 const int i0 = i00 + 32 * qb, o = 32 * qb * L::kRow;
@@ -452,7 +487,7 @@ void attn_bwd_kv_kernel(const AttnArgs a) {
                 });
                 float rl[16], rd[16];
                 bool lo_far, hi_far;
-                p.row_terms(a, i0, term + 256 * qb, rl, rd, lo_far, hi_far);
+                p.row_terms(a, i0, term_lds + 256 * qb, rl, rd, lo_far, hi_far);
                 p.hide(a, i0, s);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
@@ -478,8 +513,11 @@ void attn_bwd_kv_kernel(const AttnArgs a) {
             if (S::kBufs == 1 && u + step < n_all) {
                 dma_wait();
                 wave_fence();
-                fetch(u + step, 0);
+                fetch(next, seen, 0);
             }
+            here = next;
+            next = after;
+            if (S::kBufs == 2) now.move(cur ? 2 * kBytes : -2 * kBytes);
         }
         if (DK) p.end_head(a, g0);
     }
@@ -604,10 +642,12 @@ struct QPass {
             for (int r = 0; r < 16; ++r) s[r] = flag(vis, r) ? s[r] : -INFINITY;
         }
     }
-    // delta made exact; dQ.  rest: the row's sum of dS.
+    // delta made exact; dQ (zero for a row that takes no part).  rest: the row's
+    // sum of dS.
     __device__ __forceinline__ void store(const AttnArgs& a, const f32x16 (&acc)[ND], float rest) const {
         if (!in) return;
-        if (h == 0 && rl != -INFINITY)
+        const bool part = row_ok && rl != -INFINITY;
+        if (h == 0 && part)
             a.delta[lrow] = rd + rest - (a.glse ? a.glse[((int64_t)b * a.H + head) * a.n + i] : 0.f);
         if (!a.gq.p) return;
         T* o = (T*)a.gq.p + b * a.gq.sb + (int64_t)i * a.gq.sr + head * a.gq.sh;
@@ -615,9 +655,9 @@ struct QPass {
         for (int cb = 0; cb < ND; ++cb)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                store4<OP>(o, 32 * cb + 8 * q + 4 * h, a.d, a.gq.vec, row_ok ? acc[cb][4 * q] : 0.f,
-                           row_ok ? acc[cb][4 * q + 1] : 0.f, row_ok ? acc[cb][4 * q + 2] : 0.f,
-                           row_ok ? acc[cb][4 * q + 3] : 0.f);
+                store4<OP>(o, 32 * cb + 8 * q + 4 * h, a.d, a.gq.vec, part ? acc[cb][4 * q] : 0.f,
+                           part ? acc[cb][4 * q + 1] : 0.f, part ? acc[cb][4 * q + 2] : 0.f,
+                           part ? acc[cb][4 * q + 3] : 0.f);
     }
 };
 

@@ -1,0 +1,101 @@
+"""Attention where rows, keys or sizes are at the edge of what a call allows, against
+the definition in 64 bits.  A few heads are checked; a problem is made large enough
+for the other forms of the kernels by repeating them, and each copy has to give the
+same bits."""
+import math
+
+import pytest
+import torch
+
+from attention_reference import check, reference
+from test_attention_gpu import BF, F4, HF, gpu, randn
+
+pytestmark = pytest.mark.gpu
+
+NAN, INF = math.nan, math.inf
+
+
+def run(fs, q, k, v, d_o=None, d_lse=None, copies=1, **kw):
+    """Outputs of the first heads, on the CPU, as a dict; with copies > 1 every
+    head stands that many times in the call and all copies are compared."""
+    rep = lambda t: t.cuda().repeat(1, 1, copies, 1)
+    Q, K, V = rep(q), rep(k), rep(v)
+    dev = {x: gpu(y) for x, y in kw.items()}
+    B, n, H, _ = Q.shape
+    nan = lambda *s, dtype=q.dtype: torch.full(s, NAN, dtype=dtype, device="cuda")
+    if kw.get("bias") is not None:
+        dev["bias"] = dev["bias"].repeat(1, copies)
+    out = {"o": nan(B, n, H, v.shape[3]), "lse": nan(B, H, n, dtype=F4)}
+    fs.fs_attention_forward(Q, K, V, out["o"], out["lse"], **dev)
+    if d_o is not None:
+        out["d_q"], out["d_k"], out["d_v"] = (nan(*t.shape) for t in (Q, K, V))
+        if kw.get("bias") is not None:
+            out["d_bias"] = nan(*dev["bias"].shape, dtype=F4)
+        g = None if d_lse is None else d_lse.cuda().repeat(1, copies, 1)
+        fs.fs_attention_backward(Q, K, V, out["o"], out["lse"], rep(d_o), out["d_q"], out["d_k"],
+                                 out["d_v"], d_lse=g, d_bias=out.get("d_bias"), **dev)
+    torch.cuda.synchronize()
+    heads = {"lse": 1, "d_bias": 1}
+    for x, t in out.items():
+        axis = heads.get(x, 2)
+        parts = t.chunk(copies, axis)
+        same = torch.stack([torch.equal(p.nan_to_num(), parts[0].nan_to_num()) and
+                            torch.equal(p.isnan(), parts[0].isnan()) and torch.tensor(True)
+                            for p in parts[1:]] or [torch.tensor(True)])
+        assert same.all(), f"{x}: copies of a head differ"
+        out[x] = parts[0].cpu()
+    return out
+
+
+def compare(out, ref):
+    print({x: round(check(x, out[x], ref[x]), 3) for x in ref})
+
+
+# copies of two heads, so that few and many workgroups (the 32-row and the 128-row
+# forms of the backward passes) both occur
+EMPTY = [(BF, 3, 64, 1), (BF, 150, 64, 1), (BF, 150, 64, 66), (BF, 150, 128, 1), (BF, 150, 128, 66),
+         (HF, 140, 64, 66), (HF, 140, 200, 1), (F4, 70, 40, 1), (F4, 130, 64, 66), (F4, 40, 128, 1)]
+
+
+@pytest.mark.parametrize("dtype,n,d,copies", EMPTY)
+def test_rows_that_see_no_key_poison_nothing(fs, dtype, n, d, copies):
+    """Rows before the first key of a causal limit, or behind a left padding of
+    masked keys, hold NaN and infinities in q, d_o and d_lse."""
+    g = torch.Generator().manual_seed(n + d)
+    B, m, H = 2, n + 9, 2
+    q, k, v, d_o = (randn(g, B, r, H, d, dtype=dtype) for r in (n, m, m, n))
+    d_lse = randn(g, B, H, n)
+    # entry 0: the first rows stand before the keys; entry 1: left padding
+    lost = max(1, n // 3)
+    kw = {"causal": True, "offsets": torch.tensor([-lost, 0], dtype=torch.int32),
+          "key_mask": torch.ones(B, m, dtype=torch.uint8)}
+    kw["key_mask"][1, :lost] = 0
+    ref = reference(q, k, v, d_o=d_o, d_lse=d_lse, **kw)
+    assert torch.all(ref["lse"][0][:, :, :lost] == -INF) and torch.all(ref["lse"][0][:, :, lost:] > -INF)
+    q[0, :lost], q[1, :lost] = NAN, INF
+    d_o[0, :lost], d_o[1, :lost] = INF, NAN
+    d_lse[:, :, :lost] = NAN
+    out = run(fs, q, k, v, d_o, d_lse, copies, **kw)
+    compare(out, ref)
+    assert torch.all(out["d_q"][:, :lost] == 0)
+
+
+@pytest.mark.parametrize("dtype,n,d,copies", EMPTY)
+def test_rows_emptied_by_the_bias_poison_nothing(fs, dtype, n, d, copies):
+    """Rows whose every key stands in a bucket without weight: d_o and d_lse there
+    may hold anything."""
+    g = torch.Generator().manual_seed(n + d)
+    m, H = max(2, n // 2), 2
+    q, k, v, d_o = (randn(g, 2, r, H, d, dtype=dtype) for r in (n, m, m, n))
+    d_lse = randn(g, 2, H, n)
+    bias = randn(g, 8, H)
+    bias[:4, 1] = -INF  # the second head sees later keys only
+    kw = {"bias": bias, "edges": [1, 3, 8], "two_sided": True}
+    ref = reference(q, k, v, d_o=d_o, d_lse=d_lse, **kw)
+    empty = ref["lse"][0] == -INF
+    assert empty[:, 1, m - 1:].all() and not empty[:, 1, :m - 1].any() and not empty[:, 0].any()
+    d_o[:, m - 1:, 1] = torch.where(torch.arange(n - m + 1) % 2 == 0, NAN, INF)[:, None].to(dtype)
+    d_lse[:, 1, m - 1:] = NAN
+    out = run(fs, q, k, v, d_o, d_lse, copies, **kw)
+    compare(out, ref)
+    assert torch.all(out["d_q"][:, m - 1:, 1] == 0)
