@@ -200,6 +200,7 @@ struct KvPass {
         const int len = attn_kv_len(a, b), qlen = attn_q_len(a, b);
         j0 = kb * ROWS + (ALONE ? 0 : wid * 32), j = j0 + (lane & 31);
         key_ok = j < len;
+        if (a.causal) key_ok = key_ok && j < qlen + off;  // some row sees it
         if (key_ok && a.key_mask) key_ok = a.key_mask[b * a.mask_stride + j] != 0;
         // tiles of this workgroup's query range, from the first that sees a key
         // of this block on
@@ -609,10 +610,11 @@ struct QPass {
         line.a = lds_addr(line_mem);
         off = attn_offset(a, b);
         i0 = qb * ROWS + (ALONE ? 0 : wid * 32), i = i0 + (lane & 31);
-        row_ok = i < attn_q_len(a, b);
+        const int qlen = attn_q_len(a, b);
+        row_ok = i < qlen;
         in = i < a.n;
         len = attn_kv_len(a, b);
-        if (a.causal) len = min(len, max(0, min((qb + 1) * ROWS, a.n) + off));
+        if (a.causal) len = min(len, max(0, min((qb + 1) * ROWS, qlen) + off));
         lrow = ((int64_t)b * a.H + head) * a.n_pad + i;
         rl = in ? a.nl2[lrow] : -INFINITY;
         rd = in ? a.delta[lrow] : 0.f;

@@ -86,9 +86,11 @@ struct FwdPass {
         line.a = lds_addr(line_mem);
         off = attn_offset(a, b);
         i0 = qb * kAttnRows + wid * 32, i = i0 + (lane & 31);
-        row_ok = i < attn_q_len(a, b);
+        const int qlen = attn_q_len(a, b);
+        row_ok = i < qlen;
         int len = attn_kv_len(a, b);
-        if (a.causal) len = min(len, max(0, min(qb * kAttnRows + kAttnRows, a.n) + off));
+        // (keys that only rows behind qlen would see are not read)
+        if (a.causal) len = min(len, max(0, min(qb * kAttnRows + kAttnRows, qlen) + off));
         jb = split * a.split_keys;
         je = a.n_split == 1 ? len : min(len, jb + a.split_keys);
     }
@@ -463,9 +465,10 @@ void attn_rows_kernel(const AttnArgs a) {
     const int rho = rb * 32 + (lane & 31);
     const int g = min(rho, rows - 1) / a.n, i = min(rho, rows - 1) - g * a.n;
     const int head = kvh * a.G + g;
-    const bool row_ok = rho < rows && i < attn_q_len(a, b);
+    const int qlen = attn_q_len(a, b);
+    const bool row_ok = rho < rows && i < qlen;
     int len = attn_kv_len(a, b);
-    if (a.causal) len = min(len, max(0, a.n + off));
+    if (a.causal) len = min(len, max(0, qlen + off));
     const int jb = split * a.split_keys;
     const int je = a.n_split == 1 ? len : min(len, jb + a.split_keys);
 
@@ -588,7 +591,7 @@ void attn_rows_kernel(const AttnArgs a) {
     const int orho = rb * 32 + q;
     if (orho >= rows) return;
     const int og = orho / a.n, oi = orho - og * a.n, ohead = kvh * a.G + og;
-    const bool ok = oi < attn_q_len(a, b);
+    const bool ok = oi < qlen;
     float ref = -INFINITY;
 #pragma unroll
     for (int x = 0; x < NW; ++x) ref = fmaxf(ref, wref[x][q]);

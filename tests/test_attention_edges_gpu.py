@@ -99,3 +99,24 @@ def test_rows_emptied_by_the_bias_poison_nothing(fs, dtype, n, d, copies):
     out = run(fs, q, k, v, d_o, d_lse, copies, **kw)
     compare(out, ref)
     assert torch.all(out["d_q"][:, m - 1:, 1] == 0)
+
+
+@pytest.mark.parametrize("dtype,n,d,copies", EMPTY)
+def test_keys_that_no_row_sees_poison_nothing(fs, dtype, n, d, copies):
+    """A causal limit and lengths of the queries alone: keys behind the last query
+    row are seen by padding only and may hold anything."""
+    g = torch.Generator().manual_seed(n + d)
+    B, m, H = 3, n + 9, 2
+    q, k, v, d_o = (randn(g, B, r, H, d, dtype=dtype) for r in (n, m, m, n))
+    lens = [max(1, n // 2), n - 1, 0]
+    kw = {"causal": True, "offsets": torch.tensor([0, 3, 5], dtype=torch.int32),
+          "q_len": torch.tensor(lens, dtype=torch.int32)}
+    ref = reference(q, k, v, d_o=d_o, **kw)
+    for t in (k, v):
+        t[0, lens[0]:] = NAN
+        t[1, lens[1] + 3:] = INF
+        t[2] = -INF
+    out = run(fs, q, k, v, d_o, copies=copies, **kw)
+    compare(out, ref)
+    for x in ("d_k", "d_v"):
+        assert torch.all(out[x][0, lens[0]:] == 0) and torch.all(out[x][1, lens[1] + 3:] == 0)
