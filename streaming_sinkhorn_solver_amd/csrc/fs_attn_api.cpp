@@ -242,6 +242,14 @@ fs_status take_desc(const fs_attention_desc* p, AttnArgs& a) {
         a.q_split = (int)cdiv(d.n, a.split_rows);
     }
     a.line_blocks = (int)(a.q_split * kblocks);
+    // The traversals number their workgroups along one dimension, where a launch
+    // has fewer than 2^32 threads (the largest takes one workgroup for every 32
+    // rows of a key head at least, 128 of a head, or 32 keys).
+    const int64_t fwd = items * a.n_split * (few && row <= 128 ? 512 : 256);
+    const int64_t bwd_q = (int64_t)d.batch * d.heads * cdiv(d.n, a.alone_q ? 32 : kAttnRows) * 256;
+    const int64_t bwd_k = kitems * a.q_split * 256;
+    if (std::max({fwd, bwd_q, bwd_k}) >= (int64_t)1 << 32)
+        return fail(FS_ERR_INVALID_ARG, "batch * heads is too large: a launch has fewer than 2^32 threads");
     return FS_OK;
 }
 

@@ -57,6 +57,17 @@ struct AttnArgs {
     float* gbias;             // [buckets][H]
 };
 
+// Grid of `blocks` workgroups over two dimensions: a launch may have fewer than
+// 2^32 threads along each (flat_block gives the workgroup's number).
+inline dim3 flat_grid(int64_t blocks) {
+    constexpr int64_t kRow = 1 << 20;
+    return blocks <= kRow ? dim3((unsigned)blocks)
+                          : dim3((unsigned)kRow, (unsigned)((blocks + kRow - 1) / kRow));
+}
+__device__ __forceinline__ int64_t flat_block() {
+    return (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+}
+
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t s);
 hipError_t launch_attn_rows(const AttnArgs& a, hipStream_t s);
 hipError_t launch_attn_merge(const AttnArgs& a, hipStream_t s);

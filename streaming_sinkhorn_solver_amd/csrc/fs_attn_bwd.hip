@@ -24,7 +24,7 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(const AttnArgs a) {
     using T = typename El<OP>::T;
     constexpr int EPC = 16 / sizeof(T);
     const int64_t rows = (int64_t)a.B * a.n_pad * a.H;
-    const int64_t r = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const int64_t r = flat_block() * 16 + (threadIdx.x >> 4);
     const int lane = threadIdx.x & 15;
     if (r >= rows) return;
     const int head = (int)(r % a.H);
@@ -893,7 +893,7 @@ hipError_t launch_attn_bwd_q(const AttnArgs& a, hipStream_t s) { FS_ATTN_DISPATC
 
 hipError_t launch_attn_delta(const AttnArgs& a, hipStream_t s) {
     const int64_t rows = (int64_t)a.B * a.n_pad * a.H;
-    const unsigned g = (unsigned)((rows + 15) / 16);
+    const dim3 g = flat_grid((rows + 15) / 16);
     if (a.op == OP_BF16)
         attn_delta_kernel<OP_BF16><<<g, 256, 0, s>>>(a);
     else if (a.op == OP_F16)

@@ -641,7 +641,7 @@ __global__ __launch_bounds__(256) void attn_merge_kernel(const AttnArgs a) {
     __shared__ float weight[8][kAttnMaxSplit];
     const int64_t rows = (int64_t)a.B * a.H * a.n;
     const int grp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 8 + grp;
+    const int64_t row = flat_block() * 8 + grp;
     if (row >= rows) return;
     // lane s, s + 32: the ranges' references and sums
     float2 ml[kAttnMaxSplit / 32];
@@ -741,7 +741,7 @@ hipError_t launch_attn_rows(const AttnArgs& a, hipStream_t s) { return dispatch(
 
 hipError_t launch_attn_merge(const AttnArgs& a, hipStream_t s) {
     const int64_t rows = (int64_t)a.B * a.H * a.n;
-    const unsigned g = (unsigned)((rows + 7) / 8);
+    const dim3 g = flat_grid((rows + 7) / 8);
     if (a.op == OP_BF16)
         attn_merge_kernel<OP_BF16><<<g, 256, 0, s>>>(a);
     else if (a.op == OP_F16)

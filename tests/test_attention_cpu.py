@@ -167,3 +167,17 @@ def test_bad_norm_tensors(lib):
     assert back(*d, size=need - 1) == binding.FS_ERR_WORKSPACE
     assert back(d[0], rows(DQ, 5, 2, 64)) == inv
     assert back(*d, gw=DQ) == inv and back(g[0], d[1]) == inv
+
+
+@pytest.mark.parametrize("kw", [dict(batch=1 << 18, heads=32, kv_heads=32, n=1),    # few rows
+                                dict(batch=1 << 18, heads=64, kv_heads=2, n=100),   # many rows
+                                dict(batch=1 << 23, heads=2, kv_heads=2, n=1, m=100)])
+def test_more_threads_than_a_launch_has(lib, kw):
+    a = desc(**kw)
+    for call in (forward, backward):
+        assert call(lib, a) == binding.FS_ERR_INVALID_ARG
+        assert "2^32 threads" in binding.fs_last_error()
+    assert lib.fs_attention_workspace_bytes(ctypes.byref(a), 0) == 0
+    # half of it is fine
+    a.batch //= 4
+    assert lib.fs_attention_workspace_bytes(ctypes.byref(a), 0) > 0
