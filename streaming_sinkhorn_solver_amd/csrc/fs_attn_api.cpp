@@ -498,9 +498,11 @@ fs_status take_norm_desc(const fs_qk_norm_desc* p, NormArgs& a) {
     if (d.positions && (d.positions_stride < 0 ||
                         (d.batch > 1 && d.positions_stride > 0 && d.positions_stride < d.n)))
         return fail(FS_ERR_INVALID_ARG, "positions_stride must be 0 or at least n");
-    if ((int64_t)d.batch * d.n > ((int64_t)1 << 31) / 256 * 8 ||
+    // an item is a token's heads, or part of them: their number and the tokens' in
+    // 32 bits
+    if ((int64_t)d.batch * d.n > 1 << 26 ||
         (int64_t)d.batch * d.n * ((int64_t)d.heads_q + d.heads_k) > ((int64_t)1 << 31))
-        return fail(FS_ERR_INVALID_ARG, "batch * n * heads is beyond 2^31");
+        return fail(FS_ERR_INVALID_ARG, "batch * n is beyond 2^26, or with the heads beyond 2^31");
     a.op = op_of(d.dtype);
     a.B = d.batch;
     a.n = d.n;

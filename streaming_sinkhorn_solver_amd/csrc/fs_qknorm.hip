@@ -187,7 +187,7 @@ __global__ __launch_bounds__(256) void norm_rotate_kernel(const NormArgs a) {
     using Item = NormItem<LPR, U>;
     const NormRows& R = a.r[blockIdx.y];
     if (R.heads == 0) return;
-    const Item it(a, R.heads, blockIdx.x * 4 + wave_id());
+    const Item it(a, R.heads, (blockIdx.z * gridDim.x + blockIdx.x) * 4 + wave_id());
     if (!it.any) return;
     const int p0 = 4 * (threadIdx.x % LPR);
     const bool wide = R.x.vec && R.y.vec && a.rot % 8 == 0 && a.d % 8 == 0;
@@ -375,7 +375,7 @@ hipError_t fwd(const NormArgs& a, hipStream_t s) {
     const bool many = (int64_t)a.B * a.n * (a.r[0].heads + a.r[1].heads) >= kManyRows;
     const int64_t n = items(a, LPR, many ? 4 : 1);
     if (n == 0) return hipSuccess;
-    const dim3 g((unsigned)((n + 3) / 4), 2);
+    const dim3 f = flat_grid((n + 3) / 4), g(f.x, 2, f.y);
     if (many)
         norm_rotate_kernel<OP, LPR, 4><<<g, 256, 0, s>>>(a);
     else

@@ -1,9 +1,9 @@
-"""Attention at row counts whose launches pass 2^32 threads in one dimension if laid
-out flat."""
+"""Attention and norm + rotation at row counts whose launches pass 2^32 threads in one
+dimension if laid out flat."""
 import pytest
 import torch
 
-from attention_reference import check, reference
+from attention_reference import check, norm_reference, reference
 from test_attention_gpu import BF
 
 pytestmark = pytest.mark.gpu
@@ -33,3 +33,22 @@ def test_single_rows_of_many_sequences(fs):
     ref = reference(*(pick(t) for t in (q, k, v)), d_o=pick(d_o))
     for x, t in (("o", o), ("lse", lse), ("d_q", dq), ("d_k", dk), ("d_v", dv)):
         check(x, pick(t), ref[x])
+
+
+def test_norm_of_many_tokens(fs):
+    """2^26 tokens of one head, the most that a call takes."""
+    n, d = 1 << 26, 2
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(1, n, 1, d, generator=g, device="cuda").to(BF)
+    y = torch.full_like(x, float("nan"))
+    w = torch.rand(d, generator=g, device="cuda") + 0.5
+    fs.fs_qk_norm_rotate(x, None, w, None, y, None, eps=1e-5)
+    torch.cuda.synchronize()
+    for lo in range(0, n, n // 8):
+        part = x[:, lo:lo + n // 8].float()
+        want = part * torch.rsqrt((part * part).mean(-1, keepdim=True) + 1e-5) * w
+        # one rounding to bf16, fp32 before it
+        assert torch.all((y[:, lo:lo + n // 8].float() - want).abs() <= want.abs() * 1.01 * 2.0 ** -8)
+    ends = torch.cat((x[:, :3], x[:, -3:]), 1).cpu()
+    ref = norm_reference(ends, w.cpu(), None, None, None, 1e-5, False)
+    check("y", torch.cat((y[:, :3], y[:, -3:]), 1), ref["y"])
