@@ -416,9 +416,10 @@ int norm_bwd_blocks(int64_t rows) {
 hipError_t launch_norm_rotate(const NormArgs& a, hipStream_t s) { return launch(a, false, s); }
 
 hipError_t launch_norm_rotate_bwd(const NormArgs& a, hipStream_t s) {
-    const hipError_t e = launch(a, true, s);
+    const bool any = (int64_t)a.B * a.n > 0;  // else the weights' sums are empty
+    const hipError_t e = any ? launch(a, true, s) : hipSuccess;
     if (e != hipSuccess || (!a.r[0].gw && !a.r[1].gw)) return e;
-    norm_weight_kernel<<<dim3((unsigned)((a.d + 7) / 8), 2), 256, 0, s>>>(a, a.blocks);
+    norm_weight_kernel<<<dim3((unsigned)((a.d + 7) / 8), 2), 256, 0, s>>>(a, any ? a.blocks : 0);
     return hipGetLastError();
 }
 

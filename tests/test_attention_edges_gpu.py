@@ -120,3 +120,19 @@ def test_keys_that_no_row_sees_poison_nothing(fs, dtype, n, d, copies):
     compare(out, ref)
     for x in ("d_k", "d_v"):
         assert torch.all(out[x][0, lens[0]:] == 0) and torch.all(out[x][1, lens[1] + 3:] == 0)
+
+
+@pytest.mark.parametrize("B,n", [(2, 0), (0, 3), (0, 0)])
+def test_norm_of_no_tokens(fs, B, n):
+    """Nothing to write but the weights' gradients, sums of nothing."""
+    q, k = torch.empty(B, n, 4, 64, device="cuda"), torch.empty(B, n, 2, 64, device="cuda")
+    w = torch.ones(64, device="cuda")
+    dw = [torch.full_like(w, NAN) for _ in range(2)]
+    empty = [torch.empty_like(t) for t in (q, k)]
+    fs.fs_qk_norm_rotate(q, k, w, w, *empty)
+    fs.fs_qk_norm_rotate_backward(q, k, w, w, q, k, *empty, *dw)
+    # (and with a workspace full of NaN)
+    ws = torch.full((fs.fs_qk_norm_workspace_bytes(q, k),), 0xFF, dtype=torch.uint8, device="cuda")
+    fs.fs_qk_norm_rotate_backward(q, k, w, None, q, k, *empty, dw[0], None, workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.all(dw[0] == 0) and torch.all(dw[1] == 0)
