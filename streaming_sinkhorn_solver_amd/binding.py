@@ -742,10 +742,21 @@ _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _NO_ROWS = Rows(None, 0, 0, 0)
 
 
+_MAX = 0x7fffffff
+
+
+def _i32(name: str, *values: int):
+    """The values are numbers of 32 bits (ctypes would cut off the rest)."""
+    for x in values:
+        if not -_MAX - 1 <= x <= _MAX:
+            raise ValueError(f"{name} is beyond 32 bits (got {x})")
+
+
 def fs_bucket_edges(side_buckets: int, max_distance: int) -> list:
     """The edges of one side's buckets: one distance each for the first half,
     then evenly spaced in the logarithm up to max_distance."""
-    out = (ctypes.c_int32 * max(side_buckets, 1))()
+    _i32("side_buckets or max_distance", side_buckets, max_distance)
+    out = (ctypes.c_int32 * min(max(side_buckets, 1), 64))()
     _check(load().fs_bucket_edges(side_buckets, max_distance, out), "fs_bucket_edges")
     return list(out[:side_buckets - 1])
 
@@ -836,6 +847,8 @@ def _attention_desc(q, k, v, scale, causal, offset, offsets, q_len, kv_len, key_
     dv = v.shape[3]
     lens = (batch,)
     i32 = torch.int32
+    if offset or batch > _MAX or n > _MAX or m > _MAX:
+        _i32("a size or the offset", batch, n, m, offset)
     a = AttentionDesc(dtype, batch, n, m, heads, kv_heads, d, dv,
                       d ** -0.5 if scale is None else scale, 1 if causal else 0, offset)
     if offsets is not None:
@@ -856,6 +869,7 @@ def _attention_desc(q, k, v, scale, causal, offset, offsets, q_len, kv_len, key_
         e = [] if edges is None else edges
         buckets = (len(e) + 1) * (2 if two_sided else 1)
         a.bias = _flat(bias, "bias", dev, torch.float32, (buckets, heads))
+        _i32("an edge", *e)
         a.edges = (ctypes.c_int32 * max(len(e), 1))(*e)
         a.n_edges = len(e)
         a.two_sided = bool(two_sided)
@@ -868,6 +882,7 @@ def fs_attention_workspace_bytes(q: torch.Tensor, k: torch.Tensor, v: torch.Tens
     tensors of these shapes; edges: the bias's (None without a bias)."""
     if q.dtype not in _DTYPES:
         raise TypeError(f"q must be float32, bfloat16 or float16 (is {q.dtype})")
+    _i32("a size or an edge", q.shape[0], q.shape[1], k.shape[1], *(edges or ()))
     a = AttentionDesc(_DTYPES[q.dtype], q.shape[0], q.shape[1], k.shape[1], q.shape[2],
                       k.shape[2], q.shape[3], v.shape[3], 1.0)
     if edges is not None:
@@ -949,6 +964,8 @@ def _norm_desc(q, k, eps, cos, sin, positions, offset, interleaved):
         raise ValueError("q and k must be [batch, rows, heads, d]")
     dev = like.get_device()
     batch, n, _, d = like.shape
+    if offset or batch > _MAX or n > _MAX:
+        _i32("a size or the offset", batch, n, offset)
     a = QkNormDesc(dtype, batch, n, 0 if q is None else q.shape[2], 0 if k is None else k.shape[2],
                    d, 0, 1 if interleaved else 0, eps)
     if (cos is None) != (sin is None):

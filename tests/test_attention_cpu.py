@@ -181,3 +181,23 @@ def test_more_threads_than_a_launch_has(lib, kw):
     # half of it is fine
     a.batch //= 4
     assert lib.fs_attention_workspace_bytes(ctypes.byref(a), 0) > 0
+
+
+def test_numbers_beyond_32_bits():
+    """The binding refuses what would reach the library as another number."""
+    import torch
+
+    one = torch.zeros(1, 1, 1, 32)
+    long = one.expand(1, (1 << 32) + 7, 1, 32)
+    size = binding.fs_attention_workspace_bytes
+    assert size(one, one, one) == 256
+    for args, kw in (((long, one, one), {}), ((one, long, long), {}),
+                     ((one, one, one), {"edges": [1, (1 << 32) + 2]})):
+        with pytest.raises(ValueError, match="32 bits"):
+            size(*args, **kw)
+    with pytest.raises(ValueError, match="32 bits"):
+        binding.fs_bucket_edges((1 << 32) + 16, 128)
+    with pytest.raises(ValueError, match="32 bits"):
+        binding.fs_bucket_edges(16, (1 << 32) + 128)
+    with pytest.raises(binding.FsError):
+        binding.fs_bucket_edges(1 << 30, 128)

@@ -136,3 +136,23 @@ def test_norm_of_no_tokens(fs, B, n):
     fs.fs_qk_norm_rotate_backward(q, k, w, None, q, k, *empty, dw[0], None, workspace=ws)
     torch.cuda.synchronize()
     assert torch.all(dw[0] == 0) and torch.all(dw[1] == 0)
+
+
+def test_numbers_beyond_32_bits_are_refused(fs):
+    """An offset, an edge or a size that 32 bits do not hold is no other number."""
+    q = torch.randn(1, 4, 2, 32, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(1, 2, 4, device="cuda")
+    bias = torch.zeros(3, 2, device="cuda")
+    for kw in (dict(offset=1 << 32), dict(offset=-(1 << 32) - 1),
+               dict(bias=bias, edges=[1, (1 << 32) + 2], two_sided=False)):
+        with pytest.raises(ValueError, match="32 bits"):
+            fs.fs_attention_forward(q, q, q, o, lse, causal=True, **kw)
+        with pytest.raises(ValueError, match="32 bits"):
+            fs.fs_attention_backward(q, q, q, o, lse, o, torch.empty_like(q), causal=True, **kw)
+    many = q[:, :1].expand(-1, (1 << 32) + 4, -1, -1)
+    with pytest.raises(ValueError, match="32 bits"):
+        fs.fs_attention_forward(q, many, many, o, lse)
+    with pytest.raises(ValueError, match="32 bits"):
+        fs.fs_qk_norm_rotate(q, None, None, None, o, None, offset=1 << 32)
+    with pytest.raises(ValueError, match="32 bits"):
+        fs.fs_qk_norm_rotate(many, None, None, None, many, None)
