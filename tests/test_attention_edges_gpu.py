@@ -15,20 +15,22 @@ pytestmark = pytest.mark.gpu
 NAN, INF = math.nan, math.inf
 
 
-def run(fs, q, k, v, d_o=None, d_lse=None, copies=1, **kw):
+def run(fs, q, k, v, d_o=None, d_lse=None, copies=1, view=None, **kw):
     """Outputs of the first heads, on the CPU, as a dict; with copies > 1 every
-    head stands that many times in the call and all copies are compared."""
-    rep = lambda t: t.cuda().repeat(1, 1, copies, 1)
+    head stands that many times in the call and all copies are compared.
+    view(t): the device tensor to pass in t's place (same values)."""
+    view = view or (lambda t: t)
+    rep = lambda t: view(t.cuda().repeat(1, 1, copies, 1))
     Q, K, V = rep(q), rep(k), rep(v)
     dev = {x: gpu(y) for x, y in kw.items()}
     B, n, H, _ = Q.shape
     nan = lambda *s, dtype=q.dtype: torch.full(s, NAN, dtype=dtype, device="cuda")
     if kw.get("bias") is not None:
         dev["bias"] = dev["bias"].repeat(1, copies)
-    out = {"o": nan(B, n, H, v.shape[3]), "lse": nan(B, H, n, dtype=F4)}
+    out = {"o": view(nan(B, n, H, v.shape[3])), "lse": nan(B, H, n, dtype=F4)}
     fs.fs_attention_forward(Q, K, V, out["o"], out["lse"], **dev)
     if d_o is not None:
-        out["d_q"], out["d_k"], out["d_v"] = (nan(*t.shape) for t in (Q, K, V))
+        out["d_q"], out["d_k"], out["d_v"] = (view(nan(*t.shape)) for t in (Q, K, V))
         if kw.get("bias") is not None:
             out["d_bias"] = nan(*dev["bias"].shape, dtype=F4)
         g = None if d_lse is None else d_lse.cuda().repeat(1, copies, 1)
