@@ -149,8 +149,9 @@ fs_status take_desc(const fs_attention_desc* p, AttnArgs& a) {
     if (d.d < 1 || d.d > wmax || d.dv < 1 || d.dv > wmax)
         return fail(FS_ERR_INVALID_ARG, "d and dv must be in [1, %d] for this type (got %d, %d)",
                     wmax, d.d, d.dv);
-    if (!(d.scale > 0.f) || !std::isfinite(d.scale))
-        return fail(FS_ERR_INVALID_ARG, "scale must be positive and finite");
+    constexpr float kLog2E = 1.4426950408889634f;  // scores are kept in base 2
+    if (!(d.scale > 0.f) || !std::isfinite(d.scale * kLog2E))
+        return fail(FS_ERR_INVALID_ARG, "scale must be positive and at most 2e38");
     if (d.offset < -kAttnMaxOffset || d.offset > kAttnMaxOffset)
         return fail(FS_ERR_INVALID_ARG, "offset must be within +-2^29 (got %d)", d.offset);
     if (d.key_mask && d.key_mask_stride < 0)
@@ -169,7 +170,7 @@ fs_status take_desc(const fs_attention_desc* p, AttnArgs& a) {
     a.n_pad = (int)(cdiv(d.n, kAttnRowPad) * kAttnRowPad);
     a.dv_pad = (d.dv + 3) / 4 * 4;
     a.scale = d.scale;
-    a.c = d.scale * 1.4426950408889634f;
+    a.c = d.scale * kLog2E;
     a.causal = d.causal != 0;
     a.offset = d.offset;
     a.q_len = d.q_len;

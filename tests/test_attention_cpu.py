@@ -201,3 +201,12 @@ def test_numbers_beyond_32_bits():
         binding.fs_bucket_edges(16, (1 << 32) + 128)
     with pytest.raises(binding.FsError):
         binding.fs_bucket_edges(1 << 30, 128)
+
+
+def test_scales_that_leave_the_range(lib):
+    """A finite scale that times log2 e is not finite would make every score NaN."""
+    for scale, ok in ((1e-38, True), (2e38, True), (3e38, False), (float("inf"), False)):
+        a = desc(scale=scale)
+        assert (lib.fs_attention_workspace_bytes(ctypes.byref(a), 0) > 0) == ok
+        if not ok:
+            assert forward(lib, a) == binding.FS_ERR_INVALID_ARG and "scale" in binding.fs_last_error()
