@@ -341,11 +341,13 @@ __device__ __forceinline__ void dma_wait_but() {
 // bit in `seen` is clear are filled with zeros and never read: what stands
 // there (NaN in padding, memory behind the tensor) cannot enter a product.
 // Aligned rows (vec) go straight to LDS and are complete after dma_wait();
-// others are loaded element by element and stored at once.  ANEW: the places of a
-// thread are formed at every fill, for kernels without registers to keep them
-// (put into memory, they are read again between the copies, and each time that
-// waits for the copies before).
-template <int OP, int DP, int ROWS, int NT, bool ANEW = false>
+// others are loaded element by element and stored at once.  A thread's places in a
+// tile are the same at every fill and the compiler would keep them; for kernels
+// without the registers they are formed anew: those of the element path only, or
+// of both (kept in memory, they are read again between the copies, and each read
+// waits for the copies before it).
+enum Places { PLACES_KEPT, PLACES_KEPT_WIDE, PLACES_ANEW };
+template <int OP, int DP, int ROWS, int NT, Places PLACES = PLACES_KEPT>
 struct Loader {
     using L = Tile<OP, DP>;
     using T = typename El<OP>::T;
@@ -356,8 +358,8 @@ struct Loader {
 
     static __device__ __forceinline__ void fill(uint32_t lds, const T* base, int64_t stride,
                                                 uint64_t seen, int w, bool vec, int t) {
-        if (ANEW) asm volatile("" : "+v"(t));
-        const int c0 = t % L::kCh, r0 = t / L::kCh;
+        if (PLACES == PLACES_ANEW) asm volatile("" : "+v"(t));
+        int c0 = t % L::kCh, r0 = t / L::kCh;
         const uint32_t dst = lds + (NT == 64 ? 0 : wave_id() * 1024);
         if (vec) {
             const char* src = (const char*)(base + r0 * stride);
@@ -375,6 +377,10 @@ struct Loader {
                 }
             }
         } else {
+            if (PLACES == PLACES_KEPT_WIDE) {
+                asm volatile("" : "+v"(t));
+                c0 = t % L::kCh, r0 = t / L::kCh;
+            }
 #pragma unroll
             for (int s = 0; s < kN; ++s) {
                 const int r = r0 + s * kStep, c = c0 ^ L::swz(r);
