@@ -26,7 +26,14 @@
  *    replay uses the same buffers: two captured calls that may overlap need a
  *    workspace each).  Equal calls give equal bits: no sum depends on the
  *    order in which workgroups run.
- *  - Sums, softmax statistics and norms are fp32.
+ *  - Sums, softmax statistics and norms are fp32 (sums over workgroups' parts of
+ *    a weight's or a bias's gradient in 64 bits).  In a 16-bit type the weights P
+ *    and dS are rounded to that type before their products with v, d_o, q and k,
+ *    as the matrix units take them; an output is rounded once more.  Against the
+ *    definition in 64 bits that gives about 1.4 times the error of a product in
+ *    fp32 rounded once (bf16: 0.0023 against 0.0017 relative).
+ *  - A launch has fewer than 2^32 threads: batch * heads may reach about 2^23 with
+ *    few rows, and batch * heads * rows 2^31; more is refused.
  */
 #ifndef FS_ATTENTION_H
 #define FS_ATTENTION_H
@@ -52,15 +59,16 @@ typedef struct {
  *   O_i  = sum_j exp(s_ij - L_i) v_j
  * over the visible keys: j < kv_len[b], key_mask[b][j] != 0 and, if causal,
  * j <= i + offset_b.  Rows i >= q_len[b] and rows without a visible key give
- * O = 0 and L = -inf and take part in no gradient; q, k, v and gradient values
- * of rows behind q_len / kv_len and of masked keys are not used, whatever
- * they hold. */
+ * O = 0 and L = -inf and take part in no gradient.  Not used, whatever they hold
+ * (NaN, infinities): q, d_o and d_lse of such rows (but q of a row that only the
+ * bias empties), and k and v of keys that no row sees.  A key that some row sees
+ * is read for the rows around it too: if it holds NaN, they may. */
 typedef struct {
     int32_t dtype;            /* fs_dtype of q, k, v, o and their gradients */
     int32_t batch, n, m;      /* >= 0; n, m <= 2^28 */
-    int32_t heads, kv_heads;  /* >= 1, heads a multiple of kv_heads */
+    int32_t heads, kv_heads;  /* >= 1, heads a multiple of kv_heads and <= 65535 */
     int32_t d, dv;            /* widths of q, k and of v, o: 1..256 (fp32: 1..128) */
-    float scale;              /* > 0 */
+    float scale;              /* > 0, <= 2e38 */
     int32_t causal;
     int32_t offset;           /* position of query row 0 among the keys, |.| <= 2^29 */
     const int32_t* offsets;   /* device [batch], in place of offset; or NULL */
@@ -74,7 +82,9 @@ typedef struct {
      * (n_edges + 1 buckets: keys after the query count as distance 0), or
      * two-sided u(|r|) for r <= 0 and n_edges + 1 + u(r) for r > 0
      * (2 (n_edges + 1) buckets).  bias: device fp32 [buckets][heads], or NULL
-     * for none.  An entry of -1e30 or less gives its pairs no weight. */
+     * for none.  An entry of -1e30 or less gives its pairs no weight; others are
+     * finite and at most 2e38.  The bias speaks of positions: it is for rows and
+     * keys that have an order, such as points along a curve or a scan. */
     const float* bias;
     const int32_t* edges;
     int32_t n_edges;          /* 0..255 */
@@ -127,12 +137,12 @@ fs_status fs_attention_backward(const fs_attention_desc* desc, fs_rows q, fs_row
  * not turned.  Either q or k may be left out (heads 0). */
 typedef struct {
     int32_t dtype;               /* fs_dtype of x and y */
-    int32_t batch, n;            /* >= 0 */
-    int32_t heads_q, heads_k;    /* >= 0, either may be 0 */
+    int32_t batch, n;            /* >= 0, batch * n <= 2^26 */
+    int32_t heads_q, heads_k;    /* >= 0, either may be 0; batch * n * their sum <= 2^31 */
     int32_t d;                   /* 2..256, even */
     int32_t rot;                 /* 0..d, even; 0: no rotation */
     int32_t interleaved;
-    float eps;                   /* >= 0 */
+    float eps;                   /* >= 0 (0: a row of zeros gives NaN) */
     const float* cos_table;      /* device fp32 [n_pos][rot / 2] (NULL if rot == 0) */
     const float* sin_table;
     int32_t n_pos;               /* >= 1 if rot > 0 */

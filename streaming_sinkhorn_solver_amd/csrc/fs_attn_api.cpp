@@ -124,7 +124,12 @@ int tile_row(const fs_attention_desc& d) {
 // rows if they are narrow and fill few workgroups of the other (measured, us,
 // few-row against the other: 8 x 1024 rows of 64, 1024 keys, 11.6 / 16.8; 2 x 8
 // x 500 fp32 rows of 48, 700 keys, 25.7 / 48.5; but 8 x 4 x 512 rows of 128,
-// 2048 keys, 62.5 / 38.4 and 16 x 48 rows of 128, 8192 keys, 35.0 / 22.3).
+// 2048 keys, 62.5 / 38.4 and 16 x 48 rows of 128, 8192 keys, 35.0 / 22.3).  The
+// border, at 512 rows of 64 a head by the other's workgroups (few-row / other):
+//   workgroups        32           64          128          256          512
+//   bf16, 700 keys    16.5 / 17.8  11.5 / 19.4 20.3 / 22.8  37.8 / 18.8  73.5 / 25.2
+//   bf16, 2048 keys   17.1 / 17.4  16.6 / 21.6 31.2 / 31.0  61.3 / 41.7   120 / 54.4
+//   fp32 (48), 700    20.9 / 47.8  27.6 / 49.0 50.5 / 52.5   103 / 59.7   203 / 106
 bool few_rows(const fs_attention_desc& d) {
     if (d.n <= kAttnFewRows) return true;
     return d.d <= 64 && d.dv <= 64 && (int64_t)d.batch * d.heads * cdiv(d.n, kAttnRows) <= 64;
@@ -227,6 +232,18 @@ fs_status take_desc(const fs_attention_desc* p, AttnArgs& a) {
     // buffer a wave and pay only where 128 rows leave most CUs idle (us, 32 /
     // 128 rows: 2 x 2 x 1024 keys of 128, 256 queries, 30.5 / 48.2, but 8 x 2048
     // keys, 128 queries, 29.3 / 16.6; 4 x 8 x 2048 keys, 512 queries, 151 / 64).
+    // The borders (us, 32 / 128 rows, row terms included) by workgroups of 128 rows,
+    // the queries' pass at 512 rows and 700 keys a head, the keys' at 512 rows:
+    //   queries     64          128         256         512
+    //   bf16, 64    16.1/24.1   17.8/24.5   30.4/26.4   55.6/39.7
+    //   fp32, 48    34.0/79.1   53.5/81.8   99.3/85.3    188/151
+    //   bf16, 128   21.0/28.4   28.0/29.0   48.6/34.5   86.2/54.7
+    //   keys        48          96          128         192         256         384
+    //   bf16, 64    17.0/27.4   17.4/30.9   17.6/36.2   25.7/22.2   29.3/23.6   41.1/29.5
+    //   fp32, 48    31.8/52.5   58.1/56.3               86.9/79.8                169/153
+    //   bf16, 128   23.8/43.3   41.7/45.9   42.6/51.8   61.3/32.7   79.4/35.3    118/59.5
+    // (between 64 and 256 workgroups of keys the other form is up to a fifth
+    // faster than the one taken.)
     const bool can = row <= 256;
     a.alone_q = can && (int64_t)d.batch * d.heads * cdiv(d.n, kAttnRows) < kCus;
     a.alone_k = can && (int64_t)d.batch * d.kv_heads * cdiv(d.m, kAttnRows) <

@@ -239,10 +239,10 @@ struct KvPass {
     // before it).
     __device__ __forceinline__ void fetch(const AttnArgs& a, Place x, uint64_t seen, uint32_t lds,
                                           uint32_t terms) const {
-        // Measured on forward and backward together, wide places kept / formed anew:
-        // 2048 x 4096, 32 heads of 128 over 8, batch 2, 1243 / 1262 us; with a bias,
-        // whose sums leave no registers, 2048 x 2048, 16 heads of 64, batch 4, 502 /
-        // 490 us.
+        // Measured on forward and backward together, all places kept / those of the
+        // wide path / none: 2048 x 4096, 32 heads of 128 over 8, batch 2, 1267 / 1251
+        // / 1265 us; with a bias, whose sums take more registers, 2048 x 2048, 16
+        // heads of 64, batch 4, 508 / 504 / 494 us.
         using Load = Loader<OP, DP, QT, S::kNt, BIAS ? PLACES_ANEW : PLACES_KEPT_WIDE>;
         const int i0 = first + x.u * QT, head = kvh * a.G + x.g;
         const int part = ALONE ? 0 : wid;  // 32 rows a wave
@@ -392,9 +392,12 @@ struct KvPass {
 // no registers for both, and they are formed by two launches.  Rows of 256
 // bytes have the registers (dK, dV, and the keys and values themselves: 256
 // numbers a lane) for one wave a SIMD, which bounds them: the products wait for
-// the exponentials (636 us for 2048 x 4096, 32 heads of 128 over 8, batch 2,
-// 864 TFLOP/s; held to two waves, 186 registers go to memory and it takes 1150
-// and more).
+// the exponentials (597 us for 2048 x 4096, 32 heads of 128 over 8, batch 2, 920
+// TFLOP/s, the matrix pipes busy 40% of the cycles; held to two waves, 186
+// registers go to memory and it takes 1150 and more).
+// fp16 at 512 bytes keeps 76 registers in memory in the launch for dK (146 with
+// a bias): 196 to 209 us against 133 in bf16 for 1024 x 2048, 16 heads of 256,
+// batch 2.
 enum KvPart : int { PART_BOTH = 0, PART_DV = 1, PART_DK = 2 };
 template <int OP, int DP, bool BIAS, bool ALONE, int PART>
 __global__ __launch_bounds__(256, (Tile<OP, DP>::kRow <= 128 && !(BIAS && ALONE) ? 2 : 1))
@@ -586,8 +589,9 @@ __global__ __launch_bounds__(256) void attn_kv_merge_kernel(const AttnArgs a) {
 // result.
 //
 // Bound by the matrix unit and the exponentials between its products: two
-// waves a SIMD, 380 us for 2048 x 4096, 32 heads of 128 over 8, batch 2 (1085
-// TFLOP/s; 580 with one wave).
+// waves a SIMD, 379 to 395 us for 2048 x 4096, 32 heads of 128 over 8, batch 2
+// (1040 to 1090 TFLOP/s, the matrix pipes busy 56% of the cycles; 580 with one
+// wave).
 template <int OP, int DP, bool BIAS, bool ALONE>
 struct QPass {
     using S = BwdShape<OP, DP, ALONE, 128>;

@@ -361,8 +361,12 @@ __global__ __launch_bounds__(256) void norm_weight_kernel(const NormArgs a, int 
     if (y == 0 && x < a.d) R.gw[x] = (float)red[0][e];
 }
 
-// Rows a lane group: four where that still leaves every SIMD several waves,
-// else one (the latency of a single token's rows is then one load's).
+// Rows a lane group: four (backward: two) where that still leaves every SIMD
+// several waves, else one (the latency of a single token's rows is then one
+// load's).  Several / one, us, 40 heads of 128 in bf16: 40960 rows, forward 9.8 /
+// 9.2, backward 15.0 / 14.9; 81920, 11.9 / 13.4, 19.5 / 20.5; 131072, 17.0 / 18.5,
+// 25.1 / 26.5; 327680, 33.7 / 40.3, 48.6 / 51.0.  Few heads leave lanes of a wave
+// of several rows without any (2 heads, 131072 rows, 43.9 / 31.4, 49.2 / 38.0).
 constexpr int64_t kManyRows = 131072;
 int64_t items(const NormArgs& a, int lpr, int u) {
     const int per = 64 / lpr * u;
