@@ -304,7 +304,10 @@ __global__ __launch_bounds__(256) void norm_rotate_bwd_kernel(const NormArgs a) 
                 }
                 q = row_sum<LPR>(q);
                 m = row_sum<LPR>(m);
-                const float inv = 1.f / sqrtf(fmaf(q, dinv, a.eps));
+                // (lanes without a head hold zeros: with eps = 0 their 1 / 0 would
+                // reach the weights' sums)
+                const int head = it.h0 + k * Item::kGroups;
+                const float inv = head < R.heads ? 1.f / sqrtf(fmaf(q, dinv, a.eps)) : 0.f;
                 const float k2 = inv * inv * m * dinv;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -313,7 +316,6 @@ __global__ __launch_bounds__(256) void norm_rotate_bwd_kernel(const NormArgs a) 
                     u[k][e] = inv * fmaf(wu[e], gu[k][e], -u[k][e] * k2);
                     v[k][e] = inv * fmaf(wv[e], gv[k][e], -v[k][e] * k2);
                 }
-                const int head = it.h0 + k * Item::kGroups;
                 if (in && head < R.heads) store_pairs(a, y + head * R.y.sh, p0, WIDE, u[k], v[k]);
             }
         }

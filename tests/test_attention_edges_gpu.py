@@ -7,7 +7,7 @@ import math
 import pytest
 import torch
 
-from attention_reference import check, reference
+from attention_reference import check, norm_reference, reference
 from test_attention_gpu import BF, F4, HF, gpu, randn
 
 pytestmark = pytest.mark.gpu
@@ -158,3 +158,20 @@ def test_numbers_beyond_32_bits_are_refused(fs):
         fs.fs_qk_norm_rotate(q, None, None, None, o, None, offset=1 << 32)
     with pytest.raises(ValueError, match="32 bits"):
         fs.fs_qk_norm_rotate(many, None, None, None, many, None)
+
+
+@pytest.mark.parametrize("dtype,B,n,H,d", [(F4, 2, 5, 3, 64), (BF, 1, 40, 5, 128), (HF, 2, 9, 1, 256),
+                                           (BF, 1, 12000, 11, 96), (F4, 1, 7, 3, 34)])
+def test_norm_without_eps(fs, dtype, B, n, H, d):
+    """eps = 0 is allowed; heads that do not fill the lanes of a wave leave no trace in
+    the weights' gradients."""
+    g = torch.Generator().manual_seed(d)
+    x, dy = randn(g, B, n, H, d, dtype=dtype, std=2.0), randn(g, B, n, H, d, dtype=dtype)
+    w = 1 + randn(g, d, std=0.3)
+    y, dx = (torch.full_like(x, NAN, device="cuda") for _ in range(2))
+    dw = torch.full((d,), NAN, device="cuda")
+    fs.fs_qk_norm_rotate(x.cuda(), None, w.cuda(), None, y, None, eps=0.0)
+    fs.fs_qk_norm_rotate_backward(x.cuda(), None, w.cuda(), None, dy.cuda(), None, dx, None, dw, None,
+                                  eps=0.0)
+    torch.cuda.synchronize()
+    compare({"y": y, "dx": dx, "dw": dw}, norm_reference(x, w, None, None, None, 0.0, False, dy))
