@@ -82,8 +82,9 @@ typedef struct {
      * (n_edges + 1 buckets: keys after the query count as distance 0), or
      * two-sided u(|r|) for r <= 0 and n_edges + 1 + u(r) for r > 0
      * (2 (n_edges + 1) buckets).  bias: device fp32 [buckets][heads], or NULL
-     * for none.  An entry of -1e30 or less gives its pairs no weight; others are
-     * finite and at most 2e38.  The bias speaks of positions: it is for rows and
+     * for none.  An entry of -1e6 or less gives its pairs no weight, as a mask (a
+     * row that has no other pairs is empty); the others are at most 1e6 (fp32 holds
+     * few of a score's digits beside it).  The bias speaks of positions: it is for rows and
      * keys that have an order, such as points along a curve or a scan. */
     const float* bias;
     const int32_t* edges;

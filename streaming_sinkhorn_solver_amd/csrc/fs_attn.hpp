@@ -482,10 +482,13 @@ __device__ __forceinline__ int bucket_of(const AttnArgs& a, int r) {
     for (int e = 0; e < a.n_edges; ++e) c += dist >= (int)a.edges[e];
     return c + (a.two_sided && r > 0 ? a.n_edges + 1 : 0);
 }
-// A value of -1e30 or less (the type's lowest among them) is taken as -inf, no
-// weight: in base 2 the lowest would leave the range, and next to it scores
-// would be lost in rounding anyway.
-__device__ __forceinline__ float bias2(float x) { return x <= -1e30f ? -INFINITY : x * kLog2e; }
+// A value of -1e6 or less stands for a mask and is taken as -inf, no weight.  Next
+// to any other key it has none in fp32 either; in a row that has no other the
+// scores would be lost beside it, and with them L's last digits: exp(s - L) of the
+// backward pass would be off by 2^(half a step of L in base 2), 4% at -1e6 but 2^64
+// at -1e9 (gradients of 1e37).  The lowest values would leave the range in base 2.
+constexpr float kNoWeight = -1e6f;
+__device__ __forceinline__ float bias2(float x) { return x <= kNoWeight ? -INFINITY : x * kLog2e; }
 __device__ __forceinline__ void load_line(const AttnArgs& a, int head, LdsFloats line, int t, int nt) {
     for (int i = t; i < a.r0 + a.rp + 1; i += nt)
         line.set(i, bias2(a.bias[(int64_t)bucket_of(a, i - a.r0) * a.H + head]));

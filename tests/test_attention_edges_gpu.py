@@ -175,3 +175,21 @@ def test_norm_without_eps(fs, dtype, B, n, H, d):
                                   eps=0.0)
     torch.cuda.synchronize()
     compare({"y": y, "dx": dx, "dw": dw}, norm_reference(x, w, None, None, None, 0.0, False, dy))
+
+
+@pytest.mark.parametrize("low", [-1e9, -3e12, -1e25])
+@pytest.mark.parametrize("dtype,n,d,copies", EMPTY)
+def test_bias_far_below_every_score(fs, dtype, n, d, copies, low):
+    """Buckets with an entry that stands for a mask: no weight next to other keys, and
+    none in rows that have no others, whose scores fp32 would have lost beside it."""
+    g = torch.Generator().manual_seed(n + d)
+    m, H = max(2, n // 2), 2
+    q, k, v, d_o = (randn(g, 2, r, H, d, dtype=dtype) for r in (n, m, m, n))
+    d_lse = randn(g, 2, H, n)
+    bias = randn(g, 8, H)
+    bias[:4, 1] = low  # the second head sees later keys only
+    kw = {"edges": [1, 3, 8], "two_sided": True, "scale": 1.5}
+    out = run(fs, q, k, v, d_o, d_lse, copies, bias=bias, **kw)
+    bias[:4, 1] = -INF
+    compare(out, reference(q, k, v, d_o=d_o, d_lse=d_lse, bias=bias, **kw))
+    assert torch.all(out["lse"][:, 1, m - 1:] == -INF) and torch.all(out["o"][:, m - 1:, 1] == 0)
