@@ -20,7 +20,8 @@
  *    of a fused projection, and inputs broadcast by stride 0 are fine.  Views
  *    whose rows are 16-byte aligned with a width of whole 16-byte chunks are
  *    read with wide loads, others element by element.  Outputs may not overlap
- *    themselves, an input or the workspace.
+ *    themselves, one another, an input or the workspace (slices of one buffer
+ *    side by side do not overlap; against an input whole extents count).
  *  - Work is enqueued on `stream` and is asynchronous; nothing synchronises,
  *    nothing is allocated, and every call may be captured into a graph (a
  *    replay uses the same buffers: two captured calls that may overlap need a

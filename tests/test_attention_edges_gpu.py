@@ -193,3 +193,50 @@ def test_bias_far_below_every_score(fs, dtype, n, d, copies, low):
     bias[:4, 1] = -INF
     compare(out, reference(q, k, v, d_o=d_o, d_lse=d_lse, bias=bias, **kw))
     assert torch.all(out["lse"][:, 1, m - 1:] == -INF) and torch.all(out["o"][:, m - 1:, 1] == 0)
+
+
+@pytest.mark.parametrize("dtype,n", [(BF, 5), (HF, 140), (F4, 33)])
+def test_one_buffer_for_queries_keys_and_values(fs, dtype, n):
+    """q, k, v as slices of a fused projection, their gradients as slices of its
+    gradient; the columns between them keep their contents."""
+    g = torch.Generator().manual_seed(n)
+    B, H, K, d = 2, 4, 2, 64
+    qkv = randn(g, B, n, H + 2 * K + 1, d, dtype=dtype)
+    d_o = randn(g, B, n, H, d, dtype=dtype, std=0.1)
+    part = lambda t: (t[:, :, :H], t[:, :, H:H + K], t[:, :, H + K:H + 2 * K])
+    dev = qkv.cuda()
+    grad = torch.full_like(dev, 7.0)
+    o, lse = torch.empty(B, n, H, d, dtype=dtype, device="cuda"), torch.empty(B, H, n, device="cuda")
+    fs.fs_attention_forward(*part(dev), o, lse, causal=True)
+    fs.fs_attention_backward(*part(dev), o, lse, d_o.cuda(), *part(grad), causal=True)
+    # the same through the norm, in place of the projection's columns for q and k
+    y = torch.full_like(dev, 7.0)
+    fs.fs_qk_norm_rotate(*part(dev)[:2], None, None, *part(y)[:2])
+    torch.cuda.synchronize()
+    ref = reference(*part(qkv), d_o=d_o, causal=True)
+    compare(dict(zip(("d_q", "d_k", "d_v"), part(grad)), o=o, lse=lse), ref)
+    assert torch.all(grad[:, :, H + 2 * K:] == 7) and torch.all(y[:, :, H + K:] == 7)
+    for got, x in zip(part(y), part(qkv)[:2]):
+        check("y", got, norm_reference(x, None, None, None, None, 1e-6, False)["y"])
+
+
+def test_calls_on_two_streams_at_once(fs):
+    """Two training steps in flight together, each with its own buffers."""
+    g = torch.Generator().manual_seed(3)
+    sets, refs = [], []
+    for n, m in ((300, 700), (130, 2100)):
+        q, k, v, d_o = (randn(g, 2, r, 4, 64, dtype=BF) for r in (n, m, m, n))
+        refs.append(reference(q, k, v, d_o=d_o))
+        sets.append([t.cuda() for t in (q, k, v, d_o)])
+    outs = [[torch.full_like(t, NAN) for t in (s[0], s[0], s[1], s[2])] +
+            [torch.full((2, 4, s[0].shape[1]), NAN, device="cuda")] for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        for (q, k, v, d_o), (o, dq, dk, dv, lse), s in zip(sets, outs, streams):
+            fs.fs_attention_forward(q, k, v, o, lse, stream=s)
+            fs.fs_attention_backward(q, k, v, o, lse, d_o, dq, dk, dv, stream=s)
+    torch.cuda.synchronize()
+    for (o, dq, dk, dv, lse), ref in zip(outs, refs):
+        compare({"o": o, "lse": lse, "d_q": dq, "d_k": dk, "d_v": dv}, ref)
