@@ -1,5 +1,5 @@
 """Thin ctypes binding of ``libfs_sinkhorn.so`` (the C ABI in include/fs_sinkhorn.h,
-include/fs_attention.h and include/fs_probe.h).
+include/fs_attention.h, include/fs_layers.h and include/fs_probe.h).
 
 Argument marshalling only: torch tensors provide device memory and the current
 HIP stream; every step of the solver runs in the library's kernels.  If the
@@ -33,6 +33,10 @@ __all__ = [
     "fs_bucket_edges", "fs_attention_workspace_bytes", "fs_attention_forward",
     "fs_attention_backward", "fs_qk_norm_workspace_bytes", "fs_qk_norm_rotate",
     "fs_qk_norm_rotate_backward",
+    "fs_layer_norm_workspace_bytes", "fs_layer_norm", "fs_layer_norm_backward",
+    "fs_quantize_rows", "fs_quantized_product_workspace_bytes", "fs_quantized_product",
+    "fs_distill_workspace_bytes", "fs_distill_loss", "fs_distill_loss_backward",
+    "fs_balance_workspace_bytes", "fs_balance_loss", "fs_balance_loss_backward",
 ]
 
 FS_OK, FS_ERR_INVALID_ARG, FS_ERR_WORKSPACE, FS_ERR_DEVICE, FS_ERR_NONFINITE, \
@@ -102,6 +106,32 @@ class QkNormDesc(ctypes.Structure):
                 ("sin_table", ctypes.c_void_p), ("n_pos", ctypes.c_int32),
                 ("positions", ctypes.c_void_p), ("positions_stride", ctypes.c_int64),
                 ("offset", ctypes.c_int32)]
+
+
+class LayerNormDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("width", ctypes.c_int32), ("eps", ctypes.c_float), ("lengths", ctypes.c_void_p)]
+
+
+class QuantizedProductDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("m", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("q_x", ctypes.c_void_p), ("q_x_stride", ctypes.c_int64),
+                ("scale_x", ctypes.c_void_p), ("q_w", ctypes.c_void_p),
+                ("q_w_stride", ctypes.c_int64), ("scale_w", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("y", ctypes.c_void_p), ("y_stride", ctypes.c_int64)]
+
+
+class DistillDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("rows", ctypes.c_int32), ("classes", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("temperature", ctypes.c_float), ("ids", ctypes.c_void_p),
+                ("teacher", ctypes.c_void_p), ("teacher_lse", ctypes.c_void_p),
+                ("active", ctypes.c_void_p)]
+
+
+class BalanceDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("experts", ctypes.c_int32), ("k", ctypes.c_int32), ("normalize", ctypes.c_int32),
+                ("lengths", ctypes.c_void_p)]
 
 
 class FsError(RuntimeError):
@@ -237,6 +267,25 @@ def load():
     lib.fs_qk_norm_rotate_backward.restype = ctypes.c_int
     lib.fs_qk_norm_rotate_backward.argtypes = [norm, Rows, Rows, _fp, _fp] + [Rows] * 4 + \
         [_fp, _fp, _vp, sz, _vp]
+    layer, product = ctypes.POINTER(LayerNormDesc), ctypes.POINTER(QuantizedProductDesc)
+    distill, balance = ctypes.POINTER(DistillDesc), ctypes.POINTER(BalanceDesc)
+    for name, result, args in (
+            ("fs_layer_norm_workspace_bytes", sz, [layer]),
+            ("fs_layer_norm", i32, [layer, Rows, Rows, _fp, _fp, Rows, Rows, _fp, _fp, _vp]),
+            ("fs_layer_norm_backward", i32, [layer, Rows, _fp, _fp, _fp, Rows, Rows, Rows, _fp, _fp,
+                                             _vp, sz, _vp]),
+            ("fs_quantize_rows", i32, [i32, i32, i32, _vp, i64, _vp, i64, _fp, _vp]),
+            ("fs_quantized_product_workspace_bytes", sz, [i32, i32, i32]),
+            ("fs_quantized_product", i32, [product, _vp, sz, _vp]),
+            ("fs_distill_workspace_bytes", sz, [distill]),
+            ("fs_distill_loss", i32, [distill, Rows, _fp, _fp, _fp, Rows, _vp, sz, _vp]),
+            ("fs_distill_loss_backward", i32, [distill, Rows, _fp, _fp, Rows, _vp]),
+            ("fs_balance_workspace_bytes", sz, [balance]),
+            ("fs_balance_loss", i32, [balance, Rows, _vp, _fp, _vp, _fp, _fp, _vp, sz, _vp]),
+            ("fs_balance_loss_backward", i32, [balance, Rows, _vp, _vp, _fp, _fp, _fp, Rows,
+                                               _vp])):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = result, args
     _LIB = lib
     return lib
 
@@ -1034,3 +1083,302 @@ def fs_qk_norm_rotate_backward(q, k, q_weight, k_weight, d_q_out, d_k_out, d_q, 
                  _rows(d_q, "d_q", like, dev, qs), _rows(d_k, "d_k", like, dev, ks),
                  _flat(d_q_weight, "d_q_weight", dev, f32, w),
                  _flat(d_k_weight, "d_k_weight", dev, f32, w), ws, size)
+
+
+# ---- layers and losses (include/fs_layers.h) --------------------------------
+
+def _dtype_of(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a device tensor")
+    dtype = _DTYPES.get(t.dtype)
+    if dtype is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16 (is {t.dtype})")
+    return dtype
+
+
+def _states(t: Optional[torch.Tensor], name: str, like: torch.Tensor, dev: int, shape) -> Rows:
+    """A [batch, rows, width] or [rows, width] tensor of like's type as fs_rows."""
+    if t is None:
+        return _NO_ROWS
+    _on(t, name, dev)
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} is {t.dtype}, not {like.dtype} as the others")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)} (is {tuple(t.shape)})")
+    s = t.stride()
+    if s[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"{name}'s last axis must be contiguous")
+    return Rows(t.data_ptr(), s[0] if len(s) == 3 else 0, s[-2], 0)
+
+
+def _matrix8(t: torch.Tensor, name: str, dev: int, shape):
+    """Address and row stride of an int8 matrix."""
+    _on(t, name, dev)
+    if t.dtype != torch.int8:
+        raise TypeError(f"{name} must be int8 (is {t.dtype})")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)} (is {tuple(t.shape)})")
+    if t.stride(1) != 1 and shape[1] > 1:
+        raise ValueError(f"{name}'s last axis must be contiguous")
+    return t.data_ptr(), t.stride(0)
+
+
+def _need(t, name: str):
+    if t is None:
+        raise TypeError(f"{name} must be given")
+    return t
+
+
+def _layer_norm_desc(x, name, eps, lengths):
+    """The description and the device's number."""
+    dtype = _dtype_of(x, name)
+    if x.dim() != 3:
+        raise ValueError(f"{name} must be [batch, rows, width]")
+    batch, n, width = x.shape
+    if batch > _MAX or n > _MAX or width > _MAX:
+        _i32("a size", batch, n, width)
+    dev = x.get_device()
+    a = LayerNormDesc(dtype, batch, n, width, eps)
+    if lengths is not None:
+        a.lengths = _flat(lengths, "lengths", dev, torch.int32, (batch,))
+    return a, dev
+
+
+def fs_layer_norm_workspace_bytes(x: torch.Tensor) -> int:
+    """Bytes of workspace of fs_layer_norm_backward on rows of this shape."""
+    a, _ = _layer_norm_desc(x, "x", 0.0, None)
+    return _needed(load().fs_layer_norm_workspace_bytes, "fs_layer_norm_workspace_bytes",
+                   ctypes.byref(a))
+
+
+def fs_layer_norm(x: torch.Tensor, weight, bias, y: torch.Tensor, *, residual=None, total=None,
+                  mean=None, rstd=None, eps: float = 1e-5, lengths=None, stream=None):
+    """y <- weight (z - mean z) / sqrt(var z + eps) + bias of the rows of z = x, or
+    of z = total <- x + residual.  x, y, residual, total: [batch, rows, width];
+    weight, bias: [width] float32 (None: ones, zeros); mean, rstd: [batch, rows]
+    float32, written if given; rows from lengths[b] on are padding."""
+    lib = load()
+    a, dev = _layer_norm_desc(x, "x", eps, lengths)
+    xs, f32 = x.shape, torch.float32
+    w, rows = xs[2:], xs[:2]
+    return _call(lib.fs_layer_norm, "fs_layer_norm", dev, stream, ctypes.byref(a),
+                 _states(x, "x", x, dev, xs), _states(residual, "residual", x, dev, xs),
+                 _flat(weight, "weight", dev, f32, w), _flat(bias, "bias", dev, f32, w),
+                 _states(total, "total", x, dev, xs), _states(_need(y, "y"), "y", x, dev, xs),
+                 _flat(mean, "mean", dev, f32, rows), _flat(rstd, "rstd", dev, f32, rows))
+
+
+def fs_layer_norm_backward(z: torch.Tensor, weight, mean, rstd, d_y, d_x, d_weight=None, d_bias=None,
+                           *, d_total=None, lengths=None,
+                           workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of fs_layer_norm from those of y (d_y) and of total (d_total,
+    optional): writes d_x (the residual's too) and, where given, the weight's and
+    the bias's.  z: the forward call's total, or its x."""
+    lib = load()
+    a, dev = _layer_norm_desc(z, "z", 0.0, lengths)
+    pa = ctypes.byref(a)
+    ws, size, _keep = _work(workspace, lambda: _needed(lib.fs_layer_norm_workspace_bytes,
+                                                       "fs_layer_norm_backward", pa), z, dev, stream)
+    zs, f32 = z.shape, torch.float32
+    w, rows = zs[2:], zs[:2]
+    return _call(lib.fs_layer_norm_backward, "fs_layer_norm_backward", dev, stream, pa,
+                 _states(z, "z", z, dev, zs), _flat(weight, "weight", dev, f32, w),
+                 _flat(_need(mean, "mean"), "mean", dev, f32, rows),
+                 _flat(_need(rstd, "rstd"), "rstd", dev, f32, rows),
+                 _states(_need(d_y, "d_y"), "d_y", z, dev, zs),
+                 _states(d_total, "d_total", z, dev, zs),
+                 _states(_need(d_x, "d_x"), "d_x", z, dev, zs),
+                 _flat(d_weight, "d_weight", dev, f32, w), _flat(d_bias, "d_bias", dev, f32, w), ws,
+                 size)
+
+
+def fs_quantize_rows(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, *, stream=None):
+    """q <- the whole numbers nearest to 127 x / max |row|, scale <- max |row| / 127.
+    x: [rows, width], q: the same int8, scale: [rows] float32."""
+    dtype = _dtype_of(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, width]")
+    rows, width = x.shape
+    if rows > _MAX or width > _MAX:
+        _i32("a size", rows, width)
+    dev = x.get_device()
+    X = _states(x, "x", x, dev, x.shape)
+    qp, qs = _matrix8(q, "q", dev, x.shape)
+    return _call(load().fs_quantize_rows, "fs_quantize_rows", dev, stream, dtype, rows, width, X.data,
+                 X.stride_row, qp, qs, _flat(_need(scale, "scale"), "scale", dev, torch.float32,
+                                             (rows,)))
+
+
+def fs_quantized_product_workspace_bytes(m: int, n: int, k: int) -> int:
+    """Bytes of workspace of fs_quantized_product of [m, k] by [n, k]."""
+    _i32("a size", m, n, k)
+    return _needed(load().fs_quantized_product_workspace_bytes,
+                   "fs_quantized_product_workspace_bytes", m, n, k)
+
+
+def fs_quantized_product(q_x: torch.Tensor, scale_x: torch.Tensor, q_w: torch.Tensor,
+                         scale_w: torch.Tensor, y: torch.Tensor, *, bias=None,
+                         workspace: Optional[torch.Tensor] = None, stream=None):
+    """y <- scale_x scale_w (q_x . q_w) + bias of rows held in 8-bit integers.  q_x:
+    [m, k], q_w: [n, k] int8; scale_x: [m], scale_w, bias: [n] float32; y: [m, n]."""
+    lib = load()
+    dtype = _dtype_of(y, "y")
+    dev = y.get_device()
+    if y.dim() != 2 or q_x.dim() != 2 or q_w.dim() != 2:
+        raise ValueError("q_x, q_w and y must be matrices")
+    (m, k), n = q_x.shape, q_w.shape[0]
+    if m > _MAX or n > _MAX or k > _MAX:
+        _i32("a size", m, n, k)
+    f32 = torch.float32
+    Y = _states(y, "y", y, dev, (m, n))
+    xp, xs = _matrix8(q_x, "q_x", dev, (m, k))
+    wp, ws_ = _matrix8(q_w, "q_w", dev, (n, k))
+    a = QuantizedProductDesc(dtype, m, n, k, xp, xs,
+                             _flat(_need(scale_x, "scale_x"), "scale_x", dev, f32, (m,)), wp, ws_,
+                             _flat(_need(scale_w, "scale_w"), "scale_w", dev, f32, (n,)),
+                             _flat(bias, "bias", dev, f32, (n,)), Y.data, Y.stride_row)
+    ws, size, _keep = _work(workspace, lambda: _needed(lib.fs_quantized_product_workspace_bytes,
+                                                       "fs_quantized_product", m, n, k), y, dev,
+                            stream)
+    return _call(lib.fs_quantized_product, "fs_quantized_product", dev, stream, ctypes.byref(a), ws,
+                 size)
+
+
+def _distill_desc(logits, ids, teacher, temperature, teacher_lse, active):
+    """The description and the device's number."""
+    dtype = _dtype_of(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, classes]")
+    rows, classes = logits.shape
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be [rows, k]")
+    k = ids.shape[1]
+    if rows > _MAX or classes > _MAX or k > _MAX:
+        _i32("a size", rows, classes, k)
+    dev = logits.get_device()
+    a = DistillDesc(dtype, rows, classes, k, temperature,
+                    _flat(ids, "ids", dev, torch.int32, (rows, k)),
+                    _flat(_need(teacher, "teacher"), "teacher", dev, torch.float32, (rows, k)),
+                    _flat(teacher_lse, "teacher_lse", dev, torch.float32, (rows,)))
+    if active is not None:
+        _on(active, "active", dev)
+        if active.dtype not in (torch.uint8, torch.bool) or active.shape != (rows,) or \
+                not active.is_contiguous():
+            raise TypeError(f"active must be a contiguous uint8 or bool tensor of ({rows},)")
+        a.active = active.data_ptr()
+    return a, dev
+
+
+def fs_distill_workspace_bytes(logits: torch.Tensor, k: int) -> int:
+    """Bytes of workspace of fs_distill_loss on logits of this shape, k entries a row."""
+    dtype = _dtype_of(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, classes]")
+    _i32("a size", *logits.shape, k)
+    a = DistillDesc(dtype, *logits.shape, k, 1.0)
+    return _needed(load().fs_distill_workspace_bytes, "fs_distill_workspace_bytes", ctypes.byref(a))
+
+
+def fs_distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
+                    loss: torch.Tensor, lse: torch.Tensor, *, temperature: float = 1.0,
+                    teacher_lse=None, active=None, d_loss=None, d_logits=None,
+                    workspace: Optional[torch.Tensor] = None, stream=None):
+    """loss <- T^2 KL(teacher's top entries || softmax(logits / T)) of each row, lse
+    <- the rows' log-sum-exps.  logits: [rows, classes]; ids (int32), teacher
+    (float32): [rows, k]; loss, lse: [rows] float32.  With d_loss ([rows] float32)
+    and d_logits the gradient is written in the same pass."""
+    lib = load()
+    a, dev = _distill_desc(logits, ids, teacher, temperature, teacher_lse, active)
+    pa = ctypes.byref(a)
+    ws, size, _keep = _work(workspace, lambda: _needed(lib.fs_distill_workspace_bytes,
+                                                       "fs_distill_loss", pa), logits, dev, stream)
+    f32, xs = torch.float32, logits.shape
+    rows = xs[:1]
+    return _call(lib.fs_distill_loss, "fs_distill_loss", dev, stream, pa,
+                 _states(logits, "logits", logits, dev, xs),
+                 _flat(_need(loss, "loss"), "loss", dev, f32, rows),
+                 _flat(_need(lse, "lse"), "lse", dev, f32, rows),
+                 _flat(d_loss, "d_loss", dev, f32, rows),
+                 _states(d_logits, "d_logits", logits, dev, xs), ws, size)
+
+
+def fs_distill_loss_backward(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
+                             lse: torch.Tensor, d_loss: torch.Tensor, d_logits: torch.Tensor, *,
+                             temperature: float = 1.0, teacher_lse=None, active=None, stream=None):
+    """Gradient of fs_distill_loss: writes d_logits from d_loss and the rows' lse."""
+    a, dev = _distill_desc(logits, ids, teacher, temperature, teacher_lse, active)
+    f32, xs = torch.float32, logits.shape
+    rows = xs[:1]
+    return _call(load().fs_distill_loss_backward, "fs_distill_loss_backward", dev, stream,
+                 ctypes.byref(a), _states(logits, "logits", logits, dev, xs),
+                 _flat(_need(lse, "lse"), "lse", dev, f32, rows),
+                 _flat(_need(d_loss, "d_loss"), "d_loss", dev, f32, rows),
+                 _states(_need(d_logits, "d_logits"), "d_logits", logits, dev, xs))
+
+
+def _balance_desc(logits, k, normalize, lengths):
+    """The description and the device's number."""
+    dtype = _dtype_of(logits, "logits")
+    if logits.dim() != 3:
+        raise ValueError("logits must be [batch, rows, experts]")
+    batch, n, experts = logits.shape
+    if batch > _MAX or n > _MAX or experts > _MAX or k > _MAX:
+        _i32("a size", batch, n, experts, k)
+    dev = logits.get_device()
+    a = BalanceDesc(dtype, batch, n, experts, k, 1 if normalize else 0)
+    if lengths is not None:
+        a.lengths = _flat(lengths, "lengths", dev, torch.int32, (batch,))
+    return a, dev
+
+
+def fs_balance_workspace_bytes(logits: torch.Tensor, k: int) -> int:
+    """Bytes of workspace of fs_balance_loss on logits of this shape, k chosen a row."""
+    a, _ = _balance_desc(logits, k, False, None)
+    return _needed(load().fs_balance_workspace_bytes, "fs_balance_workspace_bytes", ctypes.byref(a))
+
+
+def fs_balance_loss(logits: torch.Tensor, ids: torch.Tensor, gates: torch.Tensor,
+                    counts: torch.Tensor, loss: torch.Tensor, lse: torch.Tensor, *,
+                    normalize: bool = False, lengths=None,
+                    workspace: Optional[torch.Tensor] = None, stream=None):
+    """Each row's k largest columns (ids, [batch, rows, k] int32) with their
+    probabilities (gates, float32), how often each column is chosen (counts,
+    [batch, experts] int32), the balance loss and the mean square of the rows' lse
+    (loss, [batch, 2] float32; lse: [batch, rows]).  logits: [batch, rows, experts]."""
+    lib = load()
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 3:
+        raise ValueError("ids must be [batch, rows, k]")
+    a, dev = _balance_desc(logits, ids.shape[2], normalize, lengths)
+    pa = ctypes.byref(a)
+    ws, size, _keep = _work(workspace, lambda: _needed(lib.fs_balance_workspace_bytes,
+                                                       "fs_balance_loss", pa), logits, dev, stream)
+    f32, i32 = torch.float32, torch.int32
+    batch, n, experts = xs = logits.shape
+    each = (batch, n, a.k)
+    return _call(lib.fs_balance_loss, "fs_balance_loss", dev, stream, pa,
+                 _states(logits, "logits", logits, dev, xs), _flat(ids, "ids", dev, i32, each),
+                 _flat(_need(gates, "gates"), "gates", dev, f32, each),
+                 _flat(_need(counts, "counts"), "counts", dev, i32, (batch, experts)),
+                 _flat(_need(loss, "loss"), "loss", dev, f32, (batch, 2)),
+                 _flat(_need(lse, "lse"), "lse", dev, f32, (batch, n)), ws, size)
+
+
+def fs_balance_loss_backward(logits: torch.Tensor, ids: torch.Tensor, counts: torch.Tensor,
+                             lse: torch.Tensor, d_logits: torch.Tensor, *, d_loss: torch.Tensor,
+                             d_gates=None, normalize: bool = False, lengths=None, stream=None):
+    """Gradient of fs_balance_loss: writes d_logits from the gradients of loss
+    ([batch, 2]) and of gates ([batch, rows, k], optional)."""
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 3:
+        raise ValueError("ids must be [batch, rows, k]")
+    a, dev = _balance_desc(logits, ids.shape[2], normalize, lengths)
+    f32, i32 = torch.float32, torch.int32
+    batch, n, experts = xs = logits.shape
+    each = (batch, n, a.k)
+    return _call(load().fs_balance_loss_backward, "fs_balance_loss_backward", dev, stream,
+                 ctypes.byref(a), _states(logits, "logits", logits, dev, xs),
+                 _flat(ids, "ids", dev, i32, each),
+                 _flat(_need(counts, "counts"), "counts", dev, i32, (batch, experts)),
+                 _flat(_need(lse, "lse"), "lse", dev, f32, (batch, n)),
+                 _flat(_need(d_loss, "d_loss"), "d_loss", dev, f32, (batch, 2)),
+                 _flat(d_gates, "d_gates", dev, f32, each),
+                 _states(_need(d_logits, "d_logits"), "d_logits", logits, dev, xs))

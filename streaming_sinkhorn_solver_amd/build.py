@@ -21,7 +21,8 @@ LIB = os.path.join(HERE, "libfs_sinkhorn.so")
 SOURCES = ["fs_api.cpp", "fs_prep.hip", "fs_lse.hip", "fs_lse_small.hip", "fs_transport.hip",
            "fs_grad.hip", "fs_probe.hip", "fs_hvp.hip", "fs_bsparse.hip", "fs_static.hip",
            "fs_persistent.hip", "fs_attn_api.cpp", "fs_attn_fwd.hip", "fs_attn_bwd.hip",
-           "fs_qknorm.hip"]
+           "fs_qknorm.hip", "fs_layers_api.cpp", "fs_layernorm.hip", "fs_quant.hip",
+           "fs_distill.hip", "fs_balance.hip"]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,263 @@
+// fs_layernorm.hip -- the layer norm of rows with the residual sum in front of
+// it, and its gradients:
+//   z = x + r,  h = (z - mean z) rstd,  y = w h + b;
+//   u = w g,  dx = rstd (u - mean u - h mean(u h)) + dz,  dw = sum g h,  db = sum g.
+// Bound by memory: a row is read once and stays in registers over both sums of
+// its statistics (the second is of squared distances from the mean, so that a
+// large mean costs no digits).
+#include "fs_layers_args.h"
+#include "fs_rowops.hpp"
+
+#include <type_traits>
+
+namespace fs {
+
+namespace {
+
+// LPR threads a row, CH groups of 8 elements a thread.
+template <int LPR>
+constexpr int threads_of() {
+    return LPR > 256 ? LPR : 256;
+}
+
+__device__ __forceinline__ void place(const LayerNormArgs& a, int64_t row, int& b, int& i) {
+    b = a.B == 1 ? 0 : (int)((uint32_t)row / (uint32_t)a.n);
+    i = (int)(row - (int64_t)b * a.n);
+}
+__device__ __forceinline__ bool row_on(const LayerNormArgs& a, int b, int i) {
+    return !a.lengths || i < a.lengths[b];
+}
+
+template <int LPR, int CH, bool WIDE>
+__device__ __forceinline__ void load_weight(const float* w, int lane, int width, float fill,
+                                            float (&out)[CH][8]) {
+    if (w) {
+        Share<float, LPR, CH, WIDE> s;
+        s.load(w, lane, width, true);
+        __builtin_memcpy(out, s.v, sizeof(out));
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) out[j][e] = fill;
+}
+
+template <int OP, int LPR, int CH, bool WIDE>
+__global__ __launch_bounds__(threads_of<LPR>()) void layer_norm_kernel(const LayerNormArgs a) {
+    using T = typename El<OP>::T;
+    constexpr int GRP = threads_of<LPR>() / LPR;
+    __shared__ float2 buf[2 * RowFold<LPR>::kWaves];
+    RowFold<LPR> fold(buf);
+    const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR, W = a.width;
+    float w[CH][8], bias[CH][8];
+    load_weight<LPR, CH, WIDE>(a.w, lane, W, 1.f, w);
+    load_weight<LPR, CH, WIDE>(a.b, lane, W, 0.f, bias);
+    const float inv_w = 1.f / (float)W;
+    const int64_t rows = (int64_t)a.B * a.n;
+    // (the groups of a workgroup leave the loop together: its sums have barriers)
+    for (int64_t first = (int64_t)blockIdx.x * GRP; first < rows; first += (int64_t)gridDim.x * GRP) {
+        const int64_t row = first + grp;
+        if (LPR <= 64 && row >= rows) break;
+        int b, i;
+        place(a, row, b, i);
+        const bool on = row_on(a, b, i);
+        Share<T, LPR, CH, WIDE> x, r;
+        x.load((const T*)a.x.p + b * a.x.sb + i * a.x.sr, lane, W, on);
+        float z[CH][8];
+        if (a.r.p) {
+            r.load((const T*)a.r.p + b * a.r.sb + i * a.r.sr, lane, W, on);
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x.v[j][e] = (T)((float)x.v[j][e] + (float)r.v[j][e]);
+            x.store((T*)a.z.p + b * a.z.sb + i * a.z.sr, lane, W);
+        }
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += z[j][e] = (float)x.v[j][e];
+        const float mean = fold.sum(s) * inv_w;
+        float q = 0.f;
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                z[j][e] = share_at<LPR, WIDE>(lane, j, e) < W ? z[j][e] - mean : 0.f;
+                q = fmaf(z[j][e], z[j][e], q);
+            }
+        q = fold.sum(q);
+        const float rstd = 1.f / sqrtf(fmaf(q, inv_w, a.eps));
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                x.v[j][e] = (T)(on ? fmaf(z[j][e] * rstd, w[j][e], bias[j][e]) : 0.f);
+        x.store((T*)a.y.p + b * a.y.sb + i * a.y.sr, lane, W);
+        if (lane == 0 && a.mean) a.mean[row] = on ? mean : 0.f;
+        if (lane == 0 && a.rstd) a.rstd[row] = on ? rstd : 0.f;
+    }
+}
+
+// Backward: a workgroup takes rows in steps of the grid; a thread's columns are
+// the same in every row, so the weights' gradients are summed in its registers,
+// over the workgroup's rows in LDS, and over workgroups by layer_norm_sum_kernel.
+template <int OP, int LPR, int CH, bool WIDE>
+__global__ __launch_bounds__(threads_of<LPR>()) void layer_norm_bwd_kernel(const LayerNormArgs a) {
+    using T = typename El<OP>::T;
+    constexpr int GRP = threads_of<LPR>() / LPR;
+    __shared__ float2 buf[2 * RowFold<LPR>::kWaves];
+    __shared__ float red[GRP > 1 ? 2 * GRP * LPR * CH * 8 : 1];
+    RowFold<LPR> fold(buf);
+    const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR, W = a.width;
+    float w[CH][8], dw[CH][8], db[CH][8];
+    load_weight<LPR, CH, WIDE>(a.w, lane, W, 1.f, w);
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[j][e] = db[j][e] = 0.f;
+    const float inv_w = 1.f / (float)W;
+    const int64_t rows = (int64_t)a.B * a.n;
+    for (int64_t first = (int64_t)blockIdx.x * GRP; first < rows; first += (int64_t)gridDim.x * GRP) {
+        const int64_t row = first + grp;
+        if (LPR <= 64 && row >= rows) break;
+        int b, i;
+        place(a, row, b, i);
+        const bool on = row_on(a, b, i);
+        Share<T, LPR, CH, WIDE> z, g, t;
+        z.load((const T*)a.x.p + b * a.x.sb + i * a.x.sr, lane, W, on);
+        g.load((const T*)a.g.p + b * a.g.sb + i * a.g.sr, lane, W, on);
+        if (a.gz.p) t.load((const T*)a.gz.p + b * a.gz.sb + i * a.gz.sr, lane, W, on);
+        const float mean = on ? a.mean[row] : 0.f, rstd = on ? a.rstd[row] : 0.f;
+        float h[CH][8], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float ge = (float)g.v[j][e];  // 0 behind the row's end
+                h[j][e] = ((float)z.v[j][e] - mean) * rstd;
+                dw[j][e] = fmaf(ge, h[j][e], dw[j][e]);
+                db[j][e] += ge;
+                const float u = ge * w[j][e];
+                s1 += u;
+                s2 = fmaf(u, h[j][e], s2);
+            }
+        const float2 s = fold.sum2(s1, s2);
+        const float m1 = s.x * inv_w, m2 = s.y * inv_w;
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float d = rstd * (fmaf((float)g.v[j][e], w[j][e], -m1) - h[j][e] * m2);
+                if (a.gz.p) d += (float)t.v[j][e];
+                z.v[j][e] = (T)(on ? d : 0.f);
+            }
+        z.store((T*)a.gx.p + b * a.gx.sb + i * a.gx.sr, lane, W);
+    }
+    if (!a.part) return;
+    float* part = a.part + (int64_t)blockIdx.x * 2 * W;
+    if constexpr (GRP == 1) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int at = share_at<LPR, WIDE>(lane, j, e);
+                if (at < W) part[at] = dw[j][e], part[W + at] = db[j][e];
+            }
+    } else {
+        constexpr int C = LPR * CH * 8;
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int at = share_at<LPR, WIDE>(lane, j, e);
+                red[grp * C + at] = dw[j][e];
+                red[(GRP + grp) * C + at] = db[j][e];
+            }
+        __syncthreads();
+        for (int x = threadIdx.x; x < W; x += threads_of<LPR>()) {
+            float sw = 0.f, sb = 0.f;
+#pragma unroll
+            for (int y = 0; y < GRP; ++y) sw += red[y * C + x], sb += red[(GRP + y) * C + x];
+            part[x] = sw;
+            part[W + x] = sb;
+        }
+    }
+}
+
+// dw and db: the workgroups' parts in 64 bits and a fixed order; 64 columns a
+// workgroup, 16 lanes a column.
+__global__ __launch_bounds__(1024) void layer_norm_sum_kernel(const LayerNormArgs a, int blocks) {
+    __shared__ double red[16][64];
+    const int c = threadIdx.x & 63, y = threadIdx.x >> 6;
+    const int64_t x = (int64_t)blockIdx.x * 64 + c;  // of 2 width
+    double s = 0.0;
+    if (x < 2 * a.width) {
+#pragma unroll 4
+        for (int k = y; k < blocks; k += 16) s += (double)a.part[(int64_t)k * 2 * a.width + x];
+    }
+    red[y][c] = s;
+    __syncthreads();
+    if (y || x >= 2 * a.width) return;
+#pragma unroll
+    for (int k = 1; k < 16; ++k) s += red[k][c];
+    if (x < a.width) {
+        if (a.gw) a.gw[x] = (float)s;
+    } else if (a.gb) {
+        a.gb[x - a.width] = (float)s;
+    }
+}
+
+template <int OP, int LPR, int CH, bool WIDE>
+hipError_t launch(const LayerNormArgs& a, bool back, hipStream_t s) {
+    constexpr int GRP = threads_of<LPR>() / LPR;
+    const int64_t groups = ((int64_t)a.B * a.n + GRP - 1) / GRP;
+    if (back)
+        layer_norm_bwd_kernel<OP, LPR, CH, WIDE><<<(unsigned)a.blocks, threads_of<LPR>(), 0, s>>>(a);
+    else
+        layer_norm_kernel<OP, LPR, CH, WIDE>
+            <<<(unsigned)(groups < 4096 ? groups : 4096), threads_of<LPR>(), 0, s>>>(a);
+    return hipGetLastError();
+}
+template <int OP, int LPR, int CH>
+hipError_t launch(const LayerNormArgs& a, bool back, hipStream_t s) {
+    return a.wide ? launch<OP, LPR, CH, true>(a, back, s) : launch<OP, LPR, CH, false>(a, back, s);
+}
+template <int OP>
+hipError_t launch(const LayerNormArgs& a, bool back, hipStream_t s) {
+    if (a.width <= 64) return launch<OP, 8, 1>(a, back, s);
+    if (a.width <= 128) return launch<OP, 16, 1>(a, back, s);
+    if (a.width <= 256) return launch<OP, 32, 1>(a, back, s);
+    if (a.width <= 512) return launch<OP, 64, 1>(a, back, s);
+    if (a.width <= 1024) return launch<OP, 64, 2>(a, back, s);
+    if (a.width <= 2048) return launch<OP, 256, 1>(a, back, s);
+    if (a.width <= 4096) return launch<OP, 256, 2>(a, back, s);
+    if (a.width <= 8192) return launch<OP, 256, 4>(a, back, s);
+    return launch<OP, 1024, 2>(a, back, s);
+}
+hipError_t launch(const LayerNormArgs& a, bool back, hipStream_t s) {
+    return a.op == OP_BF16 ? launch<OP_BF16>(a, back, s)
+           : a.op == OP_F16 ? launch<OP_F16>(a, back, s)
+                            : launch<OP_F32>(a, back, s);
+}
+
+}  // namespace
+
+int layer_norm_bwd_blocks(int64_t rows, int width) {
+    const int grp = width <= 64 ? 32 : width <= 128 ? 16 : width <= 256 ? 8 : width <= 1024 ? 4 : 1;
+    const int64_t b = (rows + grp - 1) / grp;
+    return b < 1 ? 1 : b > 512 ? 512 : (int)b;
+}
+
+hipError_t launch_layer_norm(const LayerNormArgs& a, hipStream_t s) { return launch(a, false, s); }
+
+hipError_t launch_layer_norm_bwd(const LayerNormArgs& a, hipStream_t s) {
+    const bool any = (int64_t)a.B * a.n > 0;  // else the weights' sums are empty
+    const hipError_t e = any ? launch(a, true, s) : hipSuccess;
+    if (e != hipSuccess || !a.part) return e;
+    layer_norm_sum_kernel<<<(unsigned)((2 * a.width + 63) / 64), 1024, 0, s>>>(a, any ? a.blocks : 0);
+    return hipGetLastError();
+}
+
+}  // namespace fs

@@ -1,0 +1,534 @@
+// fs_layers_api.cpp -- host side of include/fs_layers.h: argument checks,
+// workspace layout and the choice of splits.  Nothing here allocates,
+// synchronises or throws.
+#include "fs_layers.h"
+
+#include "fs_host.hpp"
+#include "fs_layers_args.h"
+
+using namespace fs;
+
+namespace {
+
+fs_status check_dtype(int32_t dtype) {
+    if (dtype < FS_DTYPE_F32 || dtype > FS_DTYPE_F16)
+        return fail(FS_ERR_INVALID_ARG, "unknown fs_dtype %d", dtype);
+    return FS_OK;
+}
+
+bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
+
+// An array of `count` elements of `size` bytes that the call needs.
+fs_status take_flat(const char* name, const void* p, int64_t count, size_t size, Extent& e) {
+    e = Extent{};
+    if (count == 0) return FS_OK;
+    if (!p) return fail(FS_ERR_INVALID_ARG, "%s must be non-NULL", name);
+    if ((uintptr_t)p % size)
+        return fail(FS_ERR_INVALID_ARG, "%s is not aligned to its element type", name);
+    e = flat(p, (size_t)count * size);
+    return FS_OK;
+}
+
+// Outputs against the inputs and against one another.  Two views may be slices
+// of one buffer side by side: only those that start together are refused.
+struct Outputs {
+    Extent e[8];
+    const char* name[8];
+    bool view[8];
+    int n = 0;
+    void add(const char* what, const Extent& x, bool is_view = false) {
+        if (x.hi > x.lo) e[n] = x, view[n] = is_view, name[n++] = what;
+    }
+    fs_status check(const Extent* in, int n_in) const {
+        for (int i = 0; i < n; ++i) {
+            FS_TRY(check_apart(name[i], e[i], in, n_in));
+            for (int j = 0; j < i; ++j)
+                if (view[i] && view[j] ? e[i].lo == e[j].lo : e[i].overlaps(e[j]))
+                    return fail(FS_ERR_INVALID_ARG, "%s overlaps %s", name[i], name[j]);
+        }
+        return FS_OK;
+    }
+};
+
+// ---- layer norm -------------------------------------------------------------
+
+fs_status take_norm(const fs_layer_norm_desc* p, LayerNormArgs& a) {
+    if (!p) return fail(FS_ERR_INVALID_ARG, "desc must be non-NULL");
+    const fs_layer_norm_desc& d = *p;
+    FS_TRY(check_dtype(d.dtype));
+    if (d.batch < 0 || d.n < 0 || (int64_t)d.batch * d.n > 0x7fffffff)
+        return fail(FS_ERR_INVALID_ARG,
+                    "batch and n must be >= 0 and their product below 2^31 (got %d, %d)", d.batch,
+                    d.n);
+    if (d.width < 1 || d.width > kNormMaxWidth)
+        return fail(FS_ERR_INVALID_ARG, "width must be in [1, %d] (got %d)", kNormMaxWidth, d.width);
+    if (!(d.eps >= 0.f) || !std::isfinite(d.eps))
+        return fail(FS_ERR_INVALID_ARG, "eps must be >= 0 and finite");
+    a.op = op_of(d.dtype);
+    a.B = d.batch;
+    a.n = d.n;
+    a.width = d.width;
+    a.eps = d.eps;
+    a.lengths = d.lengths;
+    a.blocks = layer_norm_bwd_blocks((int64_t)d.batch * d.n, d.width);
+    return FS_OK;
+}
+
+size_t norm_workspace(const LayerNormArgs& a) {
+    return std::max(kAlign, up((size_t)a.blocks * 2 * a.width * 4));
+}
+
+// Where no length tells the batch's entries apart and they follow one another
+// like their rows, they are one.
+void fold_batch(LayerNormArgs& a, AttnView* const* views, int count) {
+    if (a.lengths || a.B <= 1) return;
+    for (int i = 0; i < count; ++i)
+        if (views[i]->p && a.n > 1 && views[i]->sb != a.n * views[i]->sr) return;
+    for (int i = 0; i < count; ++i)
+        if (a.n == 1) views[i]->sr = views[i]->sb;
+    a.n *= a.B;
+    a.B = 1;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fs_layer_norm_workspace_bytes(const fs_layer_norm_desc* desc) {
+    LayerNormArgs a{};
+    if (take_norm(desc, a) != FS_OK) return 0;
+    return norm_workspace(a);
+}
+
+fs_status fs_layer_norm(const fs_layer_norm_desc* desc, fs_rows x, fs_rows residual,
+                        const float* weight, const float* bias, fs_rows total, fs_rows y,
+                        float* mean, float* rstd, void* stream) {
+    LayerNormArgs a{};
+    FS_TRY(take_norm(desc, a));
+    const int es = elem_size(desc->dtype);
+    const int64_t rows = (int64_t)a.B * a.n;
+    Extent in[5], out[4];
+    if (rows > 0 && !residual.data != !total.data)
+        return fail(FS_ERR_INVALID_ARG, "residual and total are given both or neither");
+    FS_TRY(take_view("x", x, a.B, a.n, 1, a.width, es, false, a.x, in[0]));
+    if (residual.data) {
+        FS_TRY(take_view("residual", residual, a.B, a.n, 1, a.width, es, false, a.r, in[1]));
+        FS_TRY(take_view("total", total, a.B, a.n, 1, a.width, es, true, a.z, out[1]));
+    }
+    FS_TRY(take_view("y", y, a.B, a.n, 1, a.width, es, true, a.y, out[0]));
+    if (weight) FS_TRY(take_flat("weight", weight, a.width, 4, in[2]));
+    if (bias) FS_TRY(take_flat("bias", bias, a.width, 4, in[3]));
+    if (a.lengths) FS_TRY(take_flat("lengths", a.lengths, a.B, 4, in[4]));
+    if (mean) FS_TRY(take_flat("mean", mean, rows, 4, out[2]));
+    if (rstd) FS_TRY(take_flat("rstd", rstd, rows, 4, out[3]));
+    Outputs o;
+    const char* names[4] = {"y", "total", "mean", "rstd"};
+    for (int i = 0; i < 4; ++i) o.add(names[i], out[i], i < 2);
+    FS_TRY(o.check(in, 5));
+    FS_TRY(check_gpu());
+    if (rows == 0) return FS_OK;
+    a.w = weight;
+    a.b = bias;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.wide = a.width % 8 == 0 && a.x.vec && a.y.vec && (!a.r.p || (a.r.vec && a.z.vec)) &&
+             aligned16(weight) && aligned16(bias);
+    AttnView* const views[4] = {&a.x, &a.r, &a.z, &a.y};
+    fold_batch(a, views, 4);
+    return hip_status(launch_layer_norm(a, (hipStream_t)stream), "fs_layer_norm");
+}
+
+fs_status fs_layer_norm_backward(const fs_layer_norm_desc* desc, fs_rows z, const float* weight,
+                                 const float* mean, const float* rstd, fs_rows d_y,
+                                 fs_rows d_total, fs_rows d_x, float* d_weight, float* d_bias,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+    LayerNormArgs a{};
+    FS_TRY(take_norm(desc, a));
+    const int es = elem_size(desc->dtype);
+    const int64_t rows = (int64_t)a.B * a.n;
+    Extent in[8], out[3];
+    FS_TRY(take_view("z", z, a.B, a.n, 1, a.width, es, false, a.x, in[0]));
+    FS_TRY(take_view("d_y", d_y, a.B, a.n, 1, a.width, es, false, a.g, in[1]));
+    if (d_total.data)
+        FS_TRY(take_view("d_total", d_total, a.B, a.n, 1, a.width, es, false, a.gz, in[2]));
+    FS_TRY(take_view("d_x", d_x, a.B, a.n, 1, a.width, es, true, a.gx, out[0]));
+    FS_TRY(take_flat("mean", mean, rows, 4, in[3]));
+    FS_TRY(take_flat("rstd", rstd, rows, 4, in[4]));
+    if (weight) FS_TRY(take_flat("weight", weight, a.width, 4, in[5]));
+    if (a.lengths) FS_TRY(take_flat("lengths", a.lengths, a.B, 4, in[6]));
+    if (d_weight) FS_TRY(take_flat("d_weight", d_weight, a.width, 4, out[1]));
+    if (d_bias) FS_TRY(take_flat("d_bias", d_bias, a.width, 4, out[2]));
+    const size_t need = norm_workspace(a);
+    FS_TRY(check_workspace(workspace, workspace_bytes, need));
+    in[7] = flat(workspace, need);
+    Outputs o;
+    const char* names[3] = {"d_x", "d_weight", "d_bias"};
+    for (int i = 0; i < 3; ++i) o.add(names[i], out[i]);
+    FS_TRY(o.check(in, 8));
+    FS_TRY(check_gpu());
+    a.w = weight;
+    a.mean = const_cast<float*>(mean);
+    a.rstd = const_cast<float*>(rstd);
+    a.gw = d_weight;
+    a.gb = d_bias;
+    a.part = d_weight || d_bias ? (float*)workspace : nullptr;
+    a.wide = a.width % 8 == 0 && a.x.vec && a.g.vec && a.gx.vec && (!a.gz.p || a.gz.vec) &&
+             aligned16(weight);
+    AttnView* const views[4] = {&a.x, &a.g, &a.gz, &a.gx};
+    fold_batch(a, views, 4);
+    return hip_status(launch_layer_norm_bwd(a, (hipStream_t)stream), "fs_layer_norm_backward");
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---- rows in 8-bit integers ---------------------------------------------------
+
+// A matrix of int8 (or other) rows as a view.
+fs_status take_matrix(const char* name, const void* p, int64_t rows, int64_t stride, int64_t width,
+                      int es, bool written, Extent& e) {
+    AttnView v;
+    return take_view(name, fs_rows{const_cast<void*>(p), 0, stride, 0}, 1, width ? rows : 0, 1,
+                     width, es, written, v, e);
+}
+
+constexpr int kProductMaxRows = 1 << 24;
+
+bool product_sizes(int32_t m, int32_t n, int32_t k) {
+    return m >= 0 && n >= 0 && k >= 0 && m <= kProductMaxRows && n <= kProductMaxRows &&
+           (int64_t)m * n <= (int64_t)1 << 36 && k <= kQuantMaxWidth;
+}
+size_t product_workspace(int32_t m, int32_t n, int32_t k, int* split, int* split_k) {
+    *split = product_split(m, n, k, split_k);
+    return *split > 1 ? up((size_t)*split * m * n * 4) : kAlign;
+}
+
+}  // namespace
+
+extern "C" {
+
+fs_status fs_quantize_rows(int32_t dtype, int32_t rows, int32_t width, const void* x,
+                           int64_t x_stride, int8_t* q, int64_t q_stride, float* scale,
+                           void* stream) {
+    FS_TRY(check_dtype(dtype));
+    if (rows < 0 || width < 1 || width > kQuantMaxWidth)
+        return fail(FS_ERR_INVALID_ARG, "needs rows >= 0 and 1 <= width <= %d (got %d, %d)",
+                    kQuantMaxWidth, rows, width);
+    QuantArgs a{};
+    Extent in, out[2];
+    FS_TRY(take_matrix("x", x, rows, x_stride, width, elem_size(dtype), false, in));
+    FS_TRY(take_matrix("q", q, rows, q_stride, width, 1, true, out[0]));
+    FS_TRY(take_flat("scale", scale, rows, 4, out[1]));
+    Outputs o;
+    o.add("q", out[0]);
+    o.add("scale", out[1]);
+    FS_TRY(o.check(&in, 1));
+    FS_TRY(check_gpu());
+    if (rows == 0) return FS_OK;
+    a.op = op_of(dtype);
+    a.rows = rows;
+    a.width = width;
+    a.x = (const char*)x;
+    a.sx = rows > 1 ? x_stride : 0;
+    a.q = q;
+    a.sq = rows > 1 ? q_stride : 0;
+    a.scale = scale;
+    a.wide = width % 8 == 0 && aligned16(x) && a.sx * elem_size(dtype) % 16 == 0 &&
+             (uintptr_t)q % 8 == 0 && a.sq % 8 == 0;
+    return hip_status(launch_quantize(a, (hipStream_t)stream), "fs_quantize_rows");
+}
+
+size_t fs_quantized_product_workspace_bytes(int32_t m, int32_t n, int32_t k) {
+    if (!product_sizes(m, n, k)) {
+        (void)fail(FS_ERR_INVALID_ARG, "m, n or k is out of range (got %d, %d, %d)", m, n, k);
+        return 0;
+    }
+    int split, split_k;
+    return product_workspace(m, n, k, &split, &split_k);
+}
+
+fs_status fs_quantized_product(const fs_quantized_product_desc* desc, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    if (!desc) return fail(FS_ERR_INVALID_ARG, "desc must be non-NULL");
+    const fs_quantized_product_desc& d = *desc;
+    FS_TRY(check_dtype(d.dtype));
+    if (!product_sizes(d.m, d.n, d.k))
+        return fail(FS_ERR_INVALID_ARG,
+                    "needs 0 <= m, n <= 2^24, m n <= 2^36 and 0 <= k <= %d (got %d, %d, %d)",
+                    kQuantMaxWidth, d.m, d.n, d.k);
+    Extent in[6], out;
+    const bool any = d.m > 0 && d.n > 0;
+    const int m = any ? d.m : 0, n = any ? d.n : 0;
+    FS_TRY(take_matrix("q_x", d.q_x, m, d.q_x_stride, d.k, 1, false, in[0]));
+    FS_TRY(take_matrix("q_w", d.q_w, n, d.q_w_stride, d.k, 1, false, in[1]));
+    FS_TRY(take_flat("scale_x", d.scale_x, m, 4, in[2]));
+    FS_TRY(take_flat("scale_w", d.scale_w, n, 4, in[3]));
+    if (d.bias) FS_TRY(take_flat("bias", d.bias, n, 4, in[4]));
+    FS_TRY(take_matrix("y", d.y, m, d.y_stride, n, elem_size(d.dtype), true, out));
+    ProductArgs a{};
+    const size_t need = product_workspace(d.m, d.n, d.k, &a.split, &a.split_k);
+    FS_TRY(check_workspace(workspace, workspace_bytes, need));
+    in[5] = flat(workspace, need);
+    FS_TRY(check_apart("y", out, in, 6));
+    FS_TRY(check_gpu());
+    if (!any) return FS_OK;
+    a.op = op_of(d.dtype);
+    a.m = m;
+    a.n = n;
+    a.k = d.k;
+    a.x = d.q_x;
+    a.sx = m > 1 ? d.q_x_stride : 0;
+    a.scale_x = d.scale_x;
+    a.w = d.q_w;
+    a.sw = n > 1 ? d.q_w_stride : 0;
+    a.scale_w = d.scale_w;
+    a.bias = d.bias;
+    a.y = (char*)d.y;
+    a.sy = m > 1 ? d.y_stride : 0;
+    // (offsets within a tile of 256 rows stay 32-bit numbers)
+    constexpr int64_t kStride = 1 << 22;
+    a.aligned = d.k % 16 == 0 && aligned16(d.q_x) && aligned16(d.q_w) && a.sx % 16 == 0 &&
+                a.sw % 16 == 0 && a.sx <= kStride && a.sw <= kStride;
+    a.part = (int*)workspace;
+    return hip_status(launch_product(a, (hipStream_t)stream), "fs_quantized_product");
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---- distillation --------------------------------------------------------------
+
+fs_status take_distill(const fs_distill_desc* p, DistillArgs& a) {
+    if (!p) return fail(FS_ERR_INVALID_ARG, "desc must be non-NULL");
+    const fs_distill_desc& d = *p;
+    FS_TRY(check_dtype(d.dtype));
+    if (d.rows < 0 || d.classes < 1 || d.classes > 1 << 24)
+        return fail(FS_ERR_INVALID_ARG, "needs rows >= 0 and 1 <= classes <= 2^24 (got %d, %d)",
+                    d.rows, d.classes);
+    if (d.k < 1 || d.k > kDistillMaxTop)
+        return fail(FS_ERR_INVALID_ARG, "k must be in [1, %d] (got %d)", kDistillMaxTop, d.k);
+    if (!(d.temperature >= 0x1p-20f && d.temperature <= 0x1p20f))
+        return fail(FS_ERR_INVALID_ARG, "temperature must be in [2^-20, 2^20]");
+    a.op = op_of(d.dtype);
+    a.rows = d.rows;
+    a.classes = d.classes;
+    a.k = d.k;
+    a.T = d.temperature;
+    a.ids = d.ids;
+    a.teacher = d.teacher;
+    a.teacher_lse = d.teacher_lse;
+    a.active = d.active;
+    a.split = distill_split(d.rows, d.classes, &a.split_cols);
+    return FS_OK;
+}
+
+size_t distill_workspace(const DistillArgs& a) {
+    return a.split > 1 ? up((size_t)a.rows * a.split * sizeof(float2)) : kAlign;
+}
+
+// The logits, the teacher and the row mask; four extents.
+fs_status distill_inputs(const fs_distill_desc& d, fs_rows logits, DistillArgs& a, bool& vec,
+                         Extent* in) {
+    AttnView v;
+    FS_TRY(take_view("logits", logits, 1, a.rows, 1, a.classes, elem_size(d.dtype), false, v, in[0]));
+    FS_TRY(take_flat("ids", d.ids, (int64_t)a.rows * a.k, 4, in[1]));
+    FS_TRY(take_flat("teacher", d.teacher, (int64_t)a.rows * a.k, 4, in[2]));
+    in[3] = in[4] = Extent{};
+    if (d.teacher_lse) FS_TRY(take_flat("teacher_lse", d.teacher_lse, a.rows, 4, in[3]));
+    if (d.active) FS_TRY(take_flat("active", d.active, a.rows, 1, in[4]));
+    a.x = v.p;
+    a.sx = v.sr;
+    vec = v.vec;
+    return FS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fs_distill_workspace_bytes(const fs_distill_desc* desc) {
+    DistillArgs a{};
+    if (take_distill(desc, a) != FS_OK) return 0;
+    return distill_workspace(a);
+}
+
+fs_status fs_distill_loss(const fs_distill_desc* desc, fs_rows logits, float* loss, float* lse,
+                          const float* d_loss, fs_rows d_logits, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+    DistillArgs a{};
+    FS_TRY(take_distill(desc, a));
+    Extent in[7], out[3];
+    bool vec = false;
+    FS_TRY(distill_inputs(*desc, logits, a, vec, in));
+    FS_TRY(take_flat("loss", loss, a.rows, 4, out[0]));
+    FS_TRY(take_flat("lse", lse, a.rows, 4, out[1]));
+    if (a.rows > 0 && !d_loss != !d_logits.data)
+        return fail(FS_ERR_INVALID_ARG, "d_loss and d_logits are given both or neither");
+    AttnView g{};
+    if (d_logits.data) {
+        FS_TRY(take_flat("d_loss", d_loss, a.rows, 4, in[5]));
+        FS_TRY(take_view("d_logits", d_logits, 1, a.rows, 1, a.classes, elem_size(desc->dtype), true,
+                         g, out[2]));
+    }
+    const size_t need = distill_workspace(a);
+    FS_TRY(check_workspace(workspace, workspace_bytes, need));
+    in[6] = flat(workspace, need);
+    Outputs o;
+    const char* names[3] = {"loss", "lse", "d_logits"};
+    for (int i = 0; i < 3; ++i) o.add(names[i], out[i]);
+    FS_TRY(o.check(in, 7));
+    FS_TRY(check_gpu());
+    if (a.rows == 0) return FS_OK;
+    a.gx = g.p;
+    a.sgx = g.sr;
+    a.wide = vec && (!g.p || g.vec) && a.classes % 8 == 0;
+    a.loss = loss;
+    a.lse = lse;
+    a.gloss = d_loss;
+    a.part = (float2*)workspace;
+    return hip_status(launch_distill(a, (hipStream_t)stream), "fs_distill_loss");
+}
+
+fs_status fs_distill_loss_backward(const fs_distill_desc* desc, fs_rows logits, const float* lse,
+                                   const float* d_loss, fs_rows d_logits, void* stream) {
+    DistillArgs a{};
+    FS_TRY(take_distill(desc, a));
+    Extent in[7], out;
+    bool vec = false;
+    FS_TRY(distill_inputs(*desc, logits, a, vec, in));
+    FS_TRY(take_flat("lse", lse, a.rows, 4, in[5]));
+    FS_TRY(take_flat("d_loss", d_loss, a.rows, 4, in[6]));
+    AttnView g{};
+    FS_TRY(take_view("d_logits", d_logits, 1, a.rows, 1, a.classes, elem_size(desc->dtype), true, g,
+                     out));
+    FS_TRY(check_apart("d_logits", out, in, 7));
+    FS_TRY(check_gpu());
+    if (a.rows == 0) return FS_OK;
+    a.gx = g.p;
+    a.sgx = g.sr;
+    a.wide = vec && g.vec && a.classes % 8 == 0;
+    a.lse = const_cast<float*>(lse);
+    a.gloss = d_loss;
+    return hip_status(launch_distill(a, (hipStream_t)stream), "fs_distill_loss_backward");
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---- balanced use of the columns -----------------------------------------------
+
+fs_status take_balance(const fs_balance_desc* p, BalanceArgs& a) {
+    if (!p) return fail(FS_ERR_INVALID_ARG, "desc must be non-NULL");
+    const fs_balance_desc& d = *p;
+    FS_TRY(check_dtype(d.dtype));
+    if (d.batch < 0 || d.n < 0 || d.batch > 65535 || (int64_t)d.batch * d.n > 0x7fffffff)
+        return fail(FS_ERR_INVALID_ARG,
+                    "needs 0 <= batch <= 65535, n >= 0 and batch * n below 2^31 (got %d, %d)",
+                    d.batch, d.n);
+    if (d.experts < 1 || d.experts > kBalanceMaxExperts)
+        return fail(FS_ERR_INVALID_ARG, "experts must be in [1, %d] (got %d)", kBalanceMaxExperts,
+                    d.experts);
+    if (d.k < 1 || d.k > std::min(kBalanceMaxTop, d.experts))
+        return fail(FS_ERR_INVALID_ARG, "k must be in [1, min(%d, experts)] (got %d)",
+                    kBalanceMaxTop, d.k);
+    a.op = op_of(d.dtype);
+    a.B = d.batch;
+    a.n = d.n;
+    a.E = d.experts;
+    a.k = d.k;
+    a.normalize = d.normalize != 0;
+    a.lengths = d.lengths;
+    a.blocks = balance_blocks(d.batch, d.n, d.experts);
+    return FS_OK;
+}
+
+struct BalanceLayout {
+    size_t c = 0, s = 0, total = kAlign;
+};
+BalanceLayout balance_layout(const BalanceArgs& a) {
+    BalanceLayout l;
+    if (a.blocks > 1) {
+        const size_t parts = (size_t)a.B * a.blocks;
+        l.c = up(parts * a.E * 4);
+        l.s = l.c + up(parts * a.E * 4);
+        l.total = l.s + up(parts * sizeof(float2));
+    }
+    return l;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fs_balance_workspace_bytes(const fs_balance_desc* desc) {
+    BalanceArgs a{};
+    if (take_balance(desc, a) != FS_OK) return 0;
+    return balance_layout(a).total;
+}
+
+fs_status fs_balance_loss(const fs_balance_desc* desc, fs_rows logits, int32_t* ids, float* gates,
+                          int32_t* counts, float* loss, float* lse, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+    BalanceArgs a{};
+    FS_TRY(take_balance(desc, a));
+    const int64_t rows = (int64_t)a.B * a.n;
+    Extent in[3], out[5];
+    FS_TRY(take_view("logits", logits, a.B, a.n, 1, a.E, elem_size(desc->dtype), false, a.x, in[0]));
+    if (a.lengths) FS_TRY(take_flat("lengths", a.lengths, a.B, 4, in[1]));
+    FS_TRY(take_flat("ids", ids, rows * a.k, 4, out[0]));
+    FS_TRY(take_flat("gates", gates, rows * a.k, 4, out[1]));
+    FS_TRY(take_flat("counts", counts, (int64_t)a.B * a.E, 4, out[2]));
+    FS_TRY(take_flat("loss", loss, 2 * (int64_t)a.B, 4, out[3]));
+    FS_TRY(take_flat("lse", lse, rows, 4, out[4]));
+    const BalanceLayout l = balance_layout(a);
+    FS_TRY(check_workspace(workspace, workspace_bytes, l.total));
+    in[2] = flat(workspace, l.total);
+    Outputs o;
+    const char* names[5] = {"ids", "gates", "counts", "loss", "lse"};
+    for (int i = 0; i < 5; ++i) o.add(names[i], out[i]);
+    FS_TRY(o.check(in, 3));
+    FS_TRY(check_gpu());
+    if (a.B == 0) return FS_OK;
+    a.wide = a.x.vec && a.E % 8 == 0;
+    a.ids = ids;
+    a.gates = gates;
+    a.counts = counts;
+    a.loss = loss;
+    a.lse = lse;
+    a.part_p = (float*)workspace;
+    a.part_c = (int*)((char*)workspace + l.c);
+    a.part_s = (float2*)((char*)workspace + l.s);
+    return hip_status(launch_balance(a, (hipStream_t)stream), "fs_balance_loss");
+}
+
+fs_status fs_balance_loss_backward(const fs_balance_desc* desc, fs_rows logits, const int32_t* ids,
+                                   const int32_t* counts, const float* lse, const float* d_loss,
+                                   const float* d_gates, fs_rows d_logits, void* stream) {
+    BalanceArgs a{};
+    FS_TRY(take_balance(desc, a));
+    const int64_t rows = (int64_t)a.B * a.n;
+    Extent in[7], out;
+    FS_TRY(take_view("logits", logits, a.B, a.n, 1, a.E, elem_size(desc->dtype), false, a.x, in[0]));
+    if (a.lengths) FS_TRY(take_flat("lengths", a.lengths, a.B, 4, in[1]));
+    FS_TRY(take_flat("ids", ids, rows * a.k, 4, in[2]));
+    FS_TRY(take_flat("counts", counts, (int64_t)a.B * a.E, 4, in[3]));
+    FS_TRY(take_flat("lse", lse, rows, 4, in[4]));
+    FS_TRY(take_flat("d_loss", d_loss, 2 * (int64_t)a.B, 4, in[5]));
+    if (d_gates) FS_TRY(take_flat("d_gates", d_gates, rows * a.k, 4, in[6]));
+    FS_TRY(take_view("d_logits", d_logits, a.B, a.n, 1, a.E, elem_size(desc->dtype), true, a.gx, out));
+    FS_TRY(check_apart("d_logits", out, in, 7));
+    FS_TRY(check_gpu());
+    if (rows == 0) return FS_OK;
+    a.wide = a.x.vec && a.gx.vec && a.E % 8 == 0;
+    a.ids = const_cast<int32_t*>(ids);
+    a.counts = const_cast<int32_t*>(counts);
+    a.lse = const_cast<float*>(lse);
+    a.gloss = d_loss;
+    a.ggates = d_gates;
+    return hip_status(launch_balance_bwd(a, (hipStream_t)stream), "fs_balance_loss_backward");
+}
+
+}  // extern "C"

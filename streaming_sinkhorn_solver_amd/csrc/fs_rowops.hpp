@@ -1,0 +1,160 @@
+// fs_rowops.hpp -- device-side pieces of the kernels that work on whole rows:
+// sums and maxima over a row's lanes, and a lane's share of a row's elements.
+#pragma once
+
+#include "fs_attn.hpp"
+
+namespace fs {
+
+// Lane l's value at lane l ^ O (O < 16: of a mirror image, for which the lanes
+// below O agree already; 16, 32: of the other row or half).
+template <int O>
+__device__ __forceinline__ uint32_t lane_other(uint32_t x) {
+    if constexpr (O == 1) return __builtin_amdgcn_update_dpp(x, x, 0xB1, 0xF, 0xF, false);
+    if constexpr (O == 2) return __builtin_amdgcn_update_dpp(x, x, 0x4E, 0xF, 0xF, false);
+    if constexpr (O == 4) return __builtin_amdgcn_update_dpp(x, x, 0x141, 0xF, 0xF, false);
+    if constexpr (O == 8) return __builtin_amdgcn_update_dpp(x, x, 0x140, 0xF, 0xF, false);
+    const bool upper = threadIdx.x & O;
+    if constexpr (O == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+        return upper ? r[0] : r[1];
+    }
+    if constexpr (O == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+        return upper ? r[0] : r[1];
+    }
+}
+template <int O>
+__device__ __forceinline__ float lane_other(float x) {
+    return __uint_as_float(lane_other<O>(__float_as_uint(x)));
+}
+
+// f over the LPR lanes (a power of two, up to 64) of a lane group; all lanes get
+// the result, and the same bits.
+template <int LPR, typename V, typename F>
+__device__ __forceinline__ V lanes_fold(V x, F f) {
+    if constexpr (LPR > 1) x = f(x, lane_other<1>(x));
+    if constexpr (LPR > 2) x = f(x, lane_other<2>(x));
+    if constexpr (LPR > 4) x = f(x, lane_other<4>(x));
+    if constexpr (LPR > 8) x = f(x, lane_other<8>(x));
+    if constexpr (LPR > 16) x = f(x, lane_other<16>(x));
+    if constexpr (LPR > 32) x = f(x, lane_other<32>(x));
+    return x;
+}
+template <int LPR>
+__device__ __forceinline__ float lanes_sum(float x) {
+    return lanes_fold<LPR>(x, [](float a, float b) { return a + b; });
+}
+template <int LPR>
+__device__ __forceinline__ float lanes_max(float x) {
+    return lanes_fold<LPR>(x, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int LPR>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
+    return lanes_fold<LPR>(x, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+
+// Sums over the LPR threads of a row, of whole waves if more than 64: the waves'
+// sums meet in LDS.  Two buffers in turn, so that one barrier a sum is enough: a
+// buffer is written again only behind the next sum's barrier, in front of which
+// everyone has read it.
+template <int LPR>
+struct RowFold {
+    static constexpr int kWaves = LPR > 64 ? LPR / 64 : 1;
+    float2* buf;  // [2 kWaves] in LDS
+    int turn = 0;
+    __device__ __forceinline__ explicit RowFold(float2* b) : buf(b) {}
+    __device__ __forceinline__ float2 sum2(float a, float b) {
+        constexpr int L = LPR > 64 ? 64 : LPR;
+        a = lanes_sum<L>(a);
+        b = lanes_sum<L>(b);
+        if constexpr (LPR > 64) {
+            float2* at = buf + turn * kWaves;
+            if ((threadIdx.x & 63) == 0) at[threadIdx.x >> 6] = make_float2(a, b);
+            __syncthreads();
+            a = b = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) a += at[w].x, b += at[w].y;
+            turn ^= 1;
+        }
+        return make_float2(a, b);
+    }
+    __device__ __forceinline__ float sum(float a) {
+        constexpr int L = LPR > 64 ? 64 : LPR;
+        a = lanes_sum<L>(a);
+        if constexpr (LPR > 64) {
+            float2* at = buf + turn * kWaves;
+            if ((threadIdx.x & 63) == 0) at[threadIdx.x >> 6].x = a;
+            __syncthreads();
+            a = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) a += at[w].x;
+            turn ^= 1;
+        }
+        return a;
+    }
+    __device__ __forceinline__ uint32_t max_bits(uint32_t a) {
+        constexpr int L = LPR > 64 ? 64 : LPR;
+        a = lanes_max<L>(a);
+        if constexpr (LPR > 64) {
+            float2* at = buf + turn * kWaves;
+            if ((threadIdx.x & 63) == 0) at[threadIdx.x >> 6].x = __uint_as_float(a);
+            __syncthreads();
+            a = 0;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) a = max(a, __float_as_uint(at[w].x));
+            turn ^= 1;
+        }
+        return a;
+    }
+};
+
+// A lane's share of a row of `width` elements: CH groups of 8.  WIDE: groups of
+// neighbours, read with 16 bytes a lane (rows are whole, aligned groups); else
+// single elements, LPR apart, so that a wave reads neighbours.
+template <int LPR, bool WIDE>
+__device__ __forceinline__ int share_at(int lane, int j, int e) {
+    return WIDE ? (lane + j * LPR) * 8 + e : (j * 8 + e) * LPR + lane;
+}
+
+template <typename T, int LPR, int CH, bool WIDE>
+struct Share {
+    T v[CH][8];
+    // on: the row is there; nothing is read else, and zeros stand for it.
+    __device__ __forceinline__ void load(const T* row, int lane, int width, bool on) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            if constexpr (WIDE) {
+                const int at = share_at<LPR, true>(lane, j, 0);
+                if (on && at < width)
+                    __builtin_memcpy(v[j], __builtin_assume_aligned(row + at, 16), sizeof(v[j]));
+                else
+                    __builtin_memset(v[j], 0, sizeof(v[j]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int at = share_at<LPR, false>(lane, j, e);
+                    v[j][e] = on && at < width ? row[at] : (T)0.f;
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void store(T* row, int lane, int width) const {
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            if constexpr (WIDE) {
+                const int at = share_at<LPR, true>(lane, j, 0);
+                if (at < width)
+                    __builtin_memcpy(__builtin_assume_aligned(row + at, 16), v[j], sizeof(v[j]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int at = share_at<LPR, false>(lane, j, e);
+                    if (at < width) row[at] = v[j][e];
+                }
+            }
+        }
+    }
+};
+
+}  // namespace fs
