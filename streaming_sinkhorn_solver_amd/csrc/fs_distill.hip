@@ -3,9 +3,9 @@
 //   p = softmax(x / T), tau = the teacher's weights of a row's few entries, W
 //   their sum: loss = T^2 sum tau (log tau - log p[id]),
 //   dx_c = dloss T (W p_c - sum_{id = c} tau).
-// Bound by memory: a row's log-sum-exp is formed in one pass with a running
-// maximum, the gradient in a second one over the row that comes from the caches
-// (a workgroup's row was read a moment ago).  Where rows are few, several
+// Bound by memory.  A workgroup reads its row (or its range of one) once and keeps
+// it in registers over the row's maximum, sum and gradient; rows that are too long
+// for that are read a second time for the gradient.  Where rows are few, several
 // workgroups share one and meet in a second launch.
 #include "fs_layers_args.h"
 #include "fs_rowops.hpp"
@@ -43,35 +43,58 @@ struct Running {
 #pragma unroll
         for (int e = 0; e < 8; ++e) s += ex2((x[e] - m) * c);
     }
+    __device__ __forceinline__ float under(float top, float c) const {
+        return m == -INFINITY ? s : s * ex2((m - top) * c);
+    }
 };
 
 template <int NT>
-__device__ __forceinline__ float block_fold(float x, bool sum, float* buf) {
-    x = sum ? lanes_sum<64>(x) : lanes_max<64>(x);
+__device__ __forceinline__ float block_max(float x, float* buf) {
+    x = lanes_max<64>(x);
     if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = x;
-    __syncthreads();
+    stage_barrier();
     x = buf[0];
 #pragma unroll
-    for (int w = 1; w < NT / 64; ++w) x = sum ? x + buf[w] : fmaxf(x, buf[w]);
-    __syncthreads();
+    for (int w = 1; w < NT / 64; ++w) x = fmaxf(x, buf[w]);
+    return x;
+}
+template <int NT>
+__device__ __forceinline__ float block_sum(float x, float* buf) {
+    x = lanes_sum<64>(x);
+    if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = x;
+    stage_barrier();
+    x = buf[0];
+#pragma unroll
+    for (int w = 1; w < NT / 64; ++w) x += buf[w];
     return x;
 }
 
-// The sum over threads, ranges, of (m, s) under their common maximum.
-template <int NT>
-__device__ __forceinline__ float2 block_running(Running r, float c, float* buf) {
-    const float top = block_fold<NT>(r.m, false, buf);
-    const float s = r.m == -INFINITY ? r.s : r.s * ex2((r.m - top) * c);
-    return make_float2(top, block_fold<NT>(s, true, buf));
+// From here on the compiler knows nothing of v any more: what is kept over a
+// barrier are the logits as they were read, not their fp32 forms (twice the
+// registers).
+template <typename T>
+__device__ __forceinline__ void forget(T (&v)[8]) {
+    constexpr int N = 8 * sizeof(T) / 4;
+    uint32_t w[N];
+    __builtin_memcpy(w, v, sizeof(w));
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(w[i]));
+    __builtin_memcpy(v, w, sizeof(w));
 }
 
-template <int OP, int NT, bool WIDE, int MODE>
-__global__ __launch_bounds__(NT) void distill_kernel(const DistillArgs a, int sections) {
+// NT threads, of which each keeps the first CH groups of 8 of its range in
+// registers; REST: there may be more, which are read once more for the gradient.
+// (Rows of 1024 threads: 64 registers, so that two fit a CU and one's reads and
+// writes run beside the other's exponentials.)
+template <int OP, int NT, int CH, bool REST, bool WIDE, int MODE>
+__global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void distill_kernel(const DistillArgs a,
+                                                                         int sections) {
     using T = typename El<OP>::T;
-    constexpr int U = 4, kStep = 8 * NT;
-    __shared__ float buf[NT / 64];
-    __shared__ int ids[kDistillMaxTop];
-    __shared__ float tau[kDistillMaxTop];
+    constexpr int U = 2, kStep = 8 * NT;
+    __shared__ float buf[2][NT / 64];
+    __shared__ __align__(16) int ids[kDistillMaxTop + 4];
+    __shared__ __align__(16) float tau[kDistillMaxTop + 4];
+    __shared__ float mass[2];
     const int64_t block = flat_block();
     const int64_t row = block / sections;
     const int sec = (int)(block - row * sections), tid = threadIdx.x;
@@ -82,126 +105,190 @@ __global__ __launch_bounds__(NT) void distill_kernel(const DistillArgs a, int se
     const float c = kLog2e / a.T, inv_t = 1.f / a.T;
     const bool on = !a.active || a.active[row];
 
-    const auto load = [&](int at, T(&v)[8]) {
+    // this thread's eight of the 8 NT columns from lo + `col` on; -inf behind the end
+    constexpr uint32_t ES = sizeof(T);
+    const uint32_t size = (uint32_t)(hi - lo), off = WIDE ? tid * 8 : tid;
+    const RowBuffer from(x + lo, size * ES), to(gx + lo, a.gx ? size * ES : 0);
+    const auto load = [&](uint32_t col, T(&v)[8]) {
         if constexpr (WIDE) {
-            if (at < hi)
-                __builtin_memcpy(v, __builtin_assume_aligned(x + at, 16), sizeof(v));
-            else
+            const uint32_t at = col + off;
+            u32x4 w[ES / 2];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = (T)-INFINITY;
+            for (uint32_t i = 0; i < ES / 2; ++i) {
+                w[i] = from.read16(at * ES + 16 * i);
+                constexpr uint32_t none = OP == OP_F32    ? 0xff800000u
+                                          : OP == OP_BF16 ? 0xff80ff80u
+                                                          : 0xfc00fc00u;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[i][e] = at < size ? w[i][e] : none;
+            }
+            __builtin_memcpy(v, w, sizeof(v));
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = at + e * NT < hi ? x[at + e * NT] : (T)-INFINITY;
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t at = col + off + e * NT;
+                const T t = from.read<T>(at * ES);
+                v[e] = at < size ? t : (T)-INFINITY;
+            }
         }
     };
-    const auto store = [&](int at, const T(&v)[8]) {
+    const auto store = [&](uint32_t col, const T(&v)[8]) {
         if constexpr (WIDE) {
-            if (at < hi) __builtin_memcpy(__builtin_assume_aligned(gx + at, 16), v, sizeof(v));
+            u32x4 w[ES / 2];
+            __builtin_memcpy(w, v, sizeof(v));
+#pragma unroll
+            for (uint32_t i = 0; i < ES / 2; ++i) to.write16((col + off) * ES + 16 * i, w[i]);
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (at + e * NT < hi) gx[at + e * NT] = v[e];
+            for (int e = 0; e < 8; ++e) to.write<T>((col + off + e * NT) * ES, v[e]);
         }
     };
-    const int first = lo + (WIDE ? tid * 8 : tid);
+
+    // the first reads of the range, under way while the teacher's entries are worked on
+    T v[CH > 0 ? CH : 1][8];
+    constexpr uint32_t rest = CH * kStep;
+    if (CH > 0 && on && (MODE == WHOLE || MODE == PARTS || a.gx)) {
+#pragma unroll
+        for (int u = 0; u < CH; ++u) load(u * kStep, v[u]);
+    }
+
+    // The teacher's weights, by the first wave: id (-1: none) and tau of each entry;
+    // a lane keeps log tau of its first ones, the usual case being all of them.
+    constexpr int KEEP = 2;
+    float log_tau[KEEP], ref = 0.f, weight = 0.f;
+    if (MODE != PARTS && tid < 64) {
+        float top = -INFINITY;
+        for (int k = tid; k < a.k; k += 64) {
+            int id = -1;
+            float t = -INFINITY;
+            if (on) {
+                id = a.ids[row * a.k + k];
+                if (id >= 0 && id < a.classes) t = a.teacher[row * a.k + k] * inv_t;
+                if (t == -INFINITY) id = -1;
+            }
+            ids[k] = id;
+            tau[k] = t;
+            top = fmaxf(top, t);
+        }
+        if (tid < 4) ids[a.k + tid] = -1, tau[a.k + tid] = 0.f;  // whole groups of four
+        if (a.teacher_lse) {
+            ref = on ? a.teacher_lse[row] : 0.f;  // the log of the weights' divisor
+        } else {
+            top = lanes_max<64>(top);
+            float s = 0.f;
+            for (int k = tid; k < a.k; k += 64)
+                if (ids[k] >= 0) s += ex2((tau[k] - top) * kLog2e);
+            ref = top + logf(lanes_sum<64>(s));
+        }
+        int n = 0;
+#pragma unroll
+        for (int q = 0; q < KEEP; ++q) log_tau[q] = 0.f;
+        for (int k = tid; k < a.k; k += 64, ++n) {
+            const float lt = tau[k] - ref, w = ids[k] >= 0 ? ex2(lt * kLog2e) : 0.f;
+#pragma unroll
+            for (int q = 0; q < KEEP; ++q) log_tau[q] = n == q ? lt : log_tau[q];
+            tau[k] = w;
+            weight += w;
+        }
+        weight = lanes_sum<64>(weight);
+        if (tid == 0) mass[0] = weight;
+    }
 
     // the row's (or the range's) maximum and sum
     float2 ms = make_float2(-INFINITY, 0.f);
     if constexpr (MODE == WHOLE || MODE == PARTS) {
+        Running r;
         if (on) {
-            Running r;
-            for (int at = first; at < hi; at += U * kStep) {
-                T v[U][8];
 #pragma unroll
-                for (int u = 0; u < U; ++u) load(at + u * kStep, v[u]);
-#pragma unroll
-                for (int u = 0; u < U; ++u) r.add(v[u], c);
+            for (int u = 0; u < CH; ++u) {
+                forget(v[u]);
+                r.add(v[u], c);
+                forget(v[u]);
             }
-            ms = block_running<NT>(r, c, buf);
+            if constexpr (REST)
+                for (uint32_t at = rest; at < size; at += U * kStep) {
+                    T w[U][8];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) load(at + u * kStep, w[u]);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) r.add(w[u], c);
+                }
         }
+        ms.x = block_max<NT>(r.m, buf[0]);
+        ms.y = block_sum<NT>(r.under(ms.x, c), buf[1]);
         if constexpr (MODE == PARTS) {
             if (tid == 0) a.part[row * a.split + sec] = ms;
             return;
         }
     }
-    if constexpr (MODE == JOIN) {
+    if constexpr (MODE == JOIN) {  // every wave for itself: at most 64 ranges
         Running r;
-        if (on && tid < a.split) {
-            const float2 p = a.part[row * a.split + tid];
+        const int lane = tid & 63;
+        if (lane < a.split) {
+            const float2 p = a.part[row * a.split + lane];
             r.m = p.x, r.s = p.y;
         }
-        ms = block_running<NT>(r, c, buf);
+        ms.x = lanes_max<64>(r.m);
+        ms.y = lanes_sum<64>(r.under(ms.x, c));
     }
     const float lse = MODE == BACK ? (on ? a.lse[row] : 0.f)
                                    : ms.y == 0.f ? -INFINITY : fmaf(ms.x, inv_t, logf(ms.y));
-    const float g = a.gx ? a.gloss[row] : 0.f;
-    bool some = on && lse != -INFINITY && (MODE != BACK || g != 0.f);
-
-    // the teacher's weights: (log tau, then tau) of each entry, NaN ones too
-    float weight = 0.f;
-    if (some) {
-        float top = -INFINITY;
-        for (int k = tid; k < a.k; k += NT) {
-            int id = a.ids[row * a.k + k];
-            float t = -INFINITY;
-            if (id >= 0 && id < a.classes) t = a.teacher[row * a.k + k] * inv_t;
-            if (t == -INFINITY) id = -1;
-            ids[k] = id;
-            tau[k] = t;
-            top = fmaxf(top, t);
+    if (MODE != BACK && sec == 0 && tid < 64) {
+        float sum = 0.f;
+        const bool some = lse != -INFINITY && weight != 0.f;
+        if (some) {
+            int n = 0;
+            for (int k = tid; k < a.k; k += 64, ++n) {
+                const int id = ids[k];
+                const float w = tau[k];
+                if (id < 0 || w == 0.f) continue;
+                float lt = 0.f;
+#pragma unroll
+                for (int q = 0; q < KEEP; ++q) lt = n == q ? log_tau[q] : lt;
+                if (n >= KEEP) lt = a.teacher[row * a.k + k] * inv_t - ref;
+                sum = fmaf(w, lt - fmaf((float)x[id], inv_t, -lse), sum);
+            }
+            sum = lanes_sum<64>(sum);
         }
-        float ref;  // log of the weights' divisor
-        if (a.teacher_lse) {
-            ref = a.teacher_lse[row];
-        } else {
-            top = block_fold<NT>(top, false, buf);
-            float s = 0.f;
-            for (int k = tid; k < a.k; k += NT)
-                if (ids[k] >= 0) s += ex2((tau[k] - top) * kLog2e);
-            s = block_fold<NT>(s, true, buf);
-            ref = top + logf(s);
+        if (tid == 0) {
+            a.loss[row] = some ? a.T * a.T * sum : 0.f;
+            a.lse[row] = on ? lse : 0.f;
         }
-        float sum = 0.f, all = 0.f;
-        for (int k = tid; k < a.k; k += NT) {
-            if (ids[k] < 0) continue;
-            const float lt = tau[k] - ref, w = ex2(lt * kLog2e);
-            tau[k] = w;
-            all += w;
-            if (MODE != BACK && sec == 0 && w != 0.f)
-                sum = fmaf(w, lt - fmaf((float)x[ids[k]], inv_t, -lse), sum);
-        }
-        weight = block_fold<NT>(all, true, buf);
-        some = weight != 0.f;
-        if (MODE != BACK && sec == 0) {
-            sum = block_fold<NT>(sum, true, buf);
-            if (tid == 0) a.loss[row] = some ? a.T * a.T * sum : 0.f;
-        }
-    } else if (MODE != BACK && sec == 0 && tid == 0) {
-        a.loss[row] = 0.f;
     }
-    if (MODE != BACK && sec == 0 && tid == 0) a.lse[row] = on ? lse : 0.f;
     if (!a.gx) return;
 
-    if (!some || g == 0.f) {
+    stage_barrier();
+    weight = mass[0];
+    const float g = a.gloss[row];
+    if (!on || lse == -INFINITY || weight == 0.f || g == 0.f) {
         const T zero[8] = {};
-        for (int at = first; at < hi; at += kStep) store(at, zero);
+        for (uint32_t at = 0; at < size; at += kStep) store(at, zero);
         return;
     }
     // p_c = p1 2^((f x_c - f0) f2)
     const float f = MODE == BACK ? inv_t : 1.f, f0 = MODE == BACK ? lse : ms.x;
     const float f2 = MODE == BACK ? kLog2e : c, p1 = MODE == BACK ? 1.f : 1.f / ms.y;
     const float gt = g * a.T, gp = gt * weight * p1;
-    for (int at = first; at < hi; at += U * kStep) {
-        T v[U][8];
+    const auto grad = [&](float xc) { return gp * ex2(fmaf(xc, f, -f0) * f2); };
 #pragma unroll
-        for (int u = 0; u < U; ++u) load(at + u * kStep, v[u]);
+    for (int u = 0; u < CH; ++u) {
+        forget(v[u]);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[u][e] = (T)(gp * ex2(fmaf((float)v[u][e], f, -f0) * f2));
-            store(at + u * kStep, v[u]);
-        }
+        for (int e = 0; e < 8; ++e) v[u][e] = (T)grad((float)v[u][e]);
+        store(u * kStep, v[u]);
     }
+    if constexpr (REST)
+        for (uint32_t at = rest; at < size; at += U * kStep) {
+            T w[U][8];
+#pragma unroll
+            for (int u = 0; u < U; ++u) load(at + u * kStep, w[u]);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[u][e] = (T)grad((float)w[u][e]);
+                store(at + u * kStep, w[u]);
+            }
+        }
     // the classes that the teacher names, over what was written: once the stores
     // in front of the barrier are through
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -209,35 +296,62 @@ __global__ __launch_bounds__(NT) void distill_kernel(const DistillArgs a, int se
     for (int k = tid; k < a.k; k += NT) {
         const int id = ids[k];
         if (id < lo || id >= hi) continue;
+        const float xc = (float)x[id];
         float t = 0.f;
         bool again = false;  // an earlier entry of this class does it
-        for (int o = 0; o < a.k; ++o)
-            if (ids[o] == id) {
-                again |= o < k;
-                t += tau[o];
-            }
-        if (again) continue;
-        gx[id] = (T)fmaf(gp, ex2(fmaf((float)x[id], f, -f0) * f2), -gt * t);
+        for (int o = 0; o < a.k; o += 4) {
+            typedef __attribute__((ext_vector_type(4))) int i32x4;
+            const i32x4 other = *(const i32x4*)(ids + o);
+            const f32x4 w = *(const f32x4*)(tau + o);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (other[e] == id) {
+                    again |= o + e < k;
+                    t += w[e];
+                }
+        }
+        if (!again) gx[id] = (T)(grad(xc) - gt * t);
     }
 }
 
-template <int OP, int NT, bool WIDE, int MODE>
+template <int OP, int NT, int CH, bool REST, bool WIDE, int MODE>
 hipError_t go(const DistillArgs& a, int sections, hipStream_t s) {
-    distill_kernel<OP, NT, WIDE, MODE>
+    distill_kernel<OP, NT, CH, REST, WIDE, MODE>
         <<<flat_grid((int64_t)a.rows * sections), NT, 0, s>>>(a, sections);
     return hipGetLastError();
 }
-template <int OP, int NT, bool WIDE>
+
+// The smallest shape that keeps `cols` columns in registers, or part of them.
+template <int OP, bool WIDE, int MODE>
+hipError_t held(const DistillArgs& a, int cols, int sections, hipStream_t s) {
+    if constexpr (MODE == BACK) return go<OP, 256, 0, true, WIDE, MODE>(a, sections, s);
+    if (cols <= 2048) return go<OP, 256, 1, false, WIDE, MODE>(a, sections, s);
+    if (cols <= 4096) return go<OP, 256, 2, false, WIDE, MODE>(a, sections, s);
+    if (cols <= 8192) return go<OP, 256, 4, false, WIDE, MODE>(a, sections, s);
+    if constexpr (MODE == WHOLE) {
+        if (cols <= 16384) return go<OP, 512, 4, false, WIDE, MODE>(a, sections, s);
+        if (cols <= 32768) return go<OP, 1024, 4, false, WIDE, MODE>(a, sections, s);
+        // (single elements of 16 bits come in registers of their own first)
+        if constexpr (OP == OP_F32 || !WIDE)
+            return go<OP, 1024, 4, true, WIDE, MODE>(a, sections, s);
+        else if (cols <= 65536)
+            return go<OP, 1024, 8, false, WIDE, MODE>(a, sections, s);
+        else
+            return go<OP, 1024, 8, true, WIDE, MODE>(a, sections, s);
+    }
+    return go<OP, 256, 4, true, WIDE, MODE>(a, sections, s);
+}
+template <int OP, bool WIDE>
 hipError_t launch(const DistillArgs& a, hipStream_t s) {
-    if (!a.loss) return go<OP, NT, WIDE, BACK>(a, a.split, s);
-    if (a.split == 1) return go<OP, NT, WIDE, WHOLE>(a, 1, s);
-    const hipError_t e = go<OP, NT, WIDE, PARTS>(a, a.split, s);
+    if (!a.loss) return held<OP, WIDE, BACK>(a, a.split_cols, a.split, s);
+    if (a.split == 1) return held<OP, WIDE, WHOLE>(a, a.classes, 1, s);
+    const hipError_t e = held<OP, WIDE, PARTS>(a, a.split_cols, a.split, s);
     if (e != hipSuccess) return e;
-    return go<OP, NT, WIDE, JOIN>(a, a.gx ? a.split : 1, s);
+    return held<OP, WIDE, JOIN>(a, a.split_cols, a.gx ? a.split : 1, s);
 }
 template <int OP>
 hipError_t launch(const DistillArgs& a, hipStream_t s) {
-    return a.wide ? launch<OP, 256, true>(a, s) : launch<OP, 256, false>(a, s);
+    return a.wide ? launch<OP, true>(a, s) : launch<OP, false>(a, s);
 }
 
 }  // namespace

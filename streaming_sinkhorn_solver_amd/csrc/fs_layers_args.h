@@ -100,9 +100,10 @@ struct BalanceArgs {
     const float* gloss;
     const float* ggates;
     int blocks;        // workgroups of a batch entry
-    float* part_p;     // [B][blocks][E] sums of p
-    int* part_c;       // [B][blocks][E] counts
+    float2* part;      // [B][blocks][E] sum of p, count (as bits)
     float2* part_s;    // [B][blocks] sum of lse^2, rows that take part
+    double* terms;     // [B][ceil(E / 16)] the columns' terms of the loss
+    int* arrived;      // [B] workgroups whose term is there
 };
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s);
 hipError_t launch_balance_bwd(const BalanceArgs& a, hipStream_t s);

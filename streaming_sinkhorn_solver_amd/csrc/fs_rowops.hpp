@@ -71,7 +71,7 @@ struct RowFold {
         if constexpr (LPR > 64) {
             float2* at = buf + turn * kWaves;
             if ((threadIdx.x & 63) == 0) at[threadIdx.x >> 6] = make_float2(a, b);
-            __syncthreads();
+            stage_barrier();  // (the rows' loads that are under way are not waited for)
             a = b = 0.f;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) a += at[w].x, b += at[w].y;
@@ -85,7 +85,7 @@ struct RowFold {
         if constexpr (LPR > 64) {
             float2* at = buf + turn * kWaves;
             if ((threadIdx.x & 63) == 0) at[threadIdx.x >> 6].x = a;
-            __syncthreads();
+            stage_barrier();  // (the rows' loads that are under way are not waited for)
             a = 0.f;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) a += at[w].x;
@@ -99,7 +99,7 @@ struct RowFold {
         if constexpr (LPR > 64) {
             float2* at = buf + turn * kWaves;
             if ((threadIdx.x & 63) == 0) at[threadIdx.x >> 6].x = __uint_as_float(a);
-            __syncthreads();
+            stage_barrier();  // (the rows' loads that are under way are not waited for)
             a = 0;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) a = max(a, __float_as_uint(at[w].x));
@@ -153,6 +153,45 @@ struct Share {
                     if (at < width) row[at] = v[j][e];
                 }
             }
+        }
+    }
+};
+
+// A range of memory behind a buffer descriptor: reads behind its end give zeros,
+// writes there are dropped, without a branch.  The range's start and size are one
+// for all lanes, at most 2^31 bytes; an access is in it or behind it as a whole.
+struct RowBuffer {
+    __amdgpu_buffer_rsrc_t r;
+    __device__ __forceinline__ RowBuffer(const void* p, uint32_t bytes)
+        : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000)) {}
+    __device__ __forceinline__ u32x4 read16(uint32_t at) const {
+        return __builtin_amdgcn_raw_buffer_load_b128(r, (int)at, 0, 0);
+    }
+    __device__ __forceinline__ void write16(uint32_t at, u32x4 v) const {
+        __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)at, 0, 0);
+    }
+    template <typename T>
+    __device__ __forceinline__ T read(uint32_t at) const {
+        T v;
+        if constexpr (sizeof(T) == 4) {
+            const uint32_t w = __builtin_amdgcn_raw_buffer_load_b32(r, (int)at, 0, 0);
+            __builtin_memcpy(&v, &w, 4);
+        } else {
+            const uint16_t w = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)at, 0, 0);
+            __builtin_memcpy(&v, &w, 2);
+        }
+        return v;
+    }
+    template <typename T>
+    __device__ __forceinline__ void write(uint32_t at, T v) const {
+        if constexpr (sizeof(T) == 4) {
+            uint32_t w;
+            __builtin_memcpy(&w, &v, 4);
+            __builtin_amdgcn_raw_buffer_store_b32(w, r, (int)at, 0, 0);
+        } else {
+            uint16_t w;
+            __builtin_memcpy(&w, &v, 2);
+            __builtin_amdgcn_raw_buffer_store_b16(w, r, (int)at, 0, 0);
         }
     }
 };
