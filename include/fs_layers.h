@@ -90,8 +90,9 @@ fs_status fs_quantize_rows(int32_t dtype, int32_t rows, int32_t width, const voi
  * exact; it and the two products with the scales are rounded to fp32, y to its
  * type.  q_x: [m][k] and q_w: [n][k] int8 (any value, -128 too), y: [m][n] of
  * dtype; strides of rows in elements.  bias: device fp32 [n] or NULL.  0 <= m, n
- * <= 2^24, m n <= 2^36, 0 <= k <= 65536 (k = 0: the sum is 0).  Rows that are
- * 16-byte aligned with a k of whole 16 bytes go straight to LDS. */
+ * <= 2^24, m n <= 2^36, 0 <= k <= 65536 (k = 0: the sum is 0).  With more than 32
+ * rows an operand whose rows are not 16-byte aligned, or whose k is no multiple of
+ * 16, is laid out in the workspace by each call: keep weights aligned. */
 typedef struct {
     int32_t dtype; /* fs_dtype of y */
     int32_t m, n, k;
@@ -106,9 +107,9 @@ typedef struct {
     int64_t y_stride;
 } fs_quantized_product_desc;
 
-/* Bytes of workspace (from m, n, k alone); at least 256, or 0 if they are out of
- * range.  Pure host function. */
-size_t fs_quantized_product_workspace_bytes(int32_t m, int32_t n, int32_t k);
+/* Bytes of workspace (from the sizes, the strides and the operands' alignment); at
+ * least 256, or 0 if the sizes are out of range.  Pure host function. */
+size_t fs_quantized_product_workspace_bytes(const fs_quantized_product_desc* desc);
 
 fs_status fs_quantized_product(const fs_quantized_product_desc* desc, void* workspace,
                                size_t workspace_bytes, void* stream);

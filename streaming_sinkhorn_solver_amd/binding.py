@@ -275,7 +275,7 @@ def load():
             ("fs_layer_norm_backward", i32, [layer, Rows, _fp, _fp, _fp, Rows, Rows, Rows, _fp, _fp,
                                              _vp, sz, _vp]),
             ("fs_quantize_rows", i32, [i32, i32, i32, _vp, i64, _vp, i64, _fp, _vp]),
-            ("fs_quantized_product_workspace_bytes", sz, [i32, i32, i32]),
+            ("fs_quantized_product_workspace_bytes", sz, [product]),
             ("fs_quantized_product", i32, [product, _vp, sz, _vp]),
             ("fs_distill_workspace_bytes", sz, [distill]),
             ("fs_distill_loss", i32, [distill, Rows, _fp, _fp, _fp, Rows, _vp, sz, _vp]),
@@ -1210,10 +1210,12 @@ def fs_quantize_rows(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, *, s
 
 
 def fs_quantized_product_workspace_bytes(m: int, n: int, k: int) -> int:
-    """Bytes of workspace of fs_quantized_product of [m, k] by [n, k]."""
+    """Bytes of workspace of fs_quantized_product of contiguous, 16-byte aligned [m, k]
+    by [n, k]."""
     _i32("a size", m, n, k)
+    a = QuantizedProductDesc(0, m, n, k, None, k, None, None, k)
     return _needed(load().fs_quantized_product_workspace_bytes,
-                   "fs_quantized_product_workspace_bytes", m, n, k)
+                   "fs_quantized_product_workspace_bytes", ctypes.byref(a))
 
 
 def fs_quantized_product(q_x: torch.Tensor, scale_x: torch.Tensor, q_w: torch.Tensor,
@@ -1237,11 +1239,10 @@ def fs_quantized_product(q_x: torch.Tensor, scale_x: torch.Tensor, q_w: torch.Te
                              _flat(_need(scale_x, "scale_x"), "scale_x", dev, f32, (m,)), wp, ws_,
                              _flat(_need(scale_w, "scale_w"), "scale_w", dev, f32, (n,)),
                              _flat(bias, "bias", dev, f32, (n,)), Y.data, Y.stride_row)
+    pa = ctypes.byref(a)
     ws, size, _keep = _work(workspace, lambda: _needed(lib.fs_quantized_product_workspace_bytes,
-                                                       "fs_quantized_product", m, n, k), y, dev,
-                            stream)
-    return _call(lib.fs_quantized_product, "fs_quantized_product", dev, stream, ctypes.byref(a), ws,
-                 size)
+                                                       "fs_quantized_product", pa), y, dev, stream)
+    return _call(lib.fs_quantized_product, "fs_quantized_product", dev, stream, pa, ws, size)
 
 
 def _distill_desc(logits, ids, teacher, temperature, teacher_lse, active):

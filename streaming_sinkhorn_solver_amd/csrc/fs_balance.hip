@@ -104,20 +104,26 @@ __device__ __forceinline__ void sort8(Key (&k)[8]) {
     order(1, 2), order(3, 4), order(5, 6);
 }
 
+// A lane's columns e0 .. e0 + EPL - 1 of a row; -inf behind the last and in rows
+// that take no part.  A lane without a column reads the row's first and leaves it.
 template <typename T, int EPL, bool WIDE>
 __device__ __forceinline__ void load_columns(const T* row, int e0, int E, bool on, T (&v)[EPL]) {
     if constexpr (WIDE) {
 #pragma unroll
         for (int j = 0; j < EPL; j += 8) {
-            if (on && e0 + j < E)
-                __builtin_memcpy(v + j, __builtin_assume_aligned(row + e0 + j, 16), 8 * sizeof(T));
-            else
+            const bool in = on && e0 + j < E;
+            T t[8];
+            __builtin_memcpy(t, __builtin_assume_aligned(row + (in ? e0 + j : 0), 16), sizeof(t));
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[j + e] = (T)-INFINITY;
+            for (int e = 0; e < 8; ++e) v[j + e] = in ? t[e] : (T)-INFINITY;
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) v[j] = on && e0 + j < E ? row[e0 + j] : (T)-INFINITY;
+        for (int j = 0; j < EPL; ++j) {
+            const bool in = on && e0 + j < E;
+            const T t = row[in ? e0 + j : 0];
+            v[j] = in ? t : (T)-INFINITY;
+        }
     }
 }
 

@@ -48,6 +48,8 @@ struct Running {
     }
 };
 
+__host__ __device__ constexpr int padded(int k) { return (k + 3) / 4 * 4; }
+
 template <int NT>
 __device__ __forceinline__ float block_max(float x, float* buf) {
     x = lanes_max<64>(x);
@@ -92,8 +94,8 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void distill_kernel(const D
     using T = typename El<OP>::T;
     constexpr int U = 2, kStep = 8 * NT;
     __shared__ float buf[2][NT / 64];
-    __shared__ __align__(16) int ids[kDistillMaxTop + 4];
-    __shared__ __align__(16) float tau[kDistillMaxTop + 4];
+    extern __shared__ __align__(16) int ids[];  // ids and tau of whole groups of four
+    float* const tau = (float*)(ids + padded(a.k));
     __shared__ float mass[2];
     const int64_t block = flat_block();
     const int64_t row = block / sections;
@@ -170,7 +172,7 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void distill_kernel(const D
             tau[k] = t;
             top = fmaxf(top, t);
         }
-        if (tid < 4) ids[a.k + tid] = -1, tau[a.k + tid] = 0.f;  // whole groups of four
+        if (a.k + tid < padded(a.k)) ids[a.k + tid] = -1, tau[a.k + tid] = 0.f;
         if (a.teacher_lse) {
             ref = on ? a.teacher_lse[row] : 0.f;  // the log of the weights' divisor
         } else {
@@ -317,7 +319,7 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void distill_kernel(const D
 template <int OP, int NT, int CH, bool REST, bool WIDE, int MODE>
 hipError_t go(const DistillArgs& a, int sections, hipStream_t s) {
     distill_kernel<OP, NT, CH, REST, WIDE, MODE>
-        <<<flat_grid((int64_t)a.rows * sections), NT, 0, s>>>(a, sections);
+        <<<flat_grid((int64_t)a.rows * sections), NT, 8 * padded(a.k), s>>>(a, sections);
     return hipGetLastError();
 }
 
@@ -325,8 +327,9 @@ hipError_t go(const DistillArgs& a, int sections, hipStream_t s) {
 template <int OP, bool WIDE, int MODE>
 hipError_t held(const DistillArgs& a, int cols, int sections, hipStream_t s) {
     if constexpr (MODE == BACK) return go<OP, 256, 0, true, WIDE, MODE>(a, sections, s);
-    if (cols <= 2048) return go<OP, 256, 1, false, WIDE, MODE>(a, sections, s);
-    if (cols <= 4096) return go<OP, 256, 2, false, WIDE, MODE>(a, sections, s);
+    if (cols <= 512) return go<OP, 64, 1, false, WIDE, MODE>(a, sections, s);
+    if (cols <= 2048) return go<OP, 64, 4, false, WIDE, MODE>(a, sections, s);
+    if (cols <= 4096) return go<OP, 128, 4, false, WIDE, MODE>(a, sections, s);
     if (cols <= 8192) return go<OP, 256, 4, false, WIDE, MODE>(a, sections, s);
     if constexpr (MODE == WHOLE) {
         if (cols <= 16384) return go<OP, 512, 4, false, WIDE, MODE>(a, sections, s);
@@ -356,9 +359,20 @@ hipError_t launch(const DistillArgs& a, hipStream_t s) {
 
 }  // namespace
 
-int distill_split(int rows, int classes, int* split_cols) {
-    int64_t s = rows > 0 ? (1024 + rows - 1) / rows : 1;
-    s = std::max<int64_t>(1, std::min<int64_t>({s, (int64_t)kDistillMaxSplit, classes / 4096}));
+// The loss: one workgroup a row, but where rows are long and few, whose ranges' parts
+// a second launch joins (us, bf16, loss and gradient, one workgroup a row / ranges):
+//   rows              1           32          64          128         256
+//   32000 classes     7.6 / 8.2   8.2 / 9.1   8.5 / 10.2  9.1 / 12.7  10.7 / 14.2
+//   65536 classes    10.8 / 8.0  11.7 / 9.2  12.3 / 11.1 14.2 / 14.5  17.6 / 21.2
+//   131072 classes   18.2 / 8.0  19.7 / 10.9 20.9 / 14.5 23.0 / 21.0  32.9 / 37.8
+// (fp32: 32000 classes 8.2 / 8.5, 9.0 / 9.6, 9.9 / 11.3; 131072 classes 23.0 / 8.1,
+// 25.5 / 14.4, 28.3 / 21.2, 34.0 / 36.3, 59.3 / 65.7.)  The gradient alone needs
+// nothing of the rest of its row: ranges for 1024 workgroups.
+int distill_split(int rows, int classes, bool backward, int* split_cols) {
+    int64_t s = 1;
+    if (rows > 0 && (backward || (classes > 32768 && rows < 128)))
+        s = std::min<int64_t>((1024 + rows - 1) / rows, classes / 4096);
+    s = std::max<int64_t>(1, std::min<int64_t>(s, kDistillMaxSplit));
     *split_cols = (int)(((classes + s - 1) / s + 7) / 8 * 8);
     return (classes + *split_cols - 1) / *split_cols;
 }

@@ -207,22 +207,25 @@ __global__ __launch_bounds__(threads_of<LPR>()) void layer_norm_bwd_kernel(const
     }
 }
 
-// dw and db: the workgroups' parts in 64 bits and a fixed order; 64 columns a
-// workgroup, 16 lanes a column.
+// dw and db: the workgroups' parts in 64 bits and a fixed order; 32 columns a
+// workgroup, 32 lanes a column.
 __global__ __launch_bounds__(1024) void layer_norm_sum_kernel(const LayerNormArgs a, int blocks) {
-    __shared__ double red[16][64];
-    const int c = threadIdx.x & 63, y = threadIdx.x >> 6;
-    const int64_t x = (int64_t)blockIdx.x * 64 + c;  // of 2 width
+    __shared__ double red[32][33];
+    const int c = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int64_t x = (int64_t)blockIdx.x * 32 + c;  // of 2 width
     double s = 0.0;
     if (x < 2 * a.width) {
-#pragma unroll 4
-        for (int k = y; k < blocks; k += 16) s += (double)a.part[(int64_t)k * 2 * a.width + x];
+#pragma unroll 8
+        for (int k = y; k < blocks; k += 32) s += (double)a.part[(int64_t)k * 2 * a.width + x];
     }
     red[y][c] = s;
     __syncthreads();
+    for (int o = 16; o >= 1; o >>= 1) {
+        if (y < o) red[y][c] += red[y + o][c];
+        __syncthreads();
+    }
     if (y || x >= 2 * a.width) return;
-#pragma unroll
-    for (int k = 1; k < 16; ++k) s += red[k][c];
+    s = red[0][c];
     if (x < a.width) {
         if (a.gw) a.gw[x] = (float)s;
     } else if (a.gb) {
@@ -277,7 +280,7 @@ hipError_t launch_layer_norm_bwd(const LayerNormArgs& a, hipStream_t s) {
     const bool any = (int64_t)a.B * a.n > 0;  // else the weights' sums are empty
     const hipError_t e = any ? launch(a, true, s) : hipSuccess;
     if (e != hipSuccess || !a.part) return e;
-    layer_norm_sum_kernel<<<(unsigned)((2 * a.width + 63) / 64), 1024, 0, s>>>(a, any ? a.blocks : 0);
+    layer_norm_sum_kernel<<<(unsigned)((2 * a.width + 31) / 32), 1024, 0, s>>>(a, any ? a.blocks : 0);
     return hipGetLastError();
 }
 

@@ -199,9 +199,30 @@ bool product_sizes(int32_t m, int32_t n, int32_t k) {
     return m >= 0 && n >= 0 && k >= 0 && m <= kProductMaxRows && n <= kProductMaxRows &&
            (int64_t)m * n <= (int64_t)1 << 36 && k <= kQuantMaxWidth;
 }
-size_t product_workspace(int32_t m, int32_t n, int32_t k, int* split, int* split_k) {
-    *split = product_split(m, n, k, split_k);
-    return *split > 1 ? up((size_t)*split * m * n * 4) : kAlign;
+// (offsets within a tile of 256 rows stay 32-bit numbers)
+bool ready_for_tiles(const int8_t* q, int64_t rows, int64_t stride, int32_t k) {
+    return k % 16 == 0 && aligned16(q) && (rows <= 1 || (stride % 16 == 0 && stride <= 1 << 22));
+}
+struct ProductLayout {
+    int split = 1, split_k = 1;
+    bool pack_x = false, pack_w = false;
+    size_t x = 0, w = 0, total = kAlign;
+};
+ProductLayout product_layout(const fs_quantized_product_desc& d) {
+    ProductLayout l;
+    l.split = product_split(d.m, d.n, d.k, &l.split_k);
+    size_t at = l.split > 1 ? up((size_t)l.split * d.m * d.n * 4) : 0;
+    if (!product_few(d.m) && d.k > 0) {
+        const size_t row = (size_t)cdiv(d.k, 16) * 16;
+        l.pack_x = !ready_for_tiles(d.q_x, d.m, d.q_x_stride, d.k);
+        l.pack_w = !ready_for_tiles(d.q_w, d.n, d.q_w_stride, d.k);
+        l.x = at;
+        if (l.pack_x) at += up(row * d.m);
+        l.w = at;
+        if (l.pack_w) at += up(row * d.n);
+    }
+    l.total = std::max(at, kAlign);
+    return l;
 }
 
 }  // namespace
@@ -239,13 +260,12 @@ fs_status fs_quantize_rows(int32_t dtype, int32_t rows, int32_t width, const voi
     return hip_status(launch_quantize(a, (hipStream_t)stream), "fs_quantize_rows");
 }
 
-size_t fs_quantized_product_workspace_bytes(int32_t m, int32_t n, int32_t k) {
-    if (!product_sizes(m, n, k)) {
-        (void)fail(FS_ERR_INVALID_ARG, "m, n or k is out of range (got %d, %d, %d)", m, n, k);
+size_t fs_quantized_product_workspace_bytes(const fs_quantized_product_desc* desc) {
+    if (!desc || !product_sizes(desc->m, desc->n, desc->k)) {
+        (void)fail(FS_ERR_INVALID_ARG, "desc is NULL or m, n or k out of range");
         return 0;
     }
-    int split, split_k;
-    return product_workspace(m, n, k, &split, &split_k);
+    return product_layout(*desc).total;
 }
 
 fs_status fs_quantized_product(const fs_quantized_product_desc* desc, void* workspace,
@@ -267,7 +287,8 @@ fs_status fs_quantized_product(const fs_quantized_product_desc* desc, void* work
     if (d.bias) FS_TRY(take_flat("bias", d.bias, n, 4, in[4]));
     FS_TRY(take_matrix("y", d.y, m, d.y_stride, n, elem_size(d.dtype), true, out));
     ProductArgs a{};
-    const size_t need = product_workspace(d.m, d.n, d.k, &a.split, &a.split_k);
+    const ProductLayout l = product_layout(d);
+    const size_t need = l.total;
     FS_TRY(check_workspace(workspace, workspace_bytes, need));
     in[5] = flat(workspace, need);
     FS_TRY(check_apart("y", out, in, 6));
@@ -286,11 +307,13 @@ fs_status fs_quantized_product(const fs_quantized_product_desc* desc, void* work
     a.bias = d.bias;
     a.y = (char*)d.y;
     a.sy = m > 1 ? d.y_stride : 0;
-    // (offsets within a tile of 256 rows stay 32-bit numbers)
-    constexpr int64_t kStride = 1 << 22;
-    a.aligned = d.k % 16 == 0 && aligned16(d.q_x) && aligned16(d.q_w) && a.sx % 16 == 0 &&
-                a.sw % 16 == 0 && a.sx <= kStride && a.sw <= kStride;
+    a.y_wide = n % 8 == 0 && aligned16(d.y) && a.sy * elem_size(d.dtype) % 16 == 0;
+    a.dwords = ((uintptr_t)d.q_x | (uintptr_t)d.q_w | (uintptr_t)a.sx | (uintptr_t)a.sw) % 4 == 0;
+    a.split = l.split;
+    a.split_k = l.split_k;
     a.part = (int*)workspace;
+    a.pack_x = l.pack_x ? (int8_t*)workspace + l.x : nullptr;
+    a.pack_w = l.pack_w ? (int8_t*)workspace + l.w : nullptr;
     return hip_status(launch_product(a, (hipStream_t)stream), "fs_quantized_product");
 }
 
@@ -300,7 +323,7 @@ namespace {
 
 // ---- distillation --------------------------------------------------------------
 
-fs_status take_distill(const fs_distill_desc* p, DistillArgs& a) {
+fs_status take_distill(const fs_distill_desc* p, bool backward, DistillArgs& a) {
     if (!p) return fail(FS_ERR_INVALID_ARG, "desc must be non-NULL");
     const fs_distill_desc& d = *p;
     FS_TRY(check_dtype(d.dtype));
@@ -320,7 +343,7 @@ fs_status take_distill(const fs_distill_desc* p, DistillArgs& a) {
     a.teacher = d.teacher;
     a.teacher_lse = d.teacher_lse;
     a.active = d.active;
-    a.split = distill_split(d.rows, d.classes, &a.split_cols);
+    a.split = distill_split(d.rows, d.classes, backward, &a.split_cols);
     return FS_OK;
 }
 
@@ -350,7 +373,7 @@ extern "C" {
 
 size_t fs_distill_workspace_bytes(const fs_distill_desc* desc) {
     DistillArgs a{};
-    if (take_distill(desc, a) != FS_OK) return 0;
+    if (take_distill(desc, false, a) != FS_OK) return 0;
     return distill_workspace(a);
 }
 
@@ -358,7 +381,7 @@ fs_status fs_distill_loss(const fs_distill_desc* desc, fs_rows logits, float* lo
                           const float* d_loss, fs_rows d_logits, void* workspace,
                           size_t workspace_bytes, void* stream) {
     DistillArgs a{};
-    FS_TRY(take_distill(desc, a));
+    FS_TRY(take_distill(desc, false, a));
     Extent in[7], out[3];
     bool vec = false;
     FS_TRY(distill_inputs(*desc, logits, a, vec, in));
@@ -394,7 +417,7 @@ fs_status fs_distill_loss(const fs_distill_desc* desc, fs_rows logits, float* lo
 fs_status fs_distill_loss_backward(const fs_distill_desc* desc, fs_rows logits, const float* lse,
                                    const float* d_loss, fs_rows d_logits, void* stream) {
     DistillArgs a{};
-    FS_TRY(take_distill(desc, a));
+    FS_TRY(take_distill(desc, true, a));
     Extent in[7], out;
     bool vec = false;
     FS_TRY(distill_inputs(*desc, logits, a, vec, in));

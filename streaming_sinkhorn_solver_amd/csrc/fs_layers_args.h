@@ -49,7 +49,7 @@ hipError_t launch_quantize(const QuantArgs& a, hipStream_t s);
 
 struct ProductArgs {
     int op, m, n, k;
-    int aligned;  // both operands' rows 16-byte aligned and k whole 16-byte chunks
+    int dwords;  // both operands' rows start at whole dwords
     const int8_t* x;
     int64_t sx;
     const float* scale_x;
@@ -59,12 +59,18 @@ struct ProductArgs {
     const float* bias;
     char* y;
     int64_t sy;
-    int y_vec;            // rows of y 16-byte aligned (their width is any)
-    int split, split_k;   // ranges of k, each of split_k
-    int* part;            // [split][m][n]
+    int y_wide;          // rows of y 16-byte aligned, n whole groups of eight
+    int split, split_k;  // ranges of k, each of split_k
+    int* part;           // [split][m][n]
+    // [rows][k rounded up to 16]: where an operand whose rows are not whole, aligned
+    // 16-byte chunks is laid out first; NULL for one that is, and for few rows
+    int8_t* pack_x;
+    int8_t* pack_w;
 };
 hipError_t launch_product(const ProductArgs& a, hipStream_t s);
-// Ranges of k of a product of this size (1: no workspace).
+// Few rows: no ranges, nothing laid out.
+bool product_few(int m);
+// Ranges of k of a product of this size (1: no parts).
 int product_split(int m, int n, int k, int* split_k);
 
 struct DistillArgs {
@@ -86,7 +92,7 @@ struct DistillArgs {
 };
 hipError_t launch_distill(const DistillArgs& a, hipStream_t s);
 // Ranges of a row's classes that a call on `rows` rows works on apart.
-int distill_split(int rows, int classes, int* split_cols);
+int distill_split(int rows, int classes, bool backward, int* split_cols);
 
 struct BalanceArgs {
     int op, B, n, E, k, normalize, wide;

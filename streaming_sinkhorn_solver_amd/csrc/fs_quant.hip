@@ -105,75 +105,167 @@ hipError_t quantize(const QuantArgs& a, hipStream_t s) {
 
 // ---- product ----------------------------------------------------------------
 
-// Sixteen bytes of a row from k on; zeros from k = end on.
-__device__ __forceinline__ i32x4 load_chunk(const int8_t* row, int k, int end) {
-    i32x4 v = {0, 0, 0, 0};
-    if (k + 16 <= end) {
-        __builtin_memcpy(&v, row + k, 16);
-    } else {
-        int8_t t[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) t[i] = k + i < end ? row[k + i] : (int8_t)0;
-        __builtin_memcpy(&v, t, 16);
-    }
-    return v;
-}
-
 template <int OP>
 __device__ __forceinline__ void put(const ProductArgs& a, int i, int j, int sum, float sw, float bias) {
     using T = typename El<OP>::T;
     ((T*)a.y)[i * a.sy + j] = (T)fmaf((float)sum * a.scale_x[i], sw, bias);
 }
 
-// Few rows: a workgroup takes 16 columns and all rows (RB blocks of 16), its
-// waves divide k.  Bound by the read of the columns' bytes.
-template <int OP, int RB>
-__global__ __launch_bounds__(256) void product_rows_kernel(const ProductArgs a) {
-    __shared__ int red[4][RB * 256];
+// Sixteen bytes of a row from k on.  Rows that start at a whole dword (DWORDS) are
+// read as they stand; else five dwords are read from the one on that holds the
+// first byte, and shifted (16-byte loads of any address take four times as long).
+// A dword that is read holds a byte of the row.
+template <bool DWORDS>
+struct Bytes {
+    const int8_t* p;
+    uint32_t shift;  // bytes, 0..3
+    __device__ __forceinline__ Bytes(const int8_t* row) : p(row), shift(0) {
+        if constexpr (!DWORDS) {
+            shift = (uint32_t)(uintptr_t)row & 3;
+            p = row - shift;
+        }
+    }
+    struct Raw {
+        uint32_t w[DWORDS ? 4 : 5];
+    };
+    __device__ __forceinline__ void read(int k, Raw& r) const {
+        __builtin_memcpy(r.w, __builtin_assume_aligned(p + k, 4), 16);
+        if constexpr (!DWORDS)
+            __builtin_memcpy(r.w + 4, __builtin_assume_aligned(p + k + (shift ? 16 : 12), 4), 4);
+    }
+    __device__ __forceinline__ i32x4 value(const Raw& r) const {
+        i32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = DWORDS ? (int)r.w[i] : (int)__builtin_amdgcn_alignbyte(r.w[i + 1], r.w[i], shift);
+        return v;
+    }
+    // from k on, zeros from `end` on
+    __device__ __forceinline__ i32x4 tail(int k, int end) const {
+        int8_t t[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) t[i] = k + i < end ? p[shift + k + i] : (int8_t)0;
+        i32x4 v;
+        __builtin_memcpy(&v, t, 16);
+        return v;
+    }
+};
+
+// Few rows: a workgroup takes 16 CB columns and all rows (RB blocks of 16), its
+// eight waves divide k.  Bound by the read of the columns' bytes.
+constexpr int kRowWaves = 8;
+template <int OP, int RB, int CB, bool DWORDS>
+__global__ __launch_bounds__(64 * kRowWaves) void product_rows_kernel(const ProductArgs a) {
+    constexpr int N = RB * CB * 256;
+    __shared__ int red[kRowWaves][N];
     const int lane = threadIdx.x & 63, wave = wave_id(), r = lane & 15, c = lane >> 4;
-    const int j0 = blockIdx.x * 16;
-    const int8_t* w = a.w + (int64_t)min(j0 + r, a.n - 1) * a.sw;
-    const int8_t* x[RB];
+    const int j0 = blockIdx.x * 16 * CB;
+    using Row = Bytes<DWORDS>;
+    const auto column = [&](int b) { return Row(a.w + (int64_t)min(j0 + 16 * b + r, a.n - 1) * a.sw); };
+    const auto state = [&](int b) { return Row(a.x + (int64_t)min(16 * b + r, a.m - 1) * a.sx); };
+    i32x4 acc[CB][RB] = {};
+    // whole steps of 64 k: reads that ask nothing, U of them under way together
+    constexpr int U = RB * CB == 1 ? 8 : RB * CB == 2 ? 4 : 2;
+    const int whole = a.k / 64;
+    int t = wave;
+    for (; t + kRowWaves * (U - 1) < whole; t += kRowWaves * U) {
+        typename Row::Raw wv[U][CB], xv[U][RB];
 #pragma unroll
-    for (int b = 0; b < RB; ++b) x[b] = a.x + (int64_t)min(16 * b + r, a.m - 1) * a.sx;
-    i32x4 acc[RB] = {};
-    const int steps = (a.k + 63) / 64;
-    for (int t = wave; t < steps; t += 4) {
+        for (int u = 0; u < U; ++u) {
+            const int k = (t + kRowWaves * u) * 64 + c * 16;
+#pragma unroll
+            for (int b = 0; b < CB; ++b) column(b).read(k, wv[u][b]);
+#pragma unroll
+            for (int b = 0; b < RB; ++b) state(b).read(k, xv[u][b]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int q = 0; q < CB; ++q)
+#pragma unroll
+                for (int b = 0; b < RB; ++b)
+                    acc[q][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                        state(b).value(xv[u][b]), column(q).value(wv[u][q]), acc[q][b], 0, 0, 0);
+    }
+    for (; t < (a.k + 63) / 64; t += kRowWaves) {
         const int k = t * 64 + c * 16;
-        const i32x4 wv = load_chunk(w, k, a.k);
+        i32x4 wv[CB], xv[RB];
+        if (t < whole) {
+            typename Row::Raw raw;
 #pragma unroll
-        for (int b = 0; b < RB; ++b)
-            acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(load_chunk(x[b], k, a.k), wv, acc[b], 0, 0, 0);
+            for (int b = 0; b < CB; ++b) column(b).read(k, raw), wv[b] = column(b).value(raw);
+#pragma unroll
+            for (int b = 0; b < RB; ++b) state(b).read(k, raw), xv[b] = state(b).value(raw);
+        } else {
+#pragma unroll
+            for (int b = 0; b < CB; ++b) wv[b] = column(b).tail(k, a.k);
+#pragma unroll
+            for (int b = 0; b < RB; ++b) xv[b] = state(b).tail(k, a.k);
+        }
+#pragma unroll
+        for (int q = 0; q < CB; ++q)
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+                acc[q][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xv[b], wv[q], acc[q][b], 0, 0, 0);
     }
     // a lane holds column r, rows 4 c .. 4 c + 3 of each block
 #pragma unroll
-    for (int b = 0; b < RB; ++b)
+    for (int q = 0; q < CB; ++q)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) red[wave][b * 256 + (4 * c + e) * 16 + r] = acc[b][e];
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                red[wave][((b * 16 + 4 * c + e) * CB + q) * 16 + r] = acc[q][b][e];
     __syncthreads();
-    for (int p = threadIdx.x; p < RB * 256; p += 256) {
-        const int i = p / 16, j = j0 + p % 16;
-        if (i < a.m && j < a.n)
-            put<OP>(a, i, j, red[0][p] + red[1][p] + red[2][p] + red[3][p], a.scale_w[j],
-                    a.bias ? a.bias[j] : 0.f);
+    for (int p = threadIdx.x; p < N; p += 64 * kRowWaves) {
+        const int i = p / (16 * CB), j = j0 + p % (16 * CB);
+        int sum = 0;
+#pragma unroll
+        for (int w = 0; w < kRowWaves; ++w) sum += red[w][p];
+        if (i < a.m && j < a.n) put<OP>(a, i, j, sum, a.scale_w[j], a.bias ? a.bias[j] : 0.f);
     }
 }
 
-// Tiles of BM x BN outputs over steps of 128 k, in two buffers of LDS: while the
-// matrix units work on one, the next step's rows come into the other.  The 16-byte
-// chunks of a row of 128 bytes stand in an order that depends on its number, so
-// that 16 lanes reading one chunk of 16 rows use all banks.  WM x WN waves.
+// Rows that the tiles cannot copy as they are, laid out with a stride of whole 16
+// bytes and zeros behind their end: a thread writes 16 bytes (blockIdx.z: x, w).
+__global__ __launch_bounds__(256) void product_pack_kernel(const ProductArgs a) {
+    const bool left = blockIdx.z == 0;
+    int8_t* to = left ? a.pack_x : a.pack_w;
+    if (!to) return;
+    const int chunks = (a.k + 15) / 16;
+    const int64_t at = flat_block() * 256 + threadIdx.x;
+    const int64_t row = at / chunks;
+    if (row >= (left ? a.m : a.n)) return;
+    const int c = (int)(at - row * chunks) * 16;
+    const Bytes<false> src(left ? a.x + row * a.sx : a.w + row * a.sw);
+    i32x4 v;
+    if (c + 16 <= a.k) {
+        Bytes<false>::Raw raw;
+        src.read(c, raw);
+        v = src.value(raw);
+    } else {
+        v = src.tail(c, a.k);
+    }
+    *(i32x4*)(to + at * 16) = v;
+}
+
+// Tiles of BM x BN outputs over steps of 128 k, in two or three buffers of LDS: while
+// the matrix units work on one, the next one or two steps' rows are on their way.
+// The 16-byte chunks of a row of 128 bytes stand in an order that depends on its
+// number, so that 16 lanes reading one chunk of 16 rows use all banks.  WM x WN
+// waves.
 template <int BM, int BN, int WM, int WN>
 struct Tile {
     static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
     static constexpr int MI = BM / WM / 32, NI = BN / WN / 32;
     static constexpr int kStage = (BM + BN) * 128;
+    static constexpr int kStages = 3 * kStage <= 80 * 1024 ? 3 : 2;  // two workgroups a CU
 };
 __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
     return row * 128 + ((chunk ^ (row >> 1)) & 7) * 16;
 }
 
-template <int OP, int BM, int BN, int WM, int WN, bool ALIGNED>
+template <int OP, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs a) {
     using L = Tile<BM, BN, WM, WN>;
     constexpr int MI = L::MI, NI = L::NI;
@@ -196,69 +288,48 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
     const int k0 = blockIdx.y * a.split_k, k1 = min(a.k, k0 + a.split_k);
     const int steps = (k1 - k0 + 127) / 128;
     constexpr int kCopies = (BM + BN) * 8 / L::kThreads;  // 16-byte chunks of a thread
-    // chunk c of a wave's copies covers 8 rows of the tiles, x's first
-    const auto source = [&](int c, int& row, int& chunk) -> const int8_t* {
-        const int t = (wave * kCopies + c) * 8 + (lane >> 3);
-        row = t;
-        chunk = (lane ^ (t >> 1)) & 7;
-        return t < BM ? a.x + (int64_t)min(i0 + t, a.m - 1) * a.sx
-                      : a.w + (int64_t)min(j0 + t - BM, a.n - 1) * a.sw;
-    };
+    // chunk c of a wave's copies covers 8 rows of the tiles, x's first; rows behind
+    // the last are the last one once more
     uint32_t voff[kCopies];
-    i32x4 held[kCopies];
-    if constexpr (ALIGNED) {
 #pragma unroll
-        for (int c = 0; c < kCopies; ++c) {
-            int row, chunk;
-            const int8_t* p = source(c, row, chunk);
-            const bool left = (wave * kCopies + c) * 8 < BM;
-            voff[c] = (uint32_t)(p - (left ? a.x + (int64_t)i0 * a.sx : a.w + (int64_t)j0 * a.sw)) + chunk * 16;
-        }
+    for (int c = 0; c < kCopies; ++c) {
+        const int t = (wave * kCopies + c) * 8 + (lane >> 3);
+        const uint32_t row = t < BM ? min(t, a.m - 1 - i0) : min(t - BM, a.n - 1 - j0);
+        voff[c] = row * (uint32_t)(t < BM ? a.sx : a.sw) + ((lane ^ (t >> 1)) & 7) * 16;
     }
-    const auto fetch = [&](int t) {
-        if constexpr (ALIGNED) {
-            const int k = k0 + t * 128;
+    // a quarter of a step's copies
+    const auto copy = [&](int t, int buffer, int quarter) {
+        const int k = k0 + t * 128;
 #pragma unroll
-            for (int c = 0; c < kCopies; ++c) {
-                const bool left = (wave * kCopies + c) * 8 < BM;
-                const int8_t* from = (left ? a.x + (int64_t)i0 * a.sx : a.w + (int64_t)j0 * a.sw) + k;
+        for (int c = quarter * (kCopies / 4); c < (quarter + 1) * (kCopies / 4); ++c) {
+            const bool left = (wave * kCopies + c) * 8 < BM;
+            const int8_t* from = (left ? a.x + (int64_t)i0 * a.sx : a.w + (int64_t)j0 * a.sw) + k;
+            uint32_t at = voff[c];
+            if (k + 128 > k1) {
                 // chunks behind the end: the row's first ones, which the products leave out
                 const uint32_t chunk = (lane ^ (((wave * kCopies + c) * 8 + (lane >> 3)) >> 1)) & 7;
-                const uint32_t back = k + (int)chunk * 16 < k1 ? 0 : chunk * 16;
-                dma_to_lds16((const char*)from, voff[c] - back,
-                             lds + (t & 1) * L::kStage + (wave * kCopies + c) * 1024);
+                at -= k + (int)chunk * 16 < k1 ? 0 : chunk * 16;
             }
-        } else {
-#pragma unroll
-            for (int c = 0; c < kCopies; ++c) {
-                int row, chunk;
-                const int8_t* p = source(c, row, chunk);
-                held[c] = load_chunk(p, k0 + t * 128 + chunk * 16, k1);
-            }
-        }
-    };
-    const auto keep = [&](int t) {
-        if constexpr (!ALIGNED) {
-#pragma unroll
-            for (int c = 0; c < kCopies; ++c)
-                lds_write<i32x4>(base + (t & 1) * L::kStage + (wave * kCopies + c) * 1024 + lane * 16,
-                                 held[c]);
+            dma_to_lds16((const char*)from, at,
+                         lds + buffer * L::kStage + (wave * kCopies + c) * 1024);
         }
     };
     const int wm = wave / WN, wn = wave % WN;
     const int ra = wm * MI * 32 + (lane & 31), rb = BM + wn * NI * 32 + (lane & 31);
     i32x16 acc[MI][NI] = {};
-    const auto work = [&](int t, bool tail) {
-        const uint32_t at = base + (t & 1) * L::kStage;
-        const int left = k1 - k0 - t * 128;
-        // operands of the next 32 k are read while this one's products run
+    constexpr int AHEAD = L::kStages - 1;
+    const auto work = [&](int t, int buffer, bool tail) {
+        const uint32_t at = base + buffer * L::kStage;
+        const int left = k1 - k0 - t * 128, next = buffer == 0 ? AHEAD : buffer - 1;
+        // operands of the next 32 k are read, and a quarter of a later step's rows
+        // sent for, while this one's products run
         i32x4 x[2][MI], w[2][NI];
         const auto read = [&](int kk) {
             const int chunk = 2 * kk + (lane >> 5);
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
                 x[kk & 1][i] = lds_read<i32x4>(at + chunk_at(ra + 32 * i, chunk));
-                if (ALIGNED && tail && chunk * 16 >= left) x[kk & 1][i] = i32x4{0, 0, 0, 0};
+                if (tail && chunk * 16 >= left) x[kk & 1][i] = i32x4{0, 0, 0, 0};
             }
 #pragma unroll
             for (int j = 0; j < NI; ++j)
@@ -268,6 +339,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
             if (kk < 3) read(kk + 1);
+            if (!tail && t + AHEAD < steps) copy(t + AHEAD, next, kk);
 #pragma unroll
             for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -277,43 +349,81 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    const int whole = ALIGNED ? (k1 - k0) / 128 : steps;
-    if (steps > 0) {
-        fetch(0);
-        keep(0);
-    }
-    for (int t = 0; t < whole; ++t) {
-        // this step's rows are there, and nobody reads the other buffer any more
-        if constexpr (ALIGNED) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const int whole = (k1 - k0) / 128;
+    for (int t = 0; t < AHEAD && t < steps; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) copy(t, t, q);
+    int buffer = 0;
+    const auto ready = [&](int t) {
+        // this step's rows are there, and nobody reads the buffer before it any more
+        if (AHEAD > 1 && t + 1 < steps)
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kCopies) : "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         stage_barrier();
-        if (t + 1 < steps) fetch(t + 1);
-        work(t, false);
-        if (t + 1 < steps) keep(t + 1);
+    };
+    for (int t = 0; t < whole; ++t) {
+        ready(t);
+        work(t, buffer, false);
+        buffer = buffer == AHEAD ? 0 : buffer + 1;
     }
     if (whole < steps) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        stage_barrier();
-        work(whole, true);
+        ready(whole);
+        work(whole, buffer, true);
     }
-    const int h = lane >> 5;
+    // The sums, 32 rows of the wave's columns at a time, go through LDS, so that a lane
+    // has eight neighbours of one row (a 16-byte store of a 16-bit type; single
+    // elements took as long as eight steps of k).
+    stage_barrier();  // the last step's operands are read
+    constexpr int NC = NI * 32, PITCH = NC + 4, LANES = NC / 8, ROWS = 64 / LANES;
+    static_assert(L::kWaves * 32 * PITCH * 4 <= L::kStages * L::kStage, "the sums' LDS");
+    const uint32_t mine = base + wave * 32 * PITCH * 4;
+    const int h = lane >> 5, c8 = lane % LANES * 8, col = j0 + wn * NC + c8;
+    float sw[8], bias[8];
 #pragma unroll
-    for (int j = 0; j < NI; ++j) {
-        const int col = j0 + wn * NI * 32 + 32 * j + (lane & 31);
-        if (col >= a.n) continue;
-        const float sw = a.scale_w[col], bias = a.bias ? a.bias[col] : 0.f;
+    for (int e = 0; e < 8; ++e) {
+        const int j = min(col + e, a.n - 1);
+        sw[e] = a.scale_w[j];
+        bias[e] = a.bias ? a.bias[j] : 0.f;
+    }
 #pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            __builtin_amdgcn_sched_barrier(0);  // (64 rows' places at a time would not fit)
+    for (int i = 0; i < MI; ++i) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = i0 + wm * MI * 32 + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
-                if (row >= a.m) continue;
-                if (a.split > 1)
-                    a.part[((int64_t)blockIdx.y * a.m + row) * a.n + col] = acc[i][j][r];
-                else
-                    put<OP>(a, row, col, acc[i][j][r], sw, bias);
+        for (int j = 0; j < NI; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                lds_write<int>(mine + ((8 * (r >> 2) + 4 * h + (r & 3)) * PITCH + 32 * j + (lane & 31)) * 4,
+                               acc[i][j][r]);
+        asm volatile("" ::: "memory");  // (a wave's LDS operations run in order)
+#pragma unroll
+        for (int q = 0; q < 32; q += ROWS) {
+            const int at = q + lane / LANES, row = i0 + (wm * MI + i) * 32 + at;
+            i32x4 v[2];
+            v[0] = lds_read<i32x4>(mine + (at * PITCH + c8) * 4);
+            v[1] = lds_read<i32x4>(mine + (at * PITCH + c8 + 4) * 4);
+            if (row >= a.m || col >= a.n) continue;
+            if (a.split > 1) {
+                int* to = a.part + ((int64_t)blockIdx.y * a.m + row) * a.n + col;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (col + e < a.n) to[e] = v[e >> 2][e & 3];
+                continue;
+            }
+            using T = typename El<OP>::T;
+            const float sx = a.scale_x[row];
+            T out[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) out[e] = (T)fmaf((float)v[e >> 2][e & 3] * sx, sw[e], bias[e]);
+            T* to = (T*)a.y + row * a.sy + col;
+            if (a.y_wide) {
+                __builtin_memcpy(__builtin_assume_aligned(to, 16), out, sizeof(out));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (col + e < a.n) to[e] = out[e];
             }
         }
+        asm volatile("" ::: "memory");
     }
 }
 
@@ -333,17 +443,14 @@ hipError_t tiles(const ProductArgs& a, hipStream_t s) {
     using L = Tile<BM, BN, WM, WN>;
     const int64_t count = ((int64_t)a.m + BM - 1) / BM * (((int64_t)a.n + BN - 1) / BN);
     const dim3 grid((unsigned)count, (unsigned)a.split);
-    if (a.aligned)
-        product_kernel<OP, BM, BN, WM, WN, true><<<grid, L::kThreads, 2 * L::kStage, s>>>(a);
-    else if constexpr (BM <= 128)
-        product_kernel<OP, BM, BN, WM, WN, false><<<grid, L::kThreads, 2 * L::kStage, s>>>(a);
+    product_kernel<OP, BM, BN, WM, WN><<<grid, L::kThreads, L::kStages * L::kStage, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.split == 1) return e;
     product_join_kernel<OP><<<flat_grid(((int64_t)a.m * a.n + 255) / 256), 256, 0, s>>>(a);
     return hipGetLastError();
 }
 
-constexpr int kFewRows = 64;
+constexpr int kFewRows = 32;
 
 int tile_of(int m, int n) {
     const auto count = [&](int64_t b) { return (m + b - 1) / b * ((n + b - 1) / b); };
@@ -352,27 +459,43 @@ int tile_of(int m, int n) {
     return 64;
 }
 
+template <int OP, bool DWORDS>
+hipError_t rows(const ProductArgs& a, hipStream_t s) {
+    if (a.m <= 16)
+        product_rows_kernel<OP, 1, 1, DWORDS><<<(unsigned)((a.n + 15) / 16), 64 * kRowWaves, 0, s>>>(a);
+    else
+        product_rows_kernel<OP, 2, 2, DWORDS><<<(unsigned)((a.n + 31) / 32), 64 * kRowWaves, 0, s>>>(a);
+    return hipGetLastError();
+}
+
 template <int OP>
 hipError_t product(const ProductArgs& a, hipStream_t s) {
-    if (a.m <= kFewRows) {
-        const unsigned g = (unsigned)((a.n + 15) / 16);
-        if (a.m <= 16)
-            product_rows_kernel<OP, 1><<<g, 256, 0, s>>>(a);
-        else if (a.m <= 32)
-            product_rows_kernel<OP, 2><<<g, 256, 0, s>>>(a);
-        else
-            product_rows_kernel<OP, 4><<<g, 256, 0, s>>>(a);
-        return hipGetLastError();
+    if (a.m <= kFewRows) return a.dwords ? rows<OP, true>(a, s) : rows<OP, false>(a, s);
+    ProductArgs b = a;
+    if (a.pack_x || a.pack_w) {
+        const int chunks = (a.k + 15) / 16;
+        const int most = std::max(a.pack_x ? a.m : 0, a.pack_w ? a.n : 0);
+        dim3 grid = flat_grid(((int64_t)most * chunks + 255) / 256);
+        grid.z = a.pack_w ? 2 : 1;
+        product_pack_kernel<<<grid, 256, 0, s>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        if (a.pack_x) b.x = a.pack_x, b.sx = 16 * chunks;
+        if (a.pack_w) b.w = a.pack_w, b.sw = 16 * chunks;
+        b.k = 16 * chunks;  // (k is whole chunks, or both are packed with zeros)
     }
     const int t = tile_of(a.m, a.n);
-    if (t == 256 && a.aligned) return tiles<OP, 256, 256, 2, 4>(a, s);
-    if (t >= 128) return tiles<OP, 128, 128, 2, 2>(a, s);
-    return tiles<OP, 64, 64, 2, 2>(a, s);
+    if (t == 256) return tiles<OP, 256, 256, 2, 4>(b, s);
+    if (t == 128) return tiles<OP, 128, 128, 2, 2>(b, s);
+    return tiles<OP, 64, 64, 2, 2>(b, s);
 }
 
 }  // namespace
 
+bool product_few(int m) { return m <= kFewRows; }
+
 int product_split(int m, int n, int k, int* split_k) {
+    k = (k + 15) / 16 * 16;
     *split_k = k > 0 ? k : 1;
     if (m <= kFewRows || n <= 0) return 1;
     const int64_t t = tile_of(m, n), count = (m + t - 1) / t * ((n + t - 1) / t);

@@ -120,21 +120,28 @@ __device__ __forceinline__ int share_at(int lane, int j, int e) {
 template <typename T, int LPR, int CH, bool WIDE>
 struct Share {
     T v[CH][8];
-    // on: the row is there; nothing is read else, and zeros stand for it.
+    // on: the row takes part; zeros stand for one that does not.  A lane without an
+    // element reads the row's first and leaves it: loads that ask nothing are all
+    // under way before the first is waited for.
     __device__ __forceinline__ void load(const T* row, int lane, int width, bool on) {
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
             if constexpr (WIDE) {
+                constexpr int N = 2 * sizeof(T);
                 const int at = share_at<LPR, true>(lane, j, 0);
-                if (on && at < width)
-                    __builtin_memcpy(v[j], __builtin_assume_aligned(row + at, 16), sizeof(v[j]));
-                else
-                    __builtin_memset(v[j], 0, sizeof(v[j]));
+                const bool in = on && at < width;
+                uint32_t w[N];
+                __builtin_memcpy(w, __builtin_assume_aligned(row + (in ? at : 0), 16), sizeof(w));
+#pragma unroll
+                for (int i = 0; i < N; ++i) w[i] = in ? w[i] : 0u;
+                __builtin_memcpy(v[j], w, sizeof(w));
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int at = share_at<LPR, false>(lane, j, e);
-                    v[j][e] = on && at < width ? row[at] : (T)0.f;
+                    const bool in = on && at < width;
+                    const T t = row[in ? at : 0];
+                    v[j][e] = in ? t : (T)0.f;
                 }
             }
         }

@@ -128,7 +128,9 @@ def test_product_refusals(lib, kw, word):
 def test_product_workspace(lib):
     refused(lib, product(lib, ws=None), "workspace", binding.FS_ERR_WORKSPACE)
     refused(lib, product(lib, size=64), "workspace", binding.FS_ERR_WORKSPACE)
-    assert lib.fs_quantized_product_workspace_bytes(-1, 3, 3) == 0
+    bad = QuantizedProductDesc(1, -1, 3, 3)
+    assert lib.fs_quantized_product_workspace_bytes(ctypes.byref(bad)) == 0
+    assert lib.fs_quantized_product_workspace_bytes(None) == 0
     assert binding.fs_quantized_product_workspace_bytes(8, 8192, 4096) >= 256
     assert lib.fs_quantized_product(None, A[0], 256, None) == binding.FS_ERR_INVALID_ARG
 
