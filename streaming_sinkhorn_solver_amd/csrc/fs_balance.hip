@@ -23,60 +23,50 @@ constexpr int kThreads = 256;
 // A column's place in the order of a row's logits as a whole number: the logit's
 // order (NaN counts as -inf, -0 as 0), below it the column's number from behind, so
 // that no two are alike and the lowest of equal columns is the largest.  A 16-bit
-// logit and its column fit 32 bits.  0 stands for none (a real one is above it).
+// logit has ten zeros at the end of its fp32 form, which hold the column's number.  0
+// stands for none (a real one is above it).
+__device__ __forceinline__ uint32_t order_of(float x) {
+    const uint32_t b = __float_as_uint(fmaxf(x + 0.f, -INFINITY));
+    return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float ordered(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
 template <int OP>
 struct Place {
     using Key = uint32_t;
-    static __device__ __forceinline__ Key of(float x, int col) {
-        x = x == x ? x + 0.f : -INFINITY;
-        uint32_t b;
-        if constexpr (OP == OP_BF16) {
-            b = __float_as_uint(x) >> 16;
-        } else {
-            const _Float16 h = (_Float16)x;
-            uint16_t t;
-            __builtin_memcpy(&t, &h, 2);
-            b = t;
-        }
-        b ^= b & 0x8000u ? 0xffffu : 0x8000u;
-        return b << 16 | (0xffffu - (uint32_t)col);
+    static constexpr uint32_t kLow = kBalanceMaxExperts - 1;
+    static __device__ __forceinline__ Key of(float x, int col, bool in) {
+        const Key k = (order_of(x) & ~kLow) | (kLow - (uint32_t)col);
+        return k & (in ? ~0u : 0u);
     }
-    static __device__ __forceinline__ int column(Key k) { return 0xffff - (int)(k & 0xffffu); }
+    static __device__ __forceinline__ int column(Key k) { return (int)(kLow - (k & kLow)); }
     static __device__ __forceinline__ float value(Key k) {
-        uint32_t b = k >> 16;
-        b ^= b & 0x8000u ? 0x8000u : 0xffffu;
-        if constexpr (OP == OP_BF16) return __uint_as_float(b << 16);
-        const uint16_t t = (uint16_t)b;
-        _Float16 h;
-        __builtin_memcpy(&h, &t, 2);
-        return (float)h;
+        return ordered(k & 0x80000000u ? k & ~kLow : k | kLow);
     }
     template <int LPT>
     static __device__ __forceinline__ Key most(Key k) {
         return lanes_max<LPT>(k);
     }
 };
+static_assert(kBalanceMaxExperts == 1 << 10, "a column's number has ten bits");
 template <>
 struct Place<OP_F32> {
     using Key = uint64_t;
-    static __device__ __forceinline__ Key of(float x, int col) {
-        x = x == x ? x + 0.f : -INFINITY;
-        uint32_t b = __float_as_uint(x);
-        b ^= b & 0x80000000u ? 0xffffffffu : 0x80000000u;
-        return (Key)b << 32 | (0xffffffffu - (uint32_t)col);
+    static __device__ __forceinline__ Key of(float x, int col, bool in) {
+        return in ? (Key)order_of(x) << 32 | (0xffffffffu - (uint32_t)col) : (Key)0;
     }
     static __device__ __forceinline__ int column(Key k) { return (int)(0xffffffffu - (uint32_t)k); }
-    static __device__ __forceinline__ float value(Key k) {
-        const uint32_t b = (uint32_t)(k >> 32);
-        return __uint_as_float(b ^ (b & 0x80000000u ? 0x80000000u : 0xffffffffu));
-    }
+    static __device__ __forceinline__ float value(Key k) { return ordered((uint32_t)(k >> 32)); }
     template <int LPT>
     static __device__ __forceinline__ Key most(Key k) {
-        const auto larger = [](Key a, Key b) { return a > b ? a : b; };
         const auto step = [&](auto o) {
             constexpr int O = decltype(o)::value;
-            if constexpr (LPT > O)
-                k = larger(k, (Key)lane_other<O>((uint32_t)(k >> 32)) << 32 | lane_other<O>((uint32_t)k));
+            if constexpr (LPT > O) {
+                const Key other =
+                    (Key)lane_other<O>((uint32_t)(k >> 32)) << 32 | lane_other<O>((uint32_t)k);
+                k = k > other ? k : other;
+            }
         };
         step(std::integral_constant<int, 1>{});
         step(std::integral_constant<int, 2>{});
@@ -88,20 +78,34 @@ struct Place<OP_F32> {
     }
 };
 
+template <typename Key>
+__device__ __forceinline__ void exchange(Key& a, Key& b) {
+    const Key x = a, y = b;
+    a = x > y ? x : y;
+    b = x > y ? y : x;
+}
 // Eight keys in descending order (Batcher's odd-even merge: 19 exchanges).
 template <typename Key>
 __device__ __forceinline__ void sort8(Key (&k)[8]) {
-    const auto order = [&](int i, int j) {
-        const Key a = k[i], b = k[j];
-        k[i] = a > b ? a : b;
-        k[j] = a > b ? b : a;
-    };
+    const auto order = [&](int i, int j) { exchange(k[i], k[j]); };
     order(0, 1), order(2, 3), order(4, 5), order(6, 7);
     order(0, 2), order(1, 3), order(4, 6), order(5, 7);
     order(1, 2), order(5, 6);
     order(0, 4), order(1, 5), order(2, 6), order(3, 7);
     order(2, 4), order(3, 5);
     order(1, 2), order(3, 4), order(5, 6);
+}
+// a: the eight largest of two descending lists (one list against the other from
+// behind leaves them, rising and falling once, which twelve exchanges sort).
+template <typename Key>
+__device__ __forceinline__ void merge8(Key (&a)[8], const Key (&b)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = a[j] > b[7 - j] ? a[j] : b[7 - j];
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if ((j & o) == 0) exchange(a[j], a[j + o]);
 }
 
 // A lane's columns e0 .. e0 + EPL - 1 of a row; -inf behind the last and in rows
@@ -134,15 +138,18 @@ __device__ __forceinline__ void write_loss(const BalanceArgs& a, int b, double t
     a.loss[2 * b + 1] = n > 0 ? (float)(squares / n) : 0.f;
 }
 
-// A lane sorts its eight columns (two lists of eight, of 16), and k times the
-// largest head of the lists is taken: a maximum over the lanes, and the list that
-// it came from moves up.
+// A lane sorts its columns (16 of them in two lists of eight, merged to the largest
+// eight where no more are chosen), and k times the largest head of the lists is
+// taken: a maximum over the lanes, and the list that it came from moves up.  Bound by
+// the vector unit's instructions, of which a lane of 16 columns needs fewer a row
+// than two of eight.
 template <int OP, int LPT, int EPL, int KMAX, bool WIDE>
 __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceArgs a) {
     using T = typename El<OP>::T;
     using P = Place<OP>;
     using Key = typename P::Key;
-    constexpr int GRP = kThreads / LPT, COLS = LPT * EPL, LISTS = EPL / 8;
+    constexpr int GRP = kThreads / LPT, COLS = LPT * EPL;
+    constexpr int SORTED = EPL / 8, LISTS = KMAX <= 8 ? 1 : SORTED;
     constexpr int SLOTS = (KMAX + LPT - 1) / LPT;  // of the chosen, a lane's
     __shared__ float red_p[4][COLS];
     __shared__ uint32_t hits[COLS];
@@ -167,12 +174,12 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceArgs a) 
 #pragma unroll
         for (int j = 0; j < EPL; ++j) v[j] = next[j];
         if (i + step < a.n) fetch(i + step, next);
-        Key key[LISTS][8];
+        Key key[SORTED][8];
         float x[EPL], top = -INFINITY;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             x[j] = (float)v[j];
-            key[j / 8][j % 8] = e0 + j < E ? P::of(x[j], e0 + j) : (Key)0;
+            key[j / 8][j % 8] = P::of(x[j], e0 + j, e0 + (WIDE ? j / 8 * 8 : j) < E);
             top = fmaxf(top, x[j]);
         }
         top = lanes_max<LPT>(top);
@@ -182,9 +189,10 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceArgs a) 
 #pragma unroll
         for (int j = 0; j < EPL; ++j) s += x[j] = on ? ex2((x[j] - ref) * kLog2e) : 0.f;
         s = lanes_sum<LPT>(s);
-        const float inv = on ? 1.f / s : 0.f, lse = on ? ref + logf(s) : 0.f;
+        const float inv = on ? __builtin_amdgcn_rcpf(s) : 0.f, lse = on ? fmaf(lg2(s), kLn2, ref) : 0.f;
 #pragma unroll
-        for (int l = 0; l < LISTS; ++l) sort8(key[l]);
+        for (int l = 0; l < SORTED; ++l) sort8(key[l]);
+        if constexpr (SORTED > LISTS) merge8(key[0], key[1]);
         Key mine[SLOTS] = {};
 #pragma unroll
         for (int q = 0; q < SLOTS; ++q) {
@@ -210,7 +218,7 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceArgs a) 
             gate[q] = have ? ex2((P::value(mine[q]) - ref) * kLog2e) * inv : 0.f;
             all += gate[q];
         }
-        const float scale = a.normalize && on ? 1.f / lanes_sum<LPT>(all) : 1.f;
+        const float scale = a.normalize && on ? __builtin_amdgcn_rcpf(lanes_sum<LPT>(all)) : 1.f;
 #pragma unroll
         for (int q = 0; q < SLOTS; ++q) {
             const int t = q * LPT + part;
@@ -252,13 +260,13 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceArgs a) 
             a.counts[(int64_t)b * E + e] = c;
             terms += (double)c * p;
         } else {
-            a.part[at * E + e] = make_float2(p, __int_as_float(c));
+            a.part[at * (E + 1) + e] = make_float2(p, __int_as_float(c));
         }
     }
     const float sq = red_s[0].x + red_s[1].x + red_s[2].x + red_s[3].x;
     const float rows = red_s[0].y + red_s[1].y + red_s[2].y + red_s[3].y;
     if (a.blocks > 1) {
-        if (threadIdx.x == 0) a.part_s[at] = make_float2(sq, rows);
+        if (threadIdx.x == 0) a.part[at * (E + 1) + E] = make_float2(sq, __int_as_float((int)rows));
         return;
     }
     for (int o = 32; o >= 1; o >>= 1) terms += __shfl_xor(terms, o, 64);
@@ -267,21 +275,22 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceArgs a) 
     if (threadIdx.x == 0) write_loss(a, b, red_t[0] + red_t[1] + red_t[2] + red_t[3], sq, rows);
 }
 
-// The workgroups' sums of a batch entry, 16 columns a workgroup, 64 lanes each, in
+// The workgroups' sums of a batch entry (behind the columns' those of lse^2 and of
+// rows that take part), 8 columns a workgroup, 128 lanes each, in
 // 64 bits and a fixed order.  The last of the entry's workgroups to arrive adds
 // their terms (in their order) to the loss; the counter was cleared by the launch
 // before.
 __global__ __launch_bounds__(1024) void balance_join_kernel(const BalanceArgs a) {
-    __shared__ double red_p[64][17];
-    __shared__ int red_c[64][17];
+    __shared__ double red_p[128][9];
+    __shared__ int red_c[128][9];
     __shared__ int last;
-    const int b = blockIdx.y, c = threadIdx.x & 15, y = threadIdx.x >> 4, e = blockIdx.x * 16 + c;
+    const int b = blockIdx.y, c = threadIdx.x & 7, y = threadIdx.x >> 3, e = blockIdx.x * 8 + c;
     double p = 0.0;
     int n = 0;
-    if (e < a.E) {
-#pragma unroll 4
-        for (int k = y; k < a.blocks; k += 64) {
-            const float2 v = a.part[((int64_t)b * a.blocks + k) * a.E + e];
+    if (e <= a.E) {
+#pragma unroll 8
+        for (int k = y; k < a.blocks; k += 128) {
+            const float2 v = a.part[((int64_t)b * a.blocks + k) * (a.E + 1) + e];
             p += (double)v.x;
             n += __float_as_int(v.y);
         }
@@ -289,40 +298,38 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(const BalanceArgs a)
     red_p[y][c] = p;
     red_c[y][c] = n;
     __syncthreads();
-    for (int o = 32; o >= 1; o >>= 1) {
+    for (int o = 64; o >= 1; o >>= 1) {
         if (y < o) red_p[y][c] += red_p[y + o][c], red_c[y][c] += red_c[y + o][c];
         __syncthreads();
     }
-    double* terms = a.terms + (int64_t)b * gridDim.x;
+    // [gridDim.x] terms, then the sums of squares and rows
+    double* terms = a.terms + (int64_t)b * (gridDim.x + 2);
+    const auto put = [&](int at, double v) {
+        __hip_atomic_store(terms + at, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    };
     if (threadIdx.x < 64) {
         double t = 0.0;
-        if (y == 0) {
-            if (e < a.E) a.counts[(int64_t)b * a.E + e] = red_c[0][c];
+        if (y == 0 && e < a.E) {
+            a.counts[(int64_t)b * a.E + e] = red_c[0][c];
             t = (double)red_c[0][c] * red_p[0][c];
         }
-        for (int o = 8; o >= 1; o >>= 1) t += __shfl_xor(t, o, 64);
-        if (threadIdx.x == 0) {
-            __hip_atomic_store(terms + blockIdx.x, t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (y == 0 && e == a.E) put(gridDim.x, red_p[0][c]), put(gridDim.x + 1, (double)red_c[0][c]);
+        for (int o = 4; o >= 1; o >>= 1) t += __shfl_xor(t, o, 64);
+        if (threadIdx.x == 0) put(blockIdx.x, t);
+        __threadfence();
+        if (threadIdx.x == 0)
             last = __hip_atomic_fetch_add(a.arrived + b, 1, __ATOMIC_ACQ_REL,
                                           __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
-        }
     }
     __syncthreads();
     if (!last || threadIdx.x >= 64) return;
-    double sum = 0.0, squares = 0.0, rows = 0.0;
-    for (int k = threadIdx.x; k < (int)gridDim.x; k += 64)
-        sum += __hip_atomic_load(terms + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    for (int k = threadIdx.x; k < a.blocks; k += 64) {
-        const float2 s = a.part_s[(int64_t)b * a.blocks + k];
-        squares += (double)s.x;
-        rows += (double)s.y;
-    }
-    for (int o = 32; o >= 1; o >>= 1) {
-        sum += __shfl_xor(sum, o, 64);
-        squares += __shfl_xor(squares, o, 64);
-        rows += __shfl_xor(rows, o, 64);
-    }
-    if (threadIdx.x == 0) write_loss(a, b, sum, squares, rows);
+    const auto get = [&](int at) {
+        return __hip_atomic_load(terms + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    };
+    double sum = 0.0;
+    for (int k = threadIdx.x; k < (int)gridDim.x; k += 64) sum += get(k);
+    for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
+    if (threadIdx.x == 0) write_loss(a, b, sum, get(gridDim.x), get(gridDim.x + 1));
 }
 
 // Backward.  A lane takes up to SLOTS of a row's chosen columns; what each is worth
@@ -334,7 +341,7 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(const BalanceArgs
     using T = typename El<OP>::T;
     constexpr int GRP = kThreads / LPT, SLOTS = (KMAX + LPT - 1) / LPT, COLS = LPT * EPL;
     __shared__ __align__(16) float worth_of[GRP][COLS];
-    __shared__ __align__(16) int named_by[GRP][COLS];
+    __shared__ __align__(16) float named_by[GRP][COLS];
     const int lane = threadIdx.x & 63, part = lane % LPT, e0 = part * EPL, b = blockIdx.y, E = a.E;
     const int size = a.lengths ? max(0, min(a.n, a.lengths[b])) : a.n;
     const uint32_t worth = lds_addr(worth_of[threadIdx.x / LPT]);
@@ -356,100 +363,113 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(const BalanceArgs
     for (int j = 0; j < EPL; ++j) even[j] *= balance;
     struct Row {
         T v[EPL];
-        int id[SLOTS];  // of this lane's chosen columns, -1: none
-        float g[SLOTS], x[SLOTS], lse;
-        bool on;
+        int id[SLOTS], first;  // this lane's chosen columns, the row's first
+        float g[SLOTS], lse;
     };
+    // (every read of a row is under way before the first is waited for)
     const auto fetch = [&](int64_t i, Row& r) {
         const int64_t row = (int64_t)b * a.n + i;
-        const T* x = (const T*)a.x.p + b * a.x.sb + i * a.x.sr;
+        const bool in = i < size;
         const int* ids = a.ids + row * a.k;
-        r.on = i < size && ids[0] >= 0;
-        r.lse = r.on ? a.lse[row] : 0.f;
-        load_columns<T, EPL, WIDE>(x, e0, E, r.on, r.v);
+        load_columns<T, EPL, WIDE>((const T*)a.x.p + b * a.x.sb + i * a.x.sr, e0, E, in, r.v);
+        r.first = ids[0];
+        r.lse = a.lse[row];
 #pragma unroll
         for (int q = 0; q < SLOTS; ++q) {
             const int t = q * LPT + part;
-            r.id[q] = -1;
-            r.g[q] = r.x[q] = 0.f;
-            if (!a.ggates || !r.on || t >= a.k) continue;
-            const int id = ids[t];
-            if (id < 0 || id >= E) continue;
-            r.id[q] = id;
-            r.g[q] = a.ggates[row * a.k + t];
-            if (a.normalize) r.x[q] = (float)x[id];
+            r.id[q] = ids[t < a.k ? t : 0];
+            r.g[q] = a.ggates ? a.ggates[row * a.k + (t < a.k ? t : 0)] : 0.f;
+            if (t >= a.k || !a.ggates) r.id[q] = -1;
         }
+        if (!in) r.first = -1;
     };
     const int step = gridDim.x * GRP;
-    for (int64_t i = (int64_t)blockIdx.x * GRP + threadIdx.x / LPT; i < a.n; i += step) {
-        Row r;
-        fetch(i, r);
+    int64_t i = (int64_t)blockIdx.x * GRP + threadIdx.x / LPT;
+    Row next;
+    if (i < a.n) fetch(i, next);
+    for (; i < a.n; i += step) {
+        Row r = next;
+        if (i + step < a.n) fetch(i + step, next);
+        const bool on = r.first >= 0;
         float p[EPL], dp[EPL];
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) p[j] = ex2(((float)r.v[j] - r.lse) * kLog2e);
+        for (int j = 0; j < EPL; ++j) {
+            p[j] = on ? ex2(((float)r.v[j] - r.lse) * kLog2e) : 0.f;
+            dp[j] = even[j];
+        }
         if (a.ggates) {
-            if (a.normalize) {
-                float chosen = 0.f, mid = 0.f;
+            bool have[SLOTS], twice = false;
 #pragma unroll
-                for (int q = 0; q < SLOTS; ++q) {
-                    const float pq = r.id[q] >= 0 ? ex2((r.x[q] - r.lse) * kLog2e) : 0.f;
-                    chosen += pq;
-                    mid = fmaf(pq, r.g[q], mid);
-                }
-                chosen = lanes_sum<LPT>(chosen);
-                mid = lanes_sum<LPT>(mid);
-                // (a choice from elsewhere may have no probability at all)
-                const float scale = chosen != 0.f ? 1.f / chosen : 0.f, shift = mid * scale;
-#pragma unroll
-                for (int q = 0; q < SLOTS; ++q) r.g[q] = (r.g[q] - shift) * scale;
+            for (int j = 0; j < EPL; j += 4) {
+                lds_write<f32x4>(worth + 4 * (e0 + j), f32x4{0, 0, 0, 0});
+                lds_write<f32x4>(named + 4 * (e0 + j), f32x4{0, 0, 0, 0});
             }
 #pragma unroll
-            for (int j = 0; j < EPL; j += 4) lds_write<f32x4>(worth + 4 * (e0 + j), f32x4{0, 0, 0, 0});
+            for (int q = 0; q < SLOTS; ++q) {
+                have[q] = on && r.id[q] >= 0 && r.id[q] < E;
+                if (have[q]) lds_write<int>(named + 4 * r.id[q], 1 + q * LPT + part);
+            }
+            asm volatile("" ::: "memory");
 #pragma unroll
             for (int q = 0; q < SLOTS; ++q)
-                if (r.id[q] >= 0) lds_write<int>(named + 4 * r.id[q], q * LPT + part);
+                if (have[q]) twice |= lds_read<int>(named + 4 * r.id[q]) != 1 + q * LPT + part;
             asm volatile("" ::: "memory");
-            bool twice = false;
+            if (!__ballot(twice)) {
 #pragma unroll
-            for (int q = 0; q < SLOTS; ++q)
-                if (r.id[q] >= 0) {
-                    twice |= lds_read<int>(named + 4 * r.id[q]) != q * LPT + part;
-                    lds_write<float>(worth + 4 * r.id[q], r.g[q]);
-                }
-            asm volatile("" ::: "memory");
-            if (__ballot(twice)) {
+                for (int q = 0; q < SLOTS; ++q)
+                    if (have[q]) {
+                        lds_write<float>(worth + 4 * r.id[q], r.g[q]);
+                        lds_write<float>(named + 4 * r.id[q], 1.f);
+                    }
+            } else {
 #pragma unroll
                 for (int j = 0; j < EPL; j += 4)
-                    lds_write<f32x4>(worth + 4 * (e0 + j), f32x4{0, 0, 0, 0});
+                    lds_write<f32x4>(named + 4 * (e0 + j), f32x4{0, 0, 0, 0});
                 asm volatile("" ::: "memory");
 #pragma unroll
                 for (int q = 0; q < SLOTS; ++q)
                     for (int t = 0; t < LPT; ++t) {
-                        if (part == t && r.id[q] >= 0) {
-                            const uint32_t at = worth + 4 * r.id[q];
-                            lds_write<float>(at, lds_read<float>(at) + r.g[q]);
+                        if (part == t && have[q]) {
+                            const uint32_t at = 4 * r.id[q];
+                            lds_write<float>(worth + at, lds_read<float>(worth + at) + r.g[q]);
+                            lds_write<float>(named + at, lds_read<float>(named + at) + 1.f);
                         }
                         asm volatile("" ::: "memory");
                     }
             }
+            asm volatile("" ::: "memory");
+            float dg[EPL], times[EPL], scale = 1.f, shift = 0.f;
 #pragma unroll
             for (int j = 0; j < EPL; j += 4) {
-                const f32x4 w = lds_read<f32x4>(worth + 4 * (e0 + j));
+                const f32x4 x = lds_read<f32x4>(worth + 4 * (e0 + j));
+                const f32x4 y = lds_read<f32x4>(named + 4 * (e0 + j));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dp[j + e] = even[j + e] + w[e];
+                for (int e = 0; e < 4; ++e) dg[j + e] = x[e], times[j + e] = y[e];
             }
             asm volatile("" ::: "memory");
-        } else {
+            if (a.normalize) {
+                float chosen = 0.f, mid = 0.f;
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) dp[j] = even[j];
+                for (int j = 0; j < EPL; ++j) {
+                    chosen = fmaf(p[j], times[j], chosen);
+                    mid = fmaf(p[j], dg[j], mid);
+                }
+                chosen = lanes_sum<LPT>(chosen);
+                mid = lanes_sum<LPT>(mid);
+                // (a choice from elsewhere may have no probability at all)
+                scale = chosen != 0.f ? 1.f / chosen : 0.f;
+                shift = mid * scale;
+            }
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) dp[j] = fmaf(fmaf(-times[j], shift, dg[j]), scale, dp[j]);
         }
         float mean = 0.f;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) mean = fmaf(p[j], dp[j], mean);
-        mean = lanes_sum<LPT>(mean) - square * r.lse;
+        mean = lanes_sum<LPT>(mean) - (on ? square * r.lse : 0.f);
         T* gx = (T*)a.gx.p + b * a.gx.sb + i * a.gx.sr;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) r.v[j] = (T)(r.on ? p[j] * (dp[j] - mean) : 0.f);
+        for (int j = 0; j < EPL; ++j) r.v[j] = (T)(on ? p[j] * (dp[j] - mean) : 0.f);
         if constexpr (WIDE) {
 #pragma unroll
             for (int j = 0; j < EPL; j += 8)
@@ -466,9 +486,9 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(const BalanceArgs
 template <int OP, int LPT, int EPL, int KMAX, bool WIDE>
 hipError_t go(const BalanceArgs& a, bool back, hipStream_t s) {
     if (back) {
-        // no sums over rows: enough workgroups for every CU's waves
+        // four workgroups a CU, which read a row ahead
         const int64_t turns = ((int64_t)a.n + kThreads / LPT - 1) / (kThreads / LPT);
-        const dim3 grid((unsigned)std::min<int64_t>(turns, std::max(1, 4096 / a.B)), (unsigned)a.B);
+        const dim3 grid((unsigned)std::min<int64_t>(turns, std::max(1, 1024 / a.B)), (unsigned)a.B);
         balance_bwd_kernel<OP, LPT, EPL, KMAX, WIDE><<<grid, kThreads, 0, s>>>(a);
     } else {
         const dim3 grid((unsigned)a.blocks, (unsigned)a.B);
@@ -491,9 +511,9 @@ hipError_t go(const BalanceArgs& a, bool back, hipStream_t s) {
     if (a.E <= 16) return go<OP, 2, 8>(a, back, s);
     if (a.E <= 32) return go<OP, 4, 8>(a, back, s);
     if (a.E <= 64) return go<OP, 8, 8>(a, back, s);
-    if (a.E <= 128) return go<OP, 16, 8>(a, back, s);
-    if (a.E <= 256) return go<OP, 32, 8>(a, back, s);
-    if (a.E <= 512) return go<OP, 64, 8>(a, back, s);
+    if (a.E <= 128) return go<OP, 8, 16>(a, back, s);
+    if (a.E <= 256) return go<OP, 16, 16>(a, back, s);
+    if (a.E <= 512) return go<OP, 32, 16>(a, back, s);
     return go<OP, 64, 16>(a, back, s);
 }
 hipError_t go(const BalanceArgs& a, bool back, hipStream_t s) {
@@ -504,7 +524,7 @@ hipError_t go(const BalanceArgs& a, bool back, hipStream_t s) {
 
 int rows_at_once(int E) {
     int lanes = 1;
-    while (lanes < 64 && lanes * 8 < E) lanes *= 2;
+    while (lanes < 64 && lanes * (E <= 64 ? 8 : 16) < E) lanes *= 2;
     return kThreads / lanes;
 }
 
@@ -520,7 +540,7 @@ int balance_blocks(int B, int n, int E) {
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
     const hipError_t e = go(a, false, s);
     if (e != hipSuccess || a.blocks == 1) return e;
-    balance_join_kernel<<<dim3((unsigned)((a.E + 15) / 16), (unsigned)a.B), 1024, 0, s>>>(a);
+    balance_join_kernel<<<dim3((unsigned)(a.E / 8 + 1), (unsigned)a.B), 1024, 0, s>>>(a);
     return hipGetLastError();
 }
 

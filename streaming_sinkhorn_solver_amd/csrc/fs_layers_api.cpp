@@ -469,15 +469,13 @@ fs_status take_balance(const fs_balance_desc* p, BalanceArgs& a) {
 }
 
 struct BalanceLayout {
-    size_t s = 0, terms = 0, arrived = 0, total = kAlign;
+    size_t terms = 0, arrived = 0, total = kAlign;
 };
 BalanceLayout balance_layout(const BalanceArgs& a) {
     BalanceLayout l;
     if (a.blocks > 1) {
-        const size_t parts = (size_t)a.B * a.blocks;
-        l.s = up(parts * a.E * sizeof(float2));
-        l.terms = l.s + up(parts * sizeof(float2));
-        l.arrived = l.terms + up((size_t)a.B * cdiv(a.E, 16) * sizeof(double));
+        l.terms = up((size_t)a.B * a.blocks * (a.E + 1) * sizeof(float2));
+        l.arrived = l.terms + up((size_t)a.B * (a.E / 8 + 3) * sizeof(double));
         l.total = l.arrived + up((size_t)a.B * sizeof(int));
     }
     return l;
@@ -523,7 +521,6 @@ fs_status fs_balance_loss(const fs_balance_desc* desc, fs_rows logits, int32_t* 
     a.loss = loss;
     a.lse = lse;
     a.part = (float2*)workspace;
-    a.part_s = (float2*)((char*)workspace + l.s);
     a.terms = (double*)((char*)workspace + l.terms);
     a.arrived = (int*)((char*)workspace + l.arrived);
     return hip_status(launch_balance(a, (hipStream_t)stream), "fs_balance_loss");

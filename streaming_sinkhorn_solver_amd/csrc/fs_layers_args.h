@@ -106,9 +106,8 @@ struct BalanceArgs {
     const float* gloss;
     const float* ggates;
     int blocks;        // workgroups of a batch entry
-    float2* part;      // [B][blocks][E] sum of p, count (as bits)
-    float2* part_s;    // [B][blocks] sum of lse^2, rows that take part
-    double* terms;     // [B][ceil(E / 16)] the columns' terms of the loss
+    float2* part;      // [B][blocks][E + 1] sum of p, count (as bits); of lse^2, rows
+    double* terms;     // [B][E / 8 + 1 + 2] the columns' terms of the loss; the last sums
     int* arrived;      // [B] workgroups whose term is there
 };
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s);

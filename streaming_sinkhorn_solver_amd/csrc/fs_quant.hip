@@ -254,20 +254,20 @@ __global__ __launch_bounds__(256) void product_pack_kernel(const ProductArgs a) 
 // The 16-byte chunks of a row of 128 bytes stand in an order that depends on its
 // number, so that 16 lanes reading one chunk of 16 rows use all banks.  WM x WN
 // waves.
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, int STAGES>
 struct Tile {
     static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
     static constexpr int MI = BM / WM / 32, NI = BN / WN / 32;
     static constexpr int kStage = (BM + BN) * 128;
-    static constexpr int kStages = 3 * kStage <= 80 * 1024 ? 3 : 2;  // two workgroups a CU
+    static constexpr int kStages = STAGES;
 };
 __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
     return row * 128 + ((chunk ^ (row >> 1)) & 7) * 16;
 }
 
-template <int OP, int BM, int BN, int WM, int WN>
+template <int OP, int BM, int BN, int WM, int WN, int STAGES>
 __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs a) {
-    using L = Tile<BM, BN, WM, WN>;
+    using L = Tile<BM, BN, WM, WN, STAGES>;
     constexpr int MI = L::MI, NI = L::NI;
     extern __shared__ __align__(16) char lds[];
     const uint32_t base = lds_addr(lds);
@@ -356,8 +356,8 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
     int buffer = 0;
     const auto ready = [&](int t) {
         // this step's rows are there, and nobody reads the buffer before it any more
-        if (AHEAD > 1 && t + 1 < steps)
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kCopies) : "memory");
+        if (AHEAD > 1 && t + AHEAD - 1 < steps)
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((AHEAD - 1) * kCopies) : "memory");
         else
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         stage_barrier();
@@ -371,14 +371,38 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
         ready(whole);
         work(whole, buffer, true);
     }
+    constexpr int NC = NI * 32, PITCH = NC + 4, LANES = NC / 8, ROWS = 64 / LANES;
+    static_assert(L::kWaves * 32 * PITCH * 4 <= L::kStages * L::kStage, "the sums' LDS");
+    const uint32_t mine = base + wave * 32 * PITCH * 4;
+    const int h = lane >> 5;
+    if (!a.y_wide || a.split > 1) {
+        // ranges' sums and rows of any width: single elements, neighbours by lane
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+            const int col = j0 + wn * NC + 32 * j + (lane & 31);
+            if (col >= a.n) continue;
+            const float sw = a.scale_w[col], bias = a.bias ? a.bias[col] : 0.f;
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                __builtin_amdgcn_sched_barrier(0);  // (64 rows' places at a time would not fit)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int row = i0 + (wm * MI + i) * 32 + 8 * (r >> 2) + 4 * h + (r & 3);
+                    if (row >= a.m) continue;
+                    if (a.split > 1)
+                        a.part[((int64_t)blockIdx.y * a.m + row) * a.n + col] = acc[i][j][r];
+                    else
+                        put<OP>(a, row, col, acc[i][j][r], sw, bias);
+                }
+            }
+        }
+        return;
+    }
     // The sums, 32 rows of the wave's columns at a time, go through LDS, so that a lane
     // has eight neighbours of one row (a 16-byte store of a 16-bit type; single
     // elements took as long as eight steps of k).
     stage_barrier();  // the last step's operands are read
-    constexpr int NC = NI * 32, PITCH = NC + 4, LANES = NC / 8, ROWS = 64 / LANES;
-    static_assert(L::kWaves * 32 * PITCH * 4 <= L::kStages * L::kStage, "the sums' LDS");
-    const uint32_t mine = base + wave * 32 * PITCH * 4;
-    const int h = lane >> 5, c8 = lane % LANES * 8, col = j0 + wn * NC + c8;
+    const int c8 = lane % LANES * 8, col = j0 + wn * NC + c8;
     float sw[8], bias[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -397,31 +421,17 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
         asm volatile("" ::: "memory");  // (a wave's LDS operations run in order)
 #pragma unroll
         for (int q = 0; q < 32; q += ROWS) {
+            using T = typename El<OP>::T;
             const int at = q + lane / LANES, row = i0 + (wm * MI + i) * 32 + at;
             i32x4 v[2];
             v[0] = lds_read<i32x4>(mine + (at * PITCH + c8) * 4);
             v[1] = lds_read<i32x4>(mine + (at * PITCH + c8 + 4) * 4);
             if (row >= a.m || col >= a.n) continue;
-            if (a.split > 1) {
-                int* to = a.part + ((int64_t)blockIdx.y * a.m + row) * a.n + col;
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (col + e < a.n) to[e] = v[e >> 2][e & 3];
-                continue;
-            }
-            using T = typename El<OP>::T;
             const float sx = a.scale_x[row];
             T out[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) out[e] = (T)fmaf((float)v[e >> 2][e & 3] * sx, sw[e], bias[e]);
-            T* to = (T*)a.y + row * a.sy + col;
-            if (a.y_wide) {
-                __builtin_memcpy(__builtin_assume_aligned(to, 16), out, sizeof(out));
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (col + e < a.n) to[e] = out[e];
-            }
+            __builtin_memcpy(__builtin_assume_aligned((T*)a.y + row * a.sy + col, 16), out, sizeof(out));
         }
         asm volatile("" ::: "memory");
     }
@@ -438,12 +448,12 @@ __global__ __launch_bounds__(256) void product_join_kernel(const ProductArgs a) 
     put<OP>(a, i, j, sum, a.scale_w[j], a.bias ? a.bias[j] : 0.f);
 }
 
-template <int OP, int BM, int BN, int WM, int WN>
+template <int OP, int BM, int BN, int WM, int WN, int STAGES>
 hipError_t tiles(const ProductArgs& a, hipStream_t s) {
-    using L = Tile<BM, BN, WM, WN>;
+    using L = Tile<BM, BN, WM, WN, STAGES>;
     const int64_t count = ((int64_t)a.m + BM - 1) / BM * (((int64_t)a.n + BN - 1) / BN);
     const dim3 grid((unsigned)count, (unsigned)a.split);
-    product_kernel<OP, BM, BN, WM, WN><<<grid, L::kThreads, L::kStages * L::kStage, s>>>(a);
+    product_kernel<OP, BM, BN, WM, WN, STAGES><<<grid, L::kThreads, L::kStages * L::kStage, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.split == 1) return e;
     product_join_kernel<OP><<<flat_grid(((int64_t)a.m * a.n + 255) / 256), 256, 0, s>>>(a);
@@ -452,11 +462,13 @@ hipError_t tiles(const ProductArgs& a, hipStream_t s) {
 
 constexpr int kFewRows = 32;
 
+int64_t tiles_of(int m, int n, int64_t b) { return (m + b - 1) / b * ((n + b - 1) / b); }
+
+// The largest tiles (fewest bytes through LDS for a product) that still fill the
+// chip: 4096 x 4096 x 4096 in tiles of 256 / 128, us, 68 / 83; 2048 x 4096 x 4096, 128
+// workgroups of tiles of 256, 62 / 48.
 int tile_of(int m, int n) {
-    const auto count = [&](int64_t b) { return (m + b - 1) / b * ((n + b - 1) / b); };
-    if (count(256) >= 192) return 256;
-    if (count(128) >= 192) return 128;
-    return 64;
+    return tiles_of(m, n, 256) >= 192 ? 256 : tiles_of(m, n, 128) >= 192 ? 128 : 64;
 }
 
 template <int OP, bool DWORDS>
@@ -485,9 +497,13 @@ hipError_t product(const ProductArgs& a, hipStream_t s) {
         b.k = 16 * chunks;  // (k is whole chunks, or both are packed with zeros)
     }
     const int t = tile_of(a.m, a.n);
-    if (t == 256) return tiles<OP, 256, 256, 2, 4>(b, s);
-    if (t == 128) return tiles<OP, 128, 128, 2, 2>(b, s);
-    return tiles<OP, 64, 64, 2, 2>(b, s);
+    if (t == 256) return tiles<OP, 256, 256, 2, 4, 2>(b, s);
+    // one workgroup a CU has all of LDS for rows on their way (1024 x 4096 x 4096: 27 us
+    // with four buffers, 32 with two; with more workgroups two of them share a CU: 2048
+    // x 4096 x 4096, 55 / 48)
+    if (t == 128 && tiles_of(a.m, a.n, 128) <= 256) return tiles<OP, 128, 128, 2, 4, 4>(b, s);
+    if (t == 128) return tiles<OP, 128, 128, 2, 4, 2>(b, s);
+    return tiles<OP, 64, 64, 2, 2, 5>(b, s);
 }
 
 }  // namespace
@@ -498,8 +514,8 @@ int product_split(int m, int n, int k, int* split_k) {
     k = (k + 15) / 16 * 16;
     *split_k = k > 0 ? k : 1;
     if (m <= kFewRows || n <= 0) return 1;
-    const int64_t t = tile_of(m, n), count = (m + t - 1) / t * ((n + t - 1) / t);
-    if (t > 64 || count >= 128) return 1;
+    const int64_t count = tiles_of(m, n, 64);
+    if (tile_of(m, n) > 64 || count >= 128) return 1;
     const int64_t s = std::min<int64_t>(std::min<int64_t>(256 / count, k / 1024), 16);
     if (s <= 1) return 1;
     *split_k = (int)(((k + s - 1) / s + 127) / 128 * 128);

@@ -10,10 +10,10 @@ namespace fs {
 // below O agree already; 16, 32: of the other row or half).
 template <int O>
 __device__ __forceinline__ uint32_t lane_other(uint32_t x) {
-    if constexpr (O == 1) return __builtin_amdgcn_update_dpp(x, x, 0xB1, 0xF, 0xF, false);
-    if constexpr (O == 2) return __builtin_amdgcn_update_dpp(x, x, 0x4E, 0xF, 0xF, false);
-    if constexpr (O == 4) return __builtin_amdgcn_update_dpp(x, x, 0x141, 0xF, 0xF, false);
-    if constexpr (O == 8) return __builtin_amdgcn_update_dpp(x, x, 0x140, 0xF, 0xF, false);
+    if constexpr (O == 1) return __builtin_amdgcn_update_dpp(0u, x, 0xB1, 0xF, 0xF, true);
+    if constexpr (O == 2) return __builtin_amdgcn_update_dpp(0u, x, 0x4E, 0xF, 0xF, true);
+    if constexpr (O == 4) return __builtin_amdgcn_update_dpp(0u, x, 0x141, 0xF, 0xF, true);
+    if constexpr (O == 8) return __builtin_amdgcn_update_dpp(0u, x, 0x140, 0xF, 0xF, true);
     const bool upper = threadIdx.x & O;
     if constexpr (O == 16) {
         const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
