@@ -837,6 +837,9 @@ def _flat(t: Optional[torch.Tensor], name: str, dev: int, dtype, shape) -> Optio
     """A contiguous tensor of this type and shape, as its address."""
     if t is None:
         return None
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and \
+            t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     _on(t, name, dev)
     if t.dtype != dtype or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous {dtype} tensor")
@@ -851,7 +854,8 @@ def _work(workspace: Optional[torch.Tensor], size, like: torch.Tensor, dev: int,
     if workspace is None:
         workspace = _empty(size() + 256, torch.uint8, like.device, stream)
     else:
-        _on(workspace, "workspace", dev)
+        if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev:
+            _on(workspace, "workspace", dev)
         if not workspace.is_contiguous():
             raise TypeError("workspace must be contiguous")
     base = workspace.data_ptr()
@@ -1100,15 +1104,17 @@ def _states(t: Optional[torch.Tensor], name: str, like: torch.Tensor, dev: int, 
     """A [batch, rows, width] or [rows, width] tensor of like's type as fs_rows."""
     if t is None:
         return _NO_ROWS
-    _on(t, name, dev)
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} is {t.dtype}, not {like.dtype} as the others")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)} (is {tuple(t.shape)})")
+    if t is not like:
+        if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+            _on(t, name, dev)
+        if t.dtype is not like.dtype:
+            raise TypeError(f"{name} is {t.dtype}, not {like.dtype} as the others")
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {tuple(shape)} (is {tuple(t.shape)})")
     s = t.stride()
     if s[-1] != 1 and shape[-1] != 1:
         raise ValueError(f"{name}'s last axis must be contiguous")
-    return Rows(t.data_ptr(), s[0] if len(s) == 3 else 0, s[-2], 0)
+    return Rows(t.data_ptr(), s[0], s[1]) if len(s) == 3 else Rows(t.data_ptr(), 0, s[0])
 
 
 def _matrix8(t: torch.Tensor, name: str, dev: int, shape):
