@@ -4,8 +4,7 @@
 //   L0 = E sum f P, L1 = mean lse^2, gates = p of the chosen (over their sum S);
 //   dp_e = dL0 E f_e / N + sum_{id = e} (dgate - (sum dgate gate)) / S,
 //   dx = p (dp - sum p dp + dL1 2 lse / N).
-// A row's columns lie with LPT lanes, neighbours with one lane, so that the lowest
-// of equal columns is the first of the lowest lane.  Sums over columns run in the
+// A row's columns lie with LPT lanes.  Sums over columns run in the
 // lanes' registers over a workgroup's rows, then over workgroups in a second
 // launch (in 64 bits, in a fixed order).
 #include "fs_layers_args.h"
@@ -108,24 +107,33 @@ __device__ __forceinline__ void merge8(Key (&a)[8], const Key (&b)[8]) {
             if ((j & o) == 0) exchange(a[j], a[j + o]);
 }
 
-// A lane's columns e0 .. e0 + EPL - 1 of a row; -inf behind the last and in rows
-// that take no part.  A lane without a column reads the row's first and leaves it.
-template <typename T, int EPL, bool WIDE>
-__device__ __forceinline__ void load_columns(const T* row, int e0, int E, bool on, T (&v)[EPL]) {
+// The column that is a lane's j-th of a row's LPT lanes.  WIDE: groups of eight
+// neighbours, groups side by side with neighbouring lanes; else single ones, so that
+// a wave's reads and writes are of neighbours either way.
+template <int LPT, bool WIDE>
+__device__ __forceinline__ int column_of(int part, int j) {
+    return WIDE ? (j / 8 * LPT + part) * 8 + j % 8 : j * LPT + part;
+}
+// A lane's columns of a row; -inf behind the last and in rows that take no part.  A
+// lane without a column reads the row's first and leaves it.
+template <typename T, int LPT, int EPL, bool WIDE>
+__device__ __forceinline__ void load_columns(const T* row, int part, int E, bool on, T (&v)[EPL]) {
     if constexpr (WIDE) {
 #pragma unroll
         for (int j = 0; j < EPL; j += 8) {
-            const bool in = on && e0 + j < E;
+            const int col = column_of<LPT, WIDE>(part, j);
+            const bool in = on && col < E;
             T t[8];
-            __builtin_memcpy(t, __builtin_assume_aligned(row + (in ? e0 + j : 0), 16), sizeof(t));
+            __builtin_memcpy(t, __builtin_assume_aligned(row + (in ? col : 0), 16), sizeof(t));
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[j + e] = in ? t[e] : (T)-INFINITY;
         }
     } else {
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            const bool in = on && e0 + j < E;
-            const T t = row[in ? e0 + j : 0];
+            const int col = column_of<LPT, WIDE>(part, j);
+            const bool in = on && col < E;
+            const T t = row[in ? col : 0];
             v[j] = in ? t : (T)-INFINITY;
         }
     }
@@ -155,7 +163,7 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceArgs a) 
     __shared__ uint32_t hits[COLS];
     __shared__ float2 red_s[4];
     __shared__ double red_t[4];
-    const int lane = threadIdx.x & 63, part = lane % LPT, e0 = part * EPL, b = blockIdx.y, E = a.E;
+    const int lane = threadIdx.x & 63, part = lane % LPT, b = blockIdx.y, E = a.E;
     const int size = a.lengths ? max(0, min(a.n, a.lengths[b])) : a.n;
     for (int e = threadIdx.x; e < COLS; e += kThreads) hits[e] = 0;
     if (blockIdx.x == 0 && threadIdx.x == 0 && a.blocks > 1) a.arrived[b] = 0;
@@ -163,7 +171,7 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceArgs a) 
     float sum_p[EPL] = {}, squares = 0.f, count = 0.f;
     const int step = gridDim.x * GRP;
     const auto fetch = [&](int64_t i, T(&v)[EPL]) {
-        load_columns<T, EPL, WIDE>((const T*)a.x.p + b * a.x.sb + i * a.x.sr, e0, E, i < size, v);
+        load_columns<T, LPT, EPL, WIDE>((const T*)a.x.p + b * a.x.sb + i * a.x.sr, part, E, i < size, v);
     };
     int64_t i = (int64_t)blockIdx.x * GRP + threadIdx.x / LPT;
     T next[EPL];
@@ -179,7 +187,8 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceArgs a) 
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             x[j] = (float)v[j];
-            key[j / 8][j % 8] = P::of(x[j], e0 + j, e0 + (WIDE ? j / 8 * 8 : j) < E);
+            const int col = column_of<LPT, WIDE>(part, j);
+            key[j / 8][j % 8] = P::of(x[j], col, (WIDE ? col - j % 8 : col) < E);
             top = fmaxf(top, x[j]);
         }
         top = lanes_max<LPT>(top);
@@ -247,7 +256,7 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceArgs a) 
     const int wave = threadIdx.x >> 6;
     if (lane < LPT) {
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) red_p[wave][e0 + j] = sum_p[j];
+        for (int j = 0; j < EPL; ++j) red_p[wave][column_of<LPT, WIDE>(part, j)] = sum_p[j];
     }
     if (lane == 0) red_s[wave] = make_float2(squares, count);
     __syncthreads();
@@ -342,16 +351,30 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(const BalanceArgs
     constexpr int GRP = kThreads / LPT, SLOTS = (KMAX + LPT - 1) / LPT, COLS = LPT * EPL;
     __shared__ __align__(16) float worth_of[GRP][COLS];
     __shared__ __align__(16) float named_by[GRP][COLS];
-    const int lane = threadIdx.x & 63, part = lane % LPT, e0 = part * EPL, b = blockIdx.y, E = a.E;
+    const int lane = threadIdx.x & 63, part = lane % LPT, b = blockIdx.y, E = a.E;
     const int size = a.lengths ? max(0, min(a.n, a.lengths[b])) : a.n;
     const uint32_t worth = lds_addr(worth_of[threadIdx.x / LPT]);
     const uint32_t named = lds_addr(named_by[threadIdx.x / LPT]);
+    // a lane's columns by fours, the fours of a row's lanes side by side
+    const auto fours = [&](int j) { return (uint32_t)(j / 4 * LPT + part) * 16; };
+    const auto place = [](int col) {
+        const int p = WIDE ? col / 8 % LPT : col % LPT;
+        const int j = WIDE ? col / (8 * LPT) * 8 + col % 8 : col / LPT;
+        return (uint32_t)((j / 4 * LPT + p) * 4 + j % 4) * 4;
+    };
+#pragma unroll
+    for (int j = 0; j < EPL; j += 4) {
+        lds_write<f32x4>(worth + fours(j), f32x4{0, 0, 0, 0});
+        lds_write<f32x4>(named + fours(j), f32x4{0, 0, 0, 0});
+    }
+    asm volatile("" ::: "memory");
     // what every row's probabilities are worth to the balance: E c_e / (k N^2)
     float even[EPL];
     uint32_t sum = 0;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-        const int c = e0 + j < E ? a.counts[(int64_t)b * E + e0 + j] : 0;
+        const int col = column_of<LPT, WIDE>(part, j);
+        const int c = col < E ? a.counts[(int64_t)b * E + col] : 0;
         even[j] = (float)c;
         sum += (uint32_t)c;
     }
@@ -371,7 +394,7 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(const BalanceArgs
         const int64_t row = (int64_t)b * a.n + i;
         const bool in = i < size;
         const int* ids = a.ids + row * a.k;
-        load_columns<T, EPL, WIDE>((const T*)a.x.p + b * a.x.sb + i * a.x.sr, e0, E, in, r.v);
+        load_columns<T, LPT, EPL, WIDE>((const T*)a.x.p + b * a.x.sb + i * a.x.sr, part, E, in, r.v);
         r.first = ids[0];
         r.lse = a.lse[row];
 #pragma unroll
@@ -399,40 +422,36 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(const BalanceArgs
         }
         if (a.ggates) {
             bool have[SLOTS], twice = false;
-#pragma unroll
-            for (int j = 0; j < EPL; j += 4) {
-                lds_write<f32x4>(worth + 4 * (e0 + j), f32x4{0, 0, 0, 0});
-                lds_write<f32x4>(named + 4 * (e0 + j), f32x4{0, 0, 0, 0});
-            }
+            uint32_t at[SLOTS];
 #pragma unroll
             for (int q = 0; q < SLOTS; ++q) {
                 have[q] = on && r.id[q] >= 0 && r.id[q] < E;
-                if (have[q]) lds_write<int>(named + 4 * r.id[q], 1 + q * LPT + part);
+                at[q] = have[q] ? place(r.id[q]) : 0;
+                if (have[q]) lds_write<int>(named + at[q], 1 + q * LPT + part);
             }
             asm volatile("" ::: "memory");
 #pragma unroll
             for (int q = 0; q < SLOTS; ++q)
-                if (have[q]) twice |= lds_read<int>(named + 4 * r.id[q]) != 1 + q * LPT + part;
+                if (have[q]) twice |= lds_read<int>(named + at[q]) != 1 + q * LPT + part;
             asm volatile("" ::: "memory");
             if (!__ballot(twice)) {
 #pragma unroll
                 for (int q = 0; q < SLOTS; ++q)
                     if (have[q]) {
-                        lds_write<float>(worth + 4 * r.id[q], r.g[q]);
-                        lds_write<float>(named + 4 * r.id[q], 1.f);
+                        lds_write<float>(worth + at[q], r.g[q]);
+                        lds_write<float>(named + at[q], 1.f);
                     }
             } else {
 #pragma unroll
-                for (int j = 0; j < EPL; j += 4)
-                    lds_write<f32x4>(named + 4 * (e0 + j), f32x4{0, 0, 0, 0});
+                for (int q = 0; q < SLOTS; ++q)
+                    if (have[q]) lds_write<float>(named + at[q], 0.f);
                 asm volatile("" ::: "memory");
 #pragma unroll
                 for (int q = 0; q < SLOTS; ++q)
                     for (int t = 0; t < LPT; ++t) {
                         if (part == t && have[q]) {
-                            const uint32_t at = 4 * r.id[q];
-                            lds_write<float>(worth + at, lds_read<float>(worth + at) + r.g[q]);
-                            lds_write<float>(named + at, lds_read<float>(named + at) + 1.f);
+                            lds_write<float>(worth + at[q], lds_read<float>(worth + at[q]) + r.g[q]);
+                            lds_write<float>(named + at[q], lds_read<float>(named + at[q]) + 1.f);
                         }
                         asm volatile("" ::: "memory");
                     }
@@ -441,11 +460,19 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(const BalanceArgs
             float dg[EPL], times[EPL], scale = 1.f, shift = 0.f;
 #pragma unroll
             for (int j = 0; j < EPL; j += 4) {
-                const f32x4 x = lds_read<f32x4>(worth + 4 * (e0 + j));
-                const f32x4 y = lds_read<f32x4>(named + 4 * (e0 + j));
+                const f32x4 x = lds_read<f32x4>(worth + fours(j));
+                const f32x4 y = lds_read<f32x4>(named + fours(j));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) dg[j + e] = x[e], times[j + e] = y[e];
             }
+            asm volatile("" ::: "memory");
+            // zeros again for the next row
+#pragma unroll
+            for (int q = 0; q < SLOTS; ++q)
+                if (have[q]) {
+                    lds_write<float>(worth + at[q], 0.f);
+                    lds_write<float>(named + at[q], 0.f);
+                }
             asm volatile("" ::: "memory");
             if (a.normalize) {
                 float chosen = 0.f, mid = 0.f;
@@ -472,13 +499,17 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(const BalanceArgs
         for (int j = 0; j < EPL; ++j) r.v[j] = (T)(on ? p[j] * (dp[j] - mean) : 0.f);
         if constexpr (WIDE) {
 #pragma unroll
-            for (int j = 0; j < EPL; j += 8)
-                if (e0 + j < E)
-                    __builtin_memcpy(__builtin_assume_aligned(gx + e0 + j, 16), r.v + j, 8 * sizeof(T));
+            for (int j = 0; j < EPL; j += 8) {
+                const int col = column_of<LPT, WIDE>(part, j);
+                if (col < E)
+                    __builtin_memcpy(__builtin_assume_aligned(gx + col, 16), r.v + j, 8 * sizeof(T));
+            }
         } else {
 #pragma unroll
-            for (int j = 0; j < EPL; ++j)
-                if (e0 + j < E) gx[e0 + j] = r.v[j];
+            for (int j = 0; j < EPL; ++j) {
+                const int col = column_of<LPT, WIDE>(part, j);
+                if (col < E) gx[col] = r.v[j];
+            }
         }
     }
 }

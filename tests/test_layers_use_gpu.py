@@ -390,9 +390,9 @@ def test_binding_refuses(fs):
         fs.fs_quantized_product(q, v[:3].clone(), q, v[:3].clone(),
                                 torch.zeros(3, 3, device="cuda", dtype=I4))
     with pytest.raises(fs.FsError, match="workspace"):
-        big = torch.zeros(300, 64, device="cuda", dtype=torch.int8)[:, :33]
-        s = torch.zeros(300, device="cuda")
-        fs.fs_quantized_product(big, s, big, s, torch.zeros(300, 300, device="cuda"),
+        big = torch.zeros(1800, 64, device="cuda", dtype=torch.int8)[:, :33]
+        s = torch.zeros(1800, device="cuda")
+        fs.fs_quantized_product(big, s, big, s, torch.zeros(1800, 1800, device="cuda"),
                                 workspace=torch.zeros(512, device="cuda", dtype=torch.uint8))
     t = torch.zeros(3, 2, device="cuda")
     with pytest.raises(fs.FsError, match="both or neither"):
