@@ -168,7 +168,7 @@ fs_status fs_distill_loss_backward(const fs_distill_desc* desc, fs_rows logits, 
  * 0.  The columns chosen have no gradient. */
 typedef struct {
     int32_t dtype;           /* fs_dtype of the logits and their gradient */
-    int32_t batch, n;        /* >= 0; batch <= 65535, batch * n <= 2^31 - 1 */
+    int32_t batch, n;        /* >= 0; batch <= 65535, batch * n and n * k <= 2^31 - 1 */
     int32_t experts;         /* 1..1024 */
     int32_t k;               /* 1..min(32, experts) */
     int32_t normalize;

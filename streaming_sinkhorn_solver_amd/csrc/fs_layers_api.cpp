@@ -457,6 +457,8 @@ fs_status take_balance(const fs_balance_desc* p, BalanceArgs& a) {
     if (d.k < 1 || d.k > std::min(kBalanceMaxTop, d.experts))
         return fail(FS_ERR_INVALID_ARG, "k must be in [1, min(%d, experts)] (got %d)",
                     kBalanceMaxTop, d.k);
+    if ((int64_t)d.n * d.k > 0x7fffffff)
+        return fail(FS_ERR_INVALID_ARG, "n * k must be below 2^31 (got %d, %d)", d.n, d.k);
     a.op = op_of(d.dtype);
     a.B = d.batch;
     a.n = d.n;

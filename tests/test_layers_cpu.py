@@ -206,7 +206,7 @@ def balance_back(lib, ids=A[1], counts=A[3], lse=A[5], g=A[4], gg=A[2], gx=None,
     (dict(dtype=3), "fs_dtype"), (dict(batch=-1), "batch"), (dict(batch=65536), "batch"),
     (dict(batch=65535, n=1 << 20), "2^31"), (dict(experts=0), "experts"),
     (dict(experts=1025), "experts"), (dict(k=0), "k must"), (dict(k=9), "k must"),
-    (dict(experts=64, k=33), "k must")], ids=str)
+    (dict(experts=64, k=33), "k must"), (dict(batch=1, n=1 << 30, k=2), "n * k")], ids=str)
 def test_balance_bad_sizes(lib, kw, word):
     refused(lib, balance(lib, **kw), word)
     refused(lib, balance_back(lib, **kw), word)
