@@ -165,7 +165,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void product_rows_kernel(const Prod
     const auto state = [&](int b) { return Row(a.x + (int64_t)min(16 * b + r, a.m - 1) * a.sx); };
     i32x4 acc[CB][RB] = {};
     // whole steps of 64 k: reads that ask nothing, U of them under way together
-    constexpr int U = RB * CB == 1 ? 8 : RB * CB == 2 ? 4 : 2;
+    constexpr int U = RB * CB <= 2 ? 8 : 2;
     const int whole = a.k / 64;
     int t = wave;
     for (; t + kRowWaves * (U - 1) < whole; t += kRowWaves * U) {
@@ -471,12 +471,24 @@ int tile_of(int m, int n) {
     return tiles_of(m, n, 256) >= 192 ? 256 : tiles_of(m, n, 128) >= 192 ? 128 : 64;
 }
 
+// Two blocks of columns a workgroup where that leaves 256 workgroups: the rows' bytes,
+// which each of them reads anew from L2, count as the columns' do (us, one / two: 16
+// x 8192 x 4096, 10.9 / 9.9; 8 x 32768 x 4096, 34.9 / 32.5; 32 x 32768 x 4096, 53.9 /
+// 42.1; but 1 x 32768 x 4096, 29.9 / 31.7, 8 x 4096 x 16384, 17.8 / 25.0, and 32 x 4096 x
+// 4096, 8.7 / 9.8).
 template <int OP, bool DWORDS>
 hipError_t rows(const ProductArgs& a, hipStream_t s) {
-    if (a.m <= 16)
-        product_rows_kernel<OP, 1, 1, DWORDS><<<(unsigned)((a.n + 15) / 16), 64 * kRowWaves, 0, s>>>(a);
+    constexpr int T = 64 * kRowWaves;
+    const unsigned one = (unsigned)((a.n + 15) / 16), two = (unsigned)((a.n + 31) / 32);
+    const bool wide = a.n >= 8192 && a.m > 4;
+    if (a.m <= 16 && wide)
+        product_rows_kernel<OP, 1, 2, DWORDS><<<two, T, 0, s>>>(a);
+    else if (a.m <= 16)
+        product_rows_kernel<OP, 1, 1, DWORDS><<<one, T, 0, s>>>(a);
+    else if (wide)
+        product_rows_kernel<OP, 2, 2, DWORDS><<<two, T, 0, s>>>(a);
     else
-        product_rows_kernel<OP, 2, 2, DWORDS><<<(unsigned)((a.n + 31) / 32), 64 * kRowWaves, 0, s>>>(a);
+        product_rows_kernel<OP, 2, 1, DWORDS><<<one, T, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -44,7 +44,7 @@ def test_quantize_forms(fs, dtype):
 # m, n, k: few rows (one and two blocks of 16, from dwords on and not), tiles of 64
 # (ranges of k), 128 (four and two buffers) and 256, laid out first and not
 PRODUCTS = [(16, 40, 64), (16, 40, 1000), (5, 40, 1001), (32, 70, 2048), (20, 70, 2047),
-            (8, 48, 4096), (33, 64, 128), (64, 64, 4096), (40, 80, 8193), (1700, 1800, 256),
+            (8, 48, 4096), (8, 8200, 640), (16, 8193, 1003), (32, 8195, 700), (20, 8192, 129), (33, 64, 128), (64, 64, 4096), (40, 80, 8193), (1700, 1800, 256),
             (1700, 1801, 250), (2100, 2200, 144), (3500, 3600, 272), (3500, 3601, 257),
             (70, 90, 16), (70, 90, 1)]
 
