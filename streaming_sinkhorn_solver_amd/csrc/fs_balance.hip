@@ -6,7 +6,10 @@
 //   dx = p (dp - sum p dp + dL1 2 lse / N).
 // A row's columns lie with LPT lanes.  Sums over columns run in the
 // lanes' registers over a workgroup's rows, then over workgroups in a second
-// launch (in 64 bits, in a fixed order).
+// launch (in 64 bits, in a fixed order).  (65536 rows of 256 columns, 8 chosen, bf16:
+// forward 20.7 us for 38 MB and 6.5 for the join, backward 23 us for 71 MB; bound by
+// the vector unit: 590 instructions for four rows forward, 385 backward, which issue
+// in 15 and 10 us.)
 #include "fs_layers_args.h"
 #include "fs_rowops.hpp"
 

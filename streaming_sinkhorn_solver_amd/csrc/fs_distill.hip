@@ -5,8 +5,13 @@
 //   dx_c = dloss T (W p_c - sum_{id = c} tau).
 // Bound by memory.  A workgroup reads its row (or its range of one) once and keeps
 // it in registers over the row's maximum, sum and gradient; rows that are too long
-// for that are read a second time for the gradient.  Where rows are few, several
-// workgroups share one and meet in a second launch.
+// for that are read a second time, in part, for the gradient.  Where rows are few,
+// several workgroups share one and meet in a second launch.  (Loss and gradient of
+// 4096 x 131072, bf16: 463 us for 2.15 GB of logits read and gradient written, 4.6
+// TB/s, half of each row read twice; 4096 x 65536: 210 us.  With nothing kept it took
+// 668 us: the rows of eight workgroups a CU push one another out of the caches.  With
+// all of a row kept it took 799: one workgroup a CU, whose reads, exponentials and
+// writes take turns.)
 #include "fs_layers_args.h"
 #include "fs_rowops.hpp"
 

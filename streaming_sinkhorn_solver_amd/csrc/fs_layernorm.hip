@@ -4,7 +4,11 @@
 //   u = w g,  dx = rstd (u - mean u - h mean(u h)) + dz,  dw = sum g h,  db = sum g.
 // Bound by memory: a row is read once and stays in registers over both sums of
 // its statistics (the second is of squared distances from the mean, so that a
-// large mean costs no digits).
+// large mean costs no digits).  Up to 512 elements a row lies with 8 to 64 lanes
+// of a wave, whose sums need no barrier, beyond with a workgroup.  (16384 rows of
+// 4096, bf16, with the residual: forward 90 us for 537 MB, 6.0 TB/s; backward 116
+// us for 537 MB, 4.6 TB/s, and 5 us for the weights' sums; a large copy reaches
+// 4.9 TB/s.  32 rows of 4096: 3.7 us.)
 #include "fs_layers_args.h"
 #include "fs_rowops.hpp"
 
@@ -121,7 +125,7 @@ __global__ __launch_bounds__(threads_of<LPR>()) void layer_norm_bwd_kernel(const
     const int64_t rows = (int64_t)a.B * a.n, step = (int64_t)gridDim.x * GRP;
     // A row's three reads are issued while the row in front of it is worked on: two
     // workgroups a CU (whose parts of the sums are few then) would leave memory idle
-    // over each row's latency (16384 rows of 4096, bf16: 179 us without, LN_PRE with).
+    // over each row's latency (16384 rows of 4096, bf16: 179 us without, 116 with).
     struct Row {
         Share<T, LPR, CH, WIDE> z, g, t;
         float mean, rstd;
@@ -268,6 +272,7 @@ hipError_t launch(const LayerNormArgs& a, bool back, hipStream_t s) {
 
 }  // namespace
 
+// Workgroups of the backward pass: two a CU.  Each leaves 2 x width sums to add up.
 int layer_norm_bwd_blocks(int64_t rows, int width) {
     const int grp = width <= 64 ? 32 : width <= 128 ? 16 : width <= 256 ? 8 : width <= 1024 ? 4 : 1;
     const int64_t b = (rows + grp - 1) / grp;

@@ -2,6 +2,9 @@
 // of two such sets:
 //   a = max |x|, q = 127 x / a to the nearest whole number, scale = a / 127;
 //   y_ij = scale_i scale'_j sum_k q_ik q'_jk + b_j, the sum exact in 32 bits.
+// (8192 rows of 8192, bf16: 45 to 50 us for 201 MB, 4.0 to 4.5 TB/s; the product of two
+// such sets 503 to 547 us, 2010 to 2190 TOP/s, where the library's 8-bit product took 515
+// to 547 on the same cards; 8 rows against 8192 of 4096, 9 us for 34 MB.)
 #include "fs_layers_args.h"
 #include "fs_rowops.hpp"
 
@@ -253,7 +256,11 @@ __global__ __launch_bounds__(256) void product_pack_kernel(const ProductArgs a) 
 // the matrix units work on one, the next one or two steps' rows are on their way.
 // The 16-byte chunks of a row of 128 bytes stand in an order that depends on its
 // number, so that 16 lanes reading one chunk of 16 rows use all banks.  WM x WN
-// waves.
+// waves.  Bound, for tiles of 256, by the matrix units at the clock that is left: at
+// 8192^3 their pipes are busy in half of the cycles, at 1.9 GHz, and LDS serves its
+// 128 bytes a cycle for nearly as long (eight waves of 128 x 64 read 192 KB a step of
+// 2048 cycles and 64 KB come in; four of 128 x 128, which read 128 KB, have nobody to
+// hide their waits: 577 us against 524).
 template <int BM, int BN, int WM, int WN, int STAGES>
 struct Tile {
     static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
