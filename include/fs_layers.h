@@ -127,7 +127,8 @@ fs_status fs_quantized_product(const fs_quantized_product_desc* desc, void* work
  * whatever they hold.  Rows without an entry, of -inf alone, or not active have
  * loss 0 and a gradient of zeros; lse of rows that are not active is 0 (of a row
  * of -inf alone: -inf).  Where d_loss is 0 the gradient is zeros.  A class of the
- * teacher's whose logit is -inf makes the loss infinite, not the gradient. */
+ * teacher's whose logit is -inf makes the loss infinite, not the gradient.  A NaN or
+ * an infinite logit else makes its own row's loss, lse and gradient NaN. */
 typedef struct {
     int32_t dtype;            /* fs_dtype of the logits and their gradient */
     int32_t rows;             /* >= 0 */
@@ -165,7 +166,8 @@ fs_status fs_distill_loss_backward(const fs_distill_desc* desc, fs_rows logits, 
  *   gates_ij = p[ids_ij], over the row's sum of them if normalize.
  * Rows i >= lengths[b] (never read, whatever they hold) and rows of -inf alone
  * take no part: ids -1, gates and lse 0.  Where no row takes part the losses are
- * 0.  The columns chosen have no gradient. */
+ * 0.  The columns chosen have no gradient.  A NaN or +inf among a row's logits makes
+ * its gates and its gradient NaN, and its batch entry's losses. */
 typedef struct {
     int32_t dtype;           /* fs_dtype of the logits and their gradient */
     int32_t batch, n;        /* >= 0; batch <= 65535, batch * n and n * k <= 2^31 - 1 */

@@ -865,11 +865,14 @@ def _work(workspace: Optional[torch.Tensor], size, like: torch.Tensor, dev: int,
 
 # the current stream's handle without the objects around it, where torch has it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# the current device's number without torch.cuda's check that it is set up (which
+# it is where a device tensor was given)
+_current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(fn, where: str, dev: int, stream, *args):
     """fn(*args, stream handle) with device dev current."""
-    if torch.cuda.current_device() == dev:
+    if _current() == dev:
         st = fn(*args, _raw_stream(dev) if stream is None and _raw_stream else _stream(stream))
     else:
         with torch.cuda.device(dev):
@@ -1129,12 +1132,6 @@ def _matrix8(t: torch.Tensor, name: str, dev: int, shape):
     return t.data_ptr(), t.stride(0)
 
 
-def _need(t, name: str):
-    if t is None:
-        raise TypeError(f"{name} must be given")
-    return t
-
-
 def _layer_norm_desc(x, name, eps, lengths):
     """The description and the device's number."""
     dtype = _dtype_of(x, name)
@@ -1170,7 +1167,7 @@ def fs_layer_norm(x: torch.Tensor, weight, bias, y: torch.Tensor, *, residual=No
     return _call(lib.fs_layer_norm, "fs_layer_norm", dev, stream, ctypes.byref(a),
                  _states(x, "x", x, dev, xs), _states(residual, "residual", x, dev, xs),
                  _flat(weight, "weight", dev, f32, w), _flat(bias, "bias", dev, f32, w),
-                 _states(total, "total", x, dev, xs), _states(_need(y, "y"), "y", x, dev, xs),
+                 _states(total, "total", x, dev, xs), _states(y, "y", x, dev, xs),
                  _flat(mean, "mean", dev, f32, rows), _flat(rstd, "rstd", dev, f32, rows))
 
 
@@ -1189,11 +1186,11 @@ def fs_layer_norm_backward(z: torch.Tensor, weight, mean, rstd, d_y, d_x, d_weig
     w, rows = zs[2:], zs[:2]
     return _call(lib.fs_layer_norm_backward, "fs_layer_norm_backward", dev, stream, pa,
                  _states(z, "z", z, dev, zs), _flat(weight, "weight", dev, f32, w),
-                 _flat(_need(mean, "mean"), "mean", dev, f32, rows),
-                 _flat(_need(rstd, "rstd"), "rstd", dev, f32, rows),
-                 _states(_need(d_y, "d_y"), "d_y", z, dev, zs),
+                 _flat(mean, "mean", dev, f32, rows),
+                 _flat(rstd, "rstd", dev, f32, rows),
+                 _states(d_y, "d_y", z, dev, zs),
                  _states(d_total, "d_total", z, dev, zs),
-                 _states(_need(d_x, "d_x"), "d_x", z, dev, zs),
+                 _states(d_x, "d_x", z, dev, zs),
                  _flat(d_weight, "d_weight", dev, f32, w), _flat(d_bias, "d_bias", dev, f32, w), ws,
                  size)
 
@@ -1211,7 +1208,7 @@ def fs_quantize_rows(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, *, s
     X = _states(x, "x", x, dev, x.shape)
     qp, qs = _matrix8(q, "q", dev, x.shape)
     return _call(load().fs_quantize_rows, "fs_quantize_rows", dev, stream, dtype, rows, width, X.data,
-                 X.stride_row, qp, qs, _flat(_need(scale, "scale"), "scale", dev, torch.float32,
+                 X.stride_row, qp, qs, _flat(scale, "scale", dev, torch.float32,
                                              (rows,)))
 
 
@@ -1242,8 +1239,8 @@ def fs_quantized_product(q_x: torch.Tensor, scale_x: torch.Tensor, q_w: torch.Te
     xp, xs = _matrix8(q_x, "q_x", dev, (m, k))
     wp, ws_ = _matrix8(q_w, "q_w", dev, (n, k))
     a = QuantizedProductDesc(dtype, m, n, k, xp, xs,
-                             _flat(_need(scale_x, "scale_x"), "scale_x", dev, f32, (m,)), wp, ws_,
-                             _flat(_need(scale_w, "scale_w"), "scale_w", dev, f32, (n,)),
+                             _flat(scale_x, "scale_x", dev, f32, (m,)), wp, ws_,
+                             _flat(scale_w, "scale_w", dev, f32, (n,)),
                              _flat(bias, "bias", dev, f32, (n,)), Y.data, Y.stride_row)
     pa = ctypes.byref(a)
     ws, size, _keep = _work(workspace, lambda: _needed(lib.fs_quantized_product_workspace_bytes,
@@ -1265,7 +1262,7 @@ def _distill_desc(logits, ids, teacher, temperature, teacher_lse, active):
     dev = logits.get_device()
     a = DistillDesc(dtype, rows, classes, k, temperature,
                     _flat(ids, "ids", dev, torch.int32, (rows, k)),
-                    _flat(_need(teacher, "teacher"), "teacher", dev, torch.float32, (rows, k)),
+                    _flat(teacher, "teacher", dev, torch.float32, (rows, k)),
                     _flat(teacher_lse, "teacher_lse", dev, torch.float32, (rows,)))
     if active is not None:
         _on(active, "active", dev)
@@ -1303,8 +1300,8 @@ def fs_distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tens
     rows = xs[:1]
     return _call(lib.fs_distill_loss, "fs_distill_loss", dev, stream, pa,
                  _states(logits, "logits", logits, dev, xs),
-                 _flat(_need(loss, "loss"), "loss", dev, f32, rows),
-                 _flat(_need(lse, "lse"), "lse", dev, f32, rows),
+                 _flat(loss, "loss", dev, f32, rows),
+                 _flat(lse, "lse", dev, f32, rows),
                  _flat(d_loss, "d_loss", dev, f32, rows),
                  _states(d_logits, "d_logits", logits, dev, xs), ws, size)
 
@@ -1318,9 +1315,9 @@ def fs_distill_loss_backward(logits: torch.Tensor, ids: torch.Tensor, teacher: t
     rows = xs[:1]
     return _call(load().fs_distill_loss_backward, "fs_distill_loss_backward", dev, stream,
                  ctypes.byref(a), _states(logits, "logits", logits, dev, xs),
-                 _flat(_need(lse, "lse"), "lse", dev, f32, rows),
-                 _flat(_need(d_loss, "d_loss"), "d_loss", dev, f32, rows),
-                 _states(_need(d_logits, "d_logits"), "d_logits", logits, dev, xs))
+                 _flat(lse, "lse", dev, f32, rows),
+                 _flat(d_loss, "d_loss", dev, f32, rows),
+                 _states(d_logits, "d_logits", logits, dev, xs))
 
 
 def _balance_desc(logits, k, normalize, lengths):
@@ -1364,10 +1361,10 @@ def fs_balance_loss(logits: torch.Tensor, ids: torch.Tensor, gates: torch.Tensor
     each = (batch, n, a.k)
     return _call(lib.fs_balance_loss, "fs_balance_loss", dev, stream, pa,
                  _states(logits, "logits", logits, dev, xs), _flat(ids, "ids", dev, i32, each),
-                 _flat(_need(gates, "gates"), "gates", dev, f32, each),
-                 _flat(_need(counts, "counts"), "counts", dev, i32, (batch, experts)),
-                 _flat(_need(loss, "loss"), "loss", dev, f32, (batch, 2)),
-                 _flat(_need(lse, "lse"), "lse", dev, f32, (batch, n)), ws, size)
+                 _flat(gates, "gates", dev, f32, each),
+                 _flat(counts, "counts", dev, i32, (batch, experts)),
+                 _flat(loss, "loss", dev, f32, (batch, 2)),
+                 _flat(lse, "lse", dev, f32, (batch, n)), ws, size)
 
 
 def fs_balance_loss_backward(logits: torch.Tensor, ids: torch.Tensor, counts: torch.Tensor,
@@ -1384,8 +1381,8 @@ def fs_balance_loss_backward(logits: torch.Tensor, ids: torch.Tensor, counts: to
     return _call(load().fs_balance_loss_backward, "fs_balance_loss_backward", dev, stream,
                  ctypes.byref(a), _states(logits, "logits", logits, dev, xs),
                  _flat(ids, "ids", dev, i32, each),
-                 _flat(_need(counts, "counts"), "counts", dev, i32, (batch, experts)),
-                 _flat(_need(lse, "lse"), "lse", dev, f32, (batch, n)),
-                 _flat(_need(d_loss, "d_loss"), "d_loss", dev, f32, (batch, 2)),
+                 _flat(counts, "counts", dev, i32, (batch, experts)),
+                 _flat(lse, "lse", dev, f32, (batch, n)),
+                 _flat(d_loss, "d_loss", dev, f32, (batch, 2)),
                  _flat(d_gates, "d_gates", dev, f32, each),
-                 _states(_need(d_logits, "d_logits"), "d_logits", logits, dev, xs))
+                 _states(d_logits, "d_logits", logits, dev, xs))

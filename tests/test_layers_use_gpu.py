@@ -363,7 +363,7 @@ def test_binding_refuses(fs):
     st = torch.zeros(2, 3, device="cuda")
     with pytest.raises(TypeError, match="float32"):
         fs.fs_layer_norm(x, v.to(BF), None, x.clone())
-    with pytest.raises(TypeError, match="y must be given"):
+    with pytest.raises(fs.FsError, match="y must be non-NULL"):
         fs.fs_layer_norm(x, v, None, None)
     with pytest.raises(TypeError, match="as the others"):
         fs.fs_layer_norm(x, v, None, x.float())
@@ -373,7 +373,7 @@ def test_binding_refuses(fs):
         fs.fs_layer_norm(x.transpose(1, 2).contiguous().transpose(1, 2), v, None, x.clone())
     with pytest.raises(fs.FsError, match="overlaps"):
         fs.fs_layer_norm(x, v, None, x)
-    with pytest.raises(TypeError, match="mean must be given"):
+    with pytest.raises(fs.FsError, match="mean must be non-NULL"):
         fs.fs_layer_norm_backward(x, v, None, st, x.clone(), x.clone())
     with pytest.raises(TypeError, match="device tensor"):
         fs.fs_layer_norm(x, v.cpu(), None, x.clone())
