@@ -261,7 +261,7 @@ hipError_t launch(const LayerNormArgs& a, bool back, hipStream_t s) {
     if (a.width <= 1024) return launch<OP, 64, 2>(a, back, s);
     if (a.width <= 2048) return launch<OP, 256, 1>(a, back, s);
     if (a.width <= 4096) return launch<OP, 256, 2>(a, back, s);
-    if (a.width <= 8192) return launch<OP, 256, 4>(a, back, s);
+    if (a.width <= 8192) return launch<OP, 512, 2>(a, back, s);
     return launch<OP, 1024, 2>(a, back, s);
 }
 hipError_t launch(const LayerNormArgs& a, bool back, hipStream_t s) {
@@ -272,11 +272,14 @@ hipError_t launch(const LayerNormArgs& a, bool back, hipStream_t s) {
 
 }  // namespace
 
-// Workgroups of the backward pass: two a CU.  Each leaves 2 x width sums to add up.
+// Workgroups of the backward pass: two a CU (of 1024 threads one), each of which
+// leaves 2 x width sums to add up (us, 256 / 512 workgroups: 4096 rows of 16384, bf16,
+// 137 / 155; 16384 rows of 4096, 151 / 119).
 int layer_norm_bwd_blocks(int64_t rows, int width) {
     const int grp = width <= 64 ? 32 : width <= 128 ? 16 : width <= 256 ? 8 : width <= 1024 ? 4 : 1;
     const int64_t b = (rows + grp - 1) / grp;
-    return b < 1 ? 1 : b > 512 ? 512 : (int)b;
+    const int most = width > 8192 ? 256 : 512;
+    return b < 1 ? 1 : b > most ? most : (int)b;
 }
 
 hipError_t launch_layer_norm(const LayerNormArgs& a, hipStream_t s) { return launch(a, false, s); }
