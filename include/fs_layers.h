@@ -16,8 +16,8 @@
  *    given as fs_rows (fs_attention.h) of one head: a [batch][rows][width] view
  *    whose last axis is contiguous and whose other strides (in elements) are
  *    free; stride_head is not looked at.  Views whose rows are 16-byte aligned
- *    with a width of whole 16-byte chunks are read with wide loads, others
- *    element by element.  Arrays given by plain pointers are contiguous.  Outputs
+ *    with a width of whole 16-byte chunks are read with wide loads (the layer
+ *    norm's also where they start at whole dwords), others element by element.  Arrays given by plain pointers are contiguous.  Outputs
  *    may not overlap themselves, one another, an input or the workspace (slices
  *    of one buffer side by side do not overlap; against an input whole extents
  *    count).

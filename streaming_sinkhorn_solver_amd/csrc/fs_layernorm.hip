@@ -4,7 +4,7 @@
 //   u = w g,  dx = rstd (u - mean u - h mean(u h)) + dz,  dw = sum g h,  db = sum g.
 // Bound by memory: a row is read once and stays in registers over both sums of
 // its statistics (the second is of squared distances from the mean, so that a
-// large mean costs no digits).  Up to 512 elements a row lies with 8 to 64 lanes
+// large mean costs no digits).  Up to 1024 elements a row lies with 8 to 64 lanes
 // of a wave, whose sums need no barrier, beyond with a workgroup.  (16384 rows of
 // 4096, bf16, with the residual: forward 90 us for 537 MB, 6.0 TB/s; backward 116
 // us for 537 MB, 4.6 TB/s, and 5 us for the weights' sums; a large copy reaches
@@ -32,11 +32,11 @@ __device__ __forceinline__ bool row_on(const LayerNormArgs& a, int b, int i) {
     return !a.lengths || i < a.lengths[b];
 }
 
-template <int LPR, int CH, bool WIDE>
+template <int LPR, int CH, ShareForm FORM>
 __device__ __forceinline__ void load_weight(const float* w, int lane, int width, float fill,
                                             float (&out)[CH][8]) {
     if (w) {
-        Share<float, LPR, CH, WIDE> s;
+        Share<float, LPR, CH, FORM> s;
         s.load(w, lane, width, true);
         __builtin_memcpy(out, s.v, sizeof(out));
         return;
@@ -47,7 +47,7 @@ __device__ __forceinline__ void load_weight(const float* w, int lane, int width,
         for (int e = 0; e < 8; ++e) out[j][e] = fill;
 }
 
-template <int OP, int LPR, int CH, bool WIDE>
+template <int OP, int LPR, int CH, ShareForm FORM>
 __global__ __launch_bounds__(threads_of<LPR>()) void layer_norm_kernel(const LayerNormArgs a) {
     using T = typename El<OP>::T;
     constexpr int GRP = threads_of<LPR>() / LPR;
@@ -55,8 +55,8 @@ __global__ __launch_bounds__(threads_of<LPR>()) void layer_norm_kernel(const Lay
     RowFold<LPR> fold(buf);
     const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR, W = a.width;
     float w[CH][8], bias[CH][8];
-    load_weight<LPR, CH, WIDE>(a.w, lane, W, 1.f, w);
-    load_weight<LPR, CH, WIDE>(a.b, lane, W, 0.f, bias);
+    load_weight<LPR, CH, FORM>(a.w, lane, W, 1.f, w);
+    load_weight<LPR, CH, FORM>(a.b, lane, W, 0.f, bias);
     const float inv_w = 1.f / (float)W;
     const int64_t rows = (int64_t)a.B * a.n;
     // (the groups of a workgroup leave the loop together: its sums have barriers)
@@ -66,7 +66,7 @@ __global__ __launch_bounds__(threads_of<LPR>()) void layer_norm_kernel(const Lay
         int b, i;
         place(a, row, b, i);
         const bool on = row_on(a, b, i);
-        Share<T, LPR, CH, WIDE> x, r;
+        Share<T, LPR, CH, FORM> x, r;
         x.load((const T*)a.x.p + b * a.x.sb + i * a.x.sr, lane, W, on);
         float z[CH][8];
         if (a.r.p) {
@@ -88,7 +88,7 @@ __global__ __launch_bounds__(threads_of<LPR>()) void layer_norm_kernel(const Lay
         for (int j = 0; j < CH; ++j)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                z[j][e] = share_at<LPR, WIDE>(lane, j, e) < W ? z[j][e] - mean : 0.f;
+                z[j][e] = share_at<LPR, FORM>(lane, j, e) < W ? z[j][e] - mean : 0.f;
                 q = fmaf(z[j][e], z[j][e], q);
             }
         q = fold.sum(q);
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(threads_of<LPR>()) void layer_norm_kernel(const Lay
 // Backward: a workgroup takes rows in steps of the grid; a thread's columns are
 // the same in every row, so the weights' gradients are summed in its registers,
 // over the workgroup's rows in LDS, and over workgroups by layer_norm_sum_kernel.
-template <int OP, int LPR, int CH, bool WIDE>
+template <int OP, int LPR, int CH, ShareForm FORM>
 __global__ __launch_bounds__(threads_of<LPR>()) void layer_norm_bwd_kernel(const LayerNormArgs a) {
     using T = typename El<OP>::T;
     constexpr int GRP = threads_of<LPR>() / LPR;
@@ -116,7 +116,7 @@ __global__ __launch_bounds__(threads_of<LPR>()) void layer_norm_bwd_kernel(const
     RowFold<LPR> fold(buf);
     const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR, W = a.width;
     float w[CH][8], dw[CH][8], db[CH][8];
-    load_weight<LPR, CH, WIDE>(a.w, lane, W, 1.f, w);
+    load_weight<LPR, CH, FORM>(a.w, lane, W, 1.f, w);
 #pragma unroll
     for (int j = 0; j < CH; ++j)
 #pragma unroll
@@ -127,7 +127,7 @@ __global__ __launch_bounds__(threads_of<LPR>()) void layer_norm_bwd_kernel(const
     // workgroups a CU (whose parts of the sums are few then) would leave memory idle
     // over each row's latency (16384 rows of 4096, bf16: 179 us without, 116 with).
     struct Row {
-        Share<T, LPR, CH, WIDE> z, g, t;
+        Share<T, LPR, CH, FORM> z, g, t;
         float mean, rstd;
         int b, i;
         bool on;
@@ -187,7 +187,7 @@ __global__ __launch_bounds__(threads_of<LPR>()) void layer_norm_bwd_kernel(const
         for (int j = 0; j < CH; ++j)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int at = share_at<LPR, WIDE>(lane, j, e);
+                const int at = share_at<LPR, FORM>(lane, j, e);
                 if (at < W) part[at] = dw[j][e], part[W + at] = db[j][e];
             }
     } else {
@@ -196,7 +196,7 @@ __global__ __launch_bounds__(threads_of<LPR>()) void layer_norm_bwd_kernel(const
         for (int j = 0; j < CH; ++j)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int at = share_at<LPR, WIDE>(lane, j, e);
+                const int at = share_at<LPR, FORM>(lane, j, e);
                 red[grp * C + at] = dw[j][e];
                 red[(GRP + grp) * C + at] = db[j][e];
             }
@@ -237,20 +237,22 @@ __global__ __launch_bounds__(1024) void layer_norm_sum_kernel(const LayerNormArg
     }
 }
 
-template <int OP, int LPR, int CH, bool WIDE>
+template <int OP, int LPR, int CH, ShareForm FORM>
 hipError_t launch(const LayerNormArgs& a, bool back, hipStream_t s) {
     constexpr int GRP = threads_of<LPR>() / LPR;
     const int64_t groups = ((int64_t)a.B * a.n + GRP - 1) / GRP;
     if (back)
-        layer_norm_bwd_kernel<OP, LPR, CH, WIDE><<<(unsigned)a.blocks, threads_of<LPR>(), 0, s>>>(a);
+        layer_norm_bwd_kernel<OP, LPR, CH, FORM><<<(unsigned)a.blocks, threads_of<LPR>(), 0, s>>>(a);
     else
-        layer_norm_kernel<OP, LPR, CH, WIDE>
+        layer_norm_kernel<OP, LPR, CH, FORM>
             <<<(unsigned)(groups < 4096 ? groups : 4096), threads_of<LPR>(), 0, s>>>(a);
     return hipGetLastError();
 }
 template <int OP, int LPR, int CH>
 hipError_t launch(const LayerNormArgs& a, bool back, hipStream_t s) {
-    return a.wide ? launch<OP, LPR, CH, true>(a, back, s) : launch<OP, LPR, CH, false>(a, back, s);
+    return a.form == WIDE     ? launch<OP, LPR, CH, WIDE>(a, back, s)
+           : a.form == DWORDS ? launch<OP, LPR, CH, DWORDS>(a, back, s)
+                              : launch<OP, LPR, CH, SINGLE>(a, back, s);
 }
 template <int OP>
 hipError_t launch(const LayerNormArgs& a, bool back, hipStream_t s) {

@@ -17,9 +17,13 @@ constexpr int kDistillMaxSplit = 64;
 constexpr int kBalanceMaxExperts = 1024;
 constexpr int kBalanceMaxTop = 32;
 
+// How a row's elements are read and written (Share in fs_rowops.hpp).
+enum ShareForm : int { SINGLE, WIDE, DWORDS };
+
 // Layer norm.  Where nothing tells the batch's entries apart they are one.
 struct LayerNormArgs {
-    int op, B, n, width, wide;  // wide: rows of whole 8-element groups, all 16-byte aligned
+    int op, B, n, width;
+    int form;  // ShareForm: how all of its rows may be read
     float eps;
     const int* lengths;
     AttnView x, r, z, y;     // forward: in, residual, their sum, out (r, z: p NULL for none)

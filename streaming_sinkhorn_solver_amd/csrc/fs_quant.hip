@@ -45,7 +45,7 @@ constexpr int threads_of() {
 }
 
 // Bound by memory: a row is read once and stays in registers over its maximum.
-template <int OP, int LPR, int CH, bool WIDE>
+template <int OP, int LPR, int CH, bool WIDE_ROWS>
 __global__ __launch_bounds__(threads_of<LPR>()) void quantize_kernel(const QuantArgs a) {
     using T = typename El<OP>::T;
     constexpr int GRP = threads_of<LPR>() / LPR;
@@ -54,7 +54,7 @@ __global__ __launch_bounds__(threads_of<LPR>()) void quantize_kernel(const Quant
     const int lane = threadIdx.x % LPR, W = a.width;
     const int64_t row = flat_block() * GRP + threadIdx.x / LPR;
     if (row >= a.rows) return;  // (LPR > 64: the whole workgroup)
-    Share<T, LPR, CH, WIDE> x;
+    Share<T, LPR, CH, WIDE_ROWS ? WIDE : SINGLE> x;
     x.load((const T*)a.x + row * a.sx, lane, W, true);
     // magnitudes compare as their bits do, NaN above infinity
     uint32_t top = 0;
@@ -73,13 +73,13 @@ __global__ __launch_bounds__(threads_of<LPR>()) void quantize_kernel(const Quant
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             out[e] = finite ? (int8_t)quantized((float)x.v[j][e], amax, inv) : (int8_t)0;
-        if constexpr (WIDE) {
-            const int at = share_at<LPR, true>(lane, j, 0);
+        if constexpr (WIDE_ROWS) {
+            const int at = share_at<LPR, WIDE>(lane, j, 0);
             if (at < W) __builtin_memcpy(__builtin_assume_aligned(q + at, 8), out, 8);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int at = share_at<LPR, false>(lane, j, e);
+                const int at = share_at<LPR, SINGLE>(lane, j, e);
                 if (at < W) q[at] = out[e];
             }
         }

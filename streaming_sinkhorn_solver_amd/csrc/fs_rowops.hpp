@@ -3,6 +3,7 @@
 #pragma once
 
 #include "fs_attn.hpp"
+#include "fs_layers_args.h"
 
 namespace fs {
 
@@ -110,35 +111,43 @@ struct RowFold {
 };
 
 // A lane's share of a row of `width` elements: CH groups of 8.  WIDE: groups of
-// neighbours, read with 16 bytes a lane (rows are whole, aligned groups); else
-// single elements, LPR apart, so that a wave reads neighbours.
-template <int LPR, bool WIDE>
+// neighbours, read with 16 bytes a lane (rows are whole, aligned groups).  DWORDS: the
+// same of rows that only start at whole dwords, which 16-byte accesses may; the last
+// group may be a part.  SINGLE: single elements, LPR apart, so that a wave reads
+// neighbours.
+template <int LPR, ShareForm FORM>
 __device__ __forceinline__ int share_at(int lane, int j, int e) {
-    return WIDE ? (lane + j * LPR) * 8 + e : (j * 8 + e) * LPR + lane;
+    return FORM != SINGLE ? (lane + j * LPR) * 8 + e : (j * 8 + e) * LPR + lane;
 }
 
-template <typename T, int LPR, int CH, bool WIDE>
+template <typename T, int LPR, int CH, ShareForm FORM>
 struct Share {
     T v[CH][8];
     // on: the row takes part; zeros stand for one that does not.  A lane without an
-    // element reads the row's first and leaves it: loads that ask nothing are all
-    // under way before the first is waited for.
+    // element (of a whole group) reads the row's first and leaves it: loads that ask
+    // nothing are all under way before the first is waited for.
     __device__ __forceinline__ void load(const T* row, int lane, int width, bool on) {
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            if constexpr (WIDE) {
+            if constexpr (FORM != SINGLE) {
                 constexpr int N = 2 * sizeof(T);
-                const int at = share_at<LPR, true>(lane, j, 0);
-                const bool in = on && at < width;
+                const int at = share_at<LPR, FORM>(lane, j, 0);
+                const bool in = on && (FORM == WIDE ? at < width : at + 8 <= width);
                 uint32_t w[N];
-                __builtin_memcpy(w, __builtin_assume_aligned(row + (in ? at : 0), 16), sizeof(w));
+                __builtin_memcpy(w, __builtin_assume_aligned(row + (in ? at : 0), FORM == WIDE ? 16 : 4),
+                                 sizeof(w));
 #pragma unroll
                 for (int i = 0; i < N; ++i) w[i] = in ? w[i] : 0u;
                 __builtin_memcpy(v[j], w, sizeof(w));
+                if (FORM == DWORDS && on && !in && at < width) {
+#pragma unroll
+                    for (int e = 0; e < 7; ++e)
+                        if (at + e < width) v[j][e] = row[at + e];
+                }
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int at = share_at<LPR, false>(lane, j, e);
+                    const int at = share_at<LPR, FORM>(lane, j, e);
                     const bool in = on && at < width;
                     const T t = row[in ? at : 0];
                     v[j][e] = in ? t : (T)0.f;
@@ -149,14 +158,20 @@ struct Share {
     __device__ __forceinline__ void store(T* row, int lane, int width) const {
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            if constexpr (WIDE) {
-                const int at = share_at<LPR, true>(lane, j, 0);
-                if (at < width)
-                    __builtin_memcpy(__builtin_assume_aligned(row + at, 16), v[j], sizeof(v[j]));
+            if constexpr (FORM != SINGLE) {
+                const int at = share_at<LPR, FORM>(lane, j, 0);
+                if (FORM == WIDE ? at < width : at + 8 <= width) {
+                    __builtin_memcpy(__builtin_assume_aligned(row + at, FORM == WIDE ? 16 : 4), v[j],
+                                     sizeof(v[j]));
+                } else if (FORM == DWORDS && at < width) {
+#pragma unroll
+                    for (int e = 0; e < 7; ++e)
+                        if (at + e < width) row[at + e] = v[j][e];
+                }
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int at = share_at<LPR, false>(lane, j, e);
+                    const int at = share_at<LPR, FORM>(lane, j, e);
                     if (at < width) row[at] = v[j][e];
                 }
             }
