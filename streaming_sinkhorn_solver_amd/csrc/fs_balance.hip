@@ -4,9 +4,9 @@
 //   L0 = E sum f P, L1 = mean lse^2, gates = p of the chosen (over their sum S);
 //   dp_e = dL0 E f_e / N + sum_{id = e} (dgate - (sum dgate gate)) / S,
 //   dx = p (dp - sum p dp + dL1 2 lse / N).
-// A row's columns lie with LPT lanes.  Sums over columns run in the
-// lanes' registers over a workgroup's rows, then over workgroups in a second
-// launch (in 64 bits, in a fixed order).  (65536 rows of 256 columns, 8 chosen, bf16:
+// A row's columns lie with LPT lanes.  Sums over rows run in the lanes' registers over
+// a workgroup's rows, then over workgroups in a second launch (in 64 bits, in a fixed
+// order).  (65536 rows of 256 columns, 8 chosen, bf16:
 // forward 20.7 us for 38 MB and 6.5 for the join, backward 23 us for 71 MB; bound by
 // the vector unit: 590 instructions for four rows forward, 385 backward, which issue
 // in 15 and 10 us.)
@@ -288,10 +288,9 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceArgs a) 
 }
 
 // The workgroups' sums of a batch entry (behind the columns' those of lse^2 and of
-// rows that take part), 8 columns a workgroup, 128 lanes each, in
-// 64 bits and a fixed order.  The last of the entry's workgroups to arrive adds
-// their terms (in their order) to the loss; the counter was cleared by the launch
-// before.
+// rows that take part), 8 columns a workgroup, 128 lanes each, in 64 bits and a fixed
+// order.  The last of the entry's workgroups to arrive adds their terms (in their
+// order) to the loss; the counter was cleared by the launch before.
 __global__ __launch_bounds__(1024) void balance_join_kernel(const BalanceArgs a) {
     __shared__ double red_p[128][9];
     __shared__ int red_c[128][9];

@@ -101,7 +101,7 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void distill_kernel(const D
     __shared__ float buf[2][NT / 64];
     extern __shared__ __align__(16) int ids[];  // ids and tau of whole groups of four
     float* const tau = (float*)(ids + padded(a.k));
-    __shared__ float mass[2];
+    __shared__ float mass;  // of the teacher's weights
     const int64_t block = flat_block();
     const int64_t row = block / sections;
     const int sec = (int)(block - row * sections), tid = threadIdx.x;
@@ -198,7 +198,7 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void distill_kernel(const D
             weight += w;
         }
         weight = lanes_sum<64>(weight);
-        if (tid == 0) mass[0] = weight;
+        if (tid == 0) mass = weight;
     }
 
     // the row's (or the range's) maximum and sum
@@ -265,7 +265,7 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void distill_kernel(const D
     if (!a.gx) return;
 
     stage_barrier();
-    weight = mass[0];
+    weight = mass;
     const float g = a.gloss[row];
     if (!on || lse == -INFINITY || weight == 0.f || g == 0.f) {
         const T zero[8] = {};
