@@ -337,6 +337,13 @@ hipError_t held(const DistillArgs& a, int cols, int sections, hipStream_t s) {
     if (cols <= 4096) return go<OP, 128, 4, false, WIDE, MODE>(a, sections, s);
     if (cols <= 8192) return go<OP, 256, 4, false, WIDE, MODE>(a, sections, s);
     if constexpr (MODE == WHOLE) {
+        // little more than 256 threads keep, or no gradient: many rows go better with
+        // smaller workgroups that read a rest again (us, 512 threads / 256 and a rest:
+        // 1500 x 10007, fp32, 27.3 / 23.5, loss alone 15.7 / 13.5; 4096 x 10000, bf16, 41.6
+        // / 37.4, 25.2 / 21.3; 4096 x 16384, bf16, 50.7 / 58.3, 30.0 / 25.5; 256 x 10000, 7.4
+        // / 7.5)
+        if (cols <= 16384 && a.rows >= 512 && (cols <= 10240 || !a.gx))
+            return go<OP, 256, 4, true, WIDE, MODE>(a, sections, s);
         if (cols <= 16384) return go<OP, 512, 4, false, WIDE, MODE>(a, sections, s);
         if (cols <= 32768) return go<OP, 1024, 4, false, WIDE, MODE>(a, sections, s);
         // (single elements of 16 bits come in registers of their own first)

@@ -79,6 +79,24 @@ def test_distill_forms(fs, dtype, rows):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_distill_many_rows(fs, dtype):
+    """From 512 rows on, rows of 8193 to 10240 classes (to 16384 for the loss alone) are
+    kept in part."""
+    for classes in (8200, 8201, 10241, 16384):
+        g = gen(classes)
+        x = randn(g, 512, classes, dtype=dtype, std=2.0)
+        ids = torch.randint(0, classes, (512, 3), generator=g, dtype=I4)
+        ids[0, 0] = classes - 1
+        t, dl = randn(g, 512, 3), 0.5 + torch.rand(512, generator=g)
+        print(dtype, classes, flush=True)
+        keep = torch.arange(0, 512, 37)
+        outs = distill_run(fs, x, ids, t, 1.5, dl)
+        ref = distill_reference(x[keep], ids[keep], t[keep], 1.5, d_loss=dl[keep])
+        for out in outs:
+            compare({k: v[keep.cuda()] for k, v in out.items()}, ref)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 @pytest.mark.parametrize("normalize", [False, True])
 def test_balance_forms(fs, dtype, normalize):
     for n in (3, 300):  # one workgroup, several
