@@ -1112,8 +1112,8 @@ def _states(t: Optional[torch.Tensor], name: str, like: torch.Tensor, dev: int, 
             _on(t, name, dev)
         if t.dtype is not like.dtype:
             raise TypeError(f"{name} is {t.dtype}, not {like.dtype} as the others")
-        if t.shape != shape:
-            raise ValueError(f"{name} must be {tuple(shape)} (is {tuple(t.shape)})")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)} (is {tuple(t.shape)})")
     s = t.stride()
     if s[-1] != 1 and shape[-1] != 1:
         raise ValueError(f"{name}'s last axis must be contiguous")
