@@ -166,8 +166,8 @@ fs_status fs_distill_loss_backward(const fs_distill_desc* desc, fs_rows logits, 
  *   gates_ij = p[ids_ij], over the row's sum of them if normalize.
  * Rows i >= lengths[b] (never read, whatever they hold) and rows of -inf alone
  * take no part: ids -1, gates and lse 0.  Where no row takes part the losses are
- * 0.  The columns chosen have no gradient.  A NaN or +inf among a row's logits makes
- * its gates and its gradient NaN, and its batch entry's losses. */
+ * 0.  The columns chosen have no gradient.  A NaN or +inf among a row's logits (or a
+ * row of NaN alone) makes its gates, lse and gradient NaN, and its batch entry's losses. */
 typedef struct {
     int32_t dtype;           /* fs_dtype of the logits and their gradient */
     int32_t batch, n;        /* >= 0; batch <= 65535, batch * n and n * k <= 2^31 - 1 */

@@ -195,12 +195,14 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceArgs a) 
             top = fmaxf(top, x[j]);
         }
         top = lanes_max<LPT>(top);
-        const bool on = top != -INFINITY;
-        const float ref = on ? top : 0.f;
+        const float ref = top == -INFINITY ? 0.f : top;
         float s = 0.f;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) s += x[j] = on ? ex2((x[j] - ref) * kLog2e) : 0.f;
+        for (int j = 0; j < EPL; ++j) s += x[j] = ex2((x[j] - ref) * kLog2e);
         s = lanes_sum<LPT>(s);
+        // 0 for a row of -inf alone, which takes no part; the maximum passes over a NaN, the
+        // sum is one, also where a row holds nothing else
+        const bool on = s != 0.f;
         const float inv = on ? __builtin_amdgcn_rcpf(s) : 0.f, lse = on ? fmaf(lg2(s), kLn2, ref) : 0.f;
 #pragma unroll
         for (int l = 0; l < SORTED; ++l) sort8(key[l]);
