@@ -8,8 +8,8 @@
 // a workgroup's rows, then over workgroups in a second launch (in 64 bits, in a fixed
 // order).  (65536 rows of 256 columns, 8 chosen, bf16:
 // forward 20.7 us for 38 MB and 6.5 for the join, backward 23 us for 71 MB; bound by
-// the vector unit: 590 instructions for four rows forward, 385 backward, which issue
-// in 15 and 10 us.)
+// the vector unit: 564 instructions for four rows forward, 421 backward, which issue
+// in 15 and 11 us.)
 #include "fs_layers_args.h"
 #include "fs_rowops.hpp"
 
@@ -418,12 +418,16 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(const BalanceArgs
         Row r = next;
         if (i + step < a.n) fetch(i + step, next);
         const bool on = r.first >= 0;
-        float p[EPL], dp[EPL];
+        // p by the row's own sum: lse as fp32 holds it is off by up to 2^-24 of it, a factor of
+        // all of the row (6e-5 at logits of 1000), which falls out
+        float p[EPL], dp[EPL], all = 0.f;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            p[j] = on ? ex2(((float)r.v[j] - r.lse) * kLog2e) : 0.f;
+            all += p[j] = on ? ex2(((float)r.v[j] - r.lse) * kLog2e) : 0.f;
             dp[j] = even[j];
         }
+        all = lanes_sum<LPT>(all);
+        const float inv = all != 0.f ? __builtin_amdgcn_rcpf(all) : 0.f;  // of p as it stands
         if (a.ggates) {
             bool have[SLOTS], twice = false;
             uint32_t at[SLOTS];
@@ -488,8 +492,9 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(const BalanceArgs
                 chosen = lanes_sum<LPT>(chosen);
                 mid = lanes_sum<LPT>(mid);
                 // (a choice from elsewhere may have no probability at all)
-                scale = chosen != 0.f ? 1.f / chosen : 0.f;
-                shift = mid * scale;
+                const float over = chosen != 0.f ? 1.f / chosen : 0.f;
+                scale = all * over;
+                shift = mid * over;
             }
 #pragma unroll
             for (int j = 0; j < EPL; ++j) dp[j] = fmaf(fmaf(-times[j], shift, dg[j]), scale, dp[j]);
@@ -497,10 +502,10 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(const BalanceArgs
         float mean = 0.f;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) mean = fmaf(p[j], dp[j], mean);
-        mean = lanes_sum<LPT>(mean) - (on ? square * r.lse : 0.f);
+        mean = (lanes_sum<LPT>(mean) * inv - (on ? square * r.lse : 0.f)) * inv;
         T* gx = (T*)a.gx.p + b * a.gx.sb + i * a.gx.sr;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) r.v[j] = (T)(on ? p[j] * (dp[j] - mean) : 0.f);
+        for (int j = 0; j < EPL; ++j) r.v[j] = (T)(on ? p[j] * fmaf(dp[j], inv, -mean) : 0.f);
         if constexpr (WIDE) {
 #pragma unroll
             for (int j = 0; j < EPL; j += 8) {

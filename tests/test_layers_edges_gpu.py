@@ -5,7 +5,8 @@ import math
 import pytest
 import torch
 
-from test_layers_gpu import balance_run, gen, randn
+from layers_reference import balance_reference
+from test_layers_gpu import balance_run, compare, gen, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +78,20 @@ def test_balance_rows_of_nan(fs, dtype, n, E, k):
             assert torch.isfinite(out[name][rest]).all(), name
             assert (out[name][0, masked] == 0).all(), name
         assert torch.isnan(out["loss"][0]).all() and torch.isfinite(out["loss"][1]).all()
+
+
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("E,k", [(7, 2), (64, 8), (256, 8), (333, 12), (1024, 4)])
+def test_balance_gradient_of_logits_far_from_zero(fs, normalize, E, k):
+    """A row's common offset changes neither the choice nor a probability, nor then the
+    gradient of the balance and of the gates.  Logits that are whole multiples of 2^-13
+    stay what they are under an offset of 1000, so that the outputs are within the bound
+    of those without it."""
+    g = gen(E)
+    x = torch.round(randn(g, 2, 60, E) * 8192) / 8192
+    far = x + 1000
+    assert torch.equal(far.double(), x.double() + 1000)
+    d_loss, d_gates = torch.tensor([[3.0, 0.0], [50.0, 0.0]]), randn(g, 2, 60, k, std=0.1)
+    ref = balance_reference(x, k, normalize, d_loss=d_loss, d_gates=d_gates)
+    out = balance_run(fs, far, k, d_loss, d_gates, normalize=normalize)
+    compare(out, {a: ref[a] for a in ("ids", "counts", "gates", "d_logits")})
