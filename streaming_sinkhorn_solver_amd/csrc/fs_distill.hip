@@ -160,38 +160,46 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void distill_kernel(const D
     }
 
     // The teacher's weights, by the first wave: id (-1: none) and tau of each entry;
-    // a lane keeps log tau of its first ones, the usual case being all of them.
+    // a lane keeps log tau of its first ones, the usual case being all of them.  Every
+    // logarithm is formed from differences of logits as they stand: the digits that a
+    // quotient by T or a log-sum-exp of it lacks would count |logit| / T times.
     constexpr int KEEP = 2;
-    float log_tau[KEEP], ref = 0.f, weight = 0.f;
+    float log_tau[KEEP], most = -INFINITY, ref = 0.f, weight = 0.f;
+    // log tau = (t - most) / T - ref, or t / T - ref where the caller gives ref (the
+    // quotient in two parts; what is too small for one is -inf, too large NaN)
+    const auto log_weight = [&](float t) {
+        if (!a.teacher_lse) return fmaf(t - most, inv_t, -ref);
+        const float q = t * inv_t;
+        return q == -INFINITY ? q : (q - ref) + fmaf(-q, a.T, t) * inv_t;
+    };
     if (MODE != PARTS && tid < 64) {
-        float top = -INFINITY;
         for (int k = tid; k < a.k; k += 64) {
             int id = -1;
             float t = -INFINITY;
             if (on) {
                 id = a.ids[row * a.k + k];
-                if (id >= 0 && id < a.classes) t = a.teacher[row * a.k + k] * inv_t;
+                if (id >= 0 && id < a.classes) t = a.teacher[row * a.k + k];
                 if (t == -INFINITY) id = -1;
             }
             ids[k] = id;
             tau[k] = t;
-            top = fmaxf(top, t);
+            most = fmaxf(most, t);
         }
         if (a.k + tid < padded(a.k)) ids[a.k + tid] = -1, tau[a.k + tid] = 0.f;
         if (a.teacher_lse) {
-            ref = on ? a.teacher_lse[row] : 0.f;  // the log of the weights' divisor
+            ref = on ? a.teacher_lse[row] : 0.f;
         } else {
-            top = lanes_max<64>(top);
+            most = lanes_max<64>(most);
             float s = 0.f;
             for (int k = tid; k < a.k; k += 64)
-                if (ids[k] >= 0) s += ex2((tau[k] - top) * kLog2e);
-            ref = top + logf(lanes_sum<64>(s));
+                if (ids[k] >= 0) s += ex2((tau[k] - most) * c);
+            ref = logf(lanes_sum<64>(s));
         }
         int n = 0;
 #pragma unroll
         for (int q = 0; q < KEEP; ++q) log_tau[q] = 0.f;
         for (int k = tid; k < a.k; k += 64, ++n) {
-            const float lt = tau[k] - ref, w = ids[k] >= 0 ? ex2(lt * kLog2e) : 0.f;
+            const float lt = log_weight(tau[k]), w = ids[k] >= 0 ? ex2(lt * kLog2e) : 0.f;
 #pragma unroll
             for (int q = 0; q < KEEP; ++q) log_tau[q] = n == q ? lt : log_tau[q];
             tau[k] = w;
@@ -238,8 +246,9 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void distill_kernel(const D
         ms.x = lanes_max<64>(r.m);
         ms.y = lanes_sum<64>(r.under(ms.x, c));
     }
+    const float log_sum = MODE == BACK ? 0.f : logf(ms.y);
     const float lse = MODE == BACK ? (on ? a.lse[row] : 0.f)
-                                   : ms.y == 0.f ? -INFINITY : fmaf(ms.x, inv_t, logf(ms.y));
+                                   : ms.y == 0.f ? -INFINITY : fmaf(ms.x, inv_t, log_sum);
     if (MODE != BACK && sec == 0 && tid < 64) {
         float sum = 0.f;
         const bool some = lse != -INFINITY && weight != 0.f;
@@ -252,8 +261,8 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void distill_kernel(const D
                 float lt = 0.f;
 #pragma unroll
                 for (int q = 0; q < KEEP; ++q) lt = n == q ? log_tau[q] : lt;
-                if (n >= KEEP) lt = a.teacher[row * a.k + k] * inv_t - ref;
-                sum = fmaf(w, lt - fmaf((float)x[id], inv_t, -lse), sum);
+                if (n >= KEEP) lt = log_weight(a.teacher[row * a.k + k]);
+                sum = fmaf(w, lt - fmaf((float)x[id] - ms.x, inv_t, -log_sum), sum);
             }
             sum = lanes_sum<64>(sum);
         }

@@ -5,8 +5,8 @@ import math
 import pytest
 import torch
 
-from layers_reference import balance_reference
-from test_layers_gpu import balance_run, compare, gen, randn
+from layers_reference import balance_reference, distill_reference
+from test_layers_gpu import balance_run, compare, fill, gen, gpu, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +95,95 @@ def test_balance_gradient_of_logits_far_from_zero(fs, normalize, E, k):
     ref = balance_reference(x, k, normalize, d_loss=d_loss, d_gates=d_gates)
     out = balance_run(fs, far, k, d_loss, d_gates, normalize=normalize)
     compare(out, {a: ref[a] for a in ("ids", "counts", "gates", "d_logits")})
+
+
+# ---- distillation ------------------------------------------------------------
+
+def distill_step(fs, x, ids, t, T, d_loss, teacher_lse=None, **kw):
+    """Loss, lse and gradient of one call."""
+    out = {"loss": fill(x.shape[0]), "lse": fill(x.shape[0]),
+           "d_logits": fill(*x.shape, dtype=x.dtype)}
+    fs.fs_distill_loss(gpu(x), gpu(ids), gpu(t), out["loss"], out["lse"], temperature=T,
+                       teacher_lse=gpu(teacher_lse), d_loss=gpu(d_loss), d_logits=out["d_logits"], **kw)
+    return out
+
+
+def far_inputs(R, V, k, T, offset, step, mass):
+    """Logits of a student and a teacher, a few T apart and whole multiples of `step`, and
+    the same beside an offset that leaves them what they are.  (near, far): x, t,
+    teacher_lse each."""
+    g = gen(V + k)
+    x, t = (torch.round(randn(g, *s, std=2 * T) / step) * step for s in ((R, V), (R, k)))
+    ids = torch.randint(0, V, (R, k), generator=g, dtype=I4)
+    ids[0, -1] = -1
+    x.scatter_(1, ids.clamp(0).long(), t)  # (a student that begins to know)
+    fx, ft = x + offset, t + offset
+    assert torch.equal(fx.double(), x.double() + offset)
+    assert torch.equal(ft.double(), t.double() + offset)
+    lse = far = None
+    if mass:
+        far = (torch.logsumexp(ft.double() / T, 1) + 0.4).float()
+        lse = far.double() - offset / T  # what the rounded one stands for
+    return (x, t.double(), lse), (fx, ft, far), ids, 0.5 + torch.rand(R, generator=g)
+
+
+# temperature, offset, the logits' step: an fp32 number at the offset holds it
+FAR = [(1.0, 1000.0, 2.0 ** -13), (0.3, -300.0, 2.0 ** -14), (1e-3, 14.0, 2.0 ** -20),
+       (2.0 ** -10, 14.0, 2.0 ** -20), (2.0 ** -20, 14.0, 2.0 ** -20), (1e5, 3e6, 0.5)]
+
+
+@pytest.mark.parametrize("mass", [False, True])
+@pytest.mark.parametrize("R,V,k", [(5, 300, 8), (3, 9000, 200), (2, 40001, 3), (2, 70000, 16), (140, 40000, 3)],
+                         ids=str)
+@pytest.mark.parametrize("T,offset,step", FAR, ids=str)
+def test_distill_logits_far_from_zero(fs, T, offset, step, R, V, k, mass):
+    """A common offset of a row's logits changes no probability: loss and gradient of one
+    call are within the bounds of the logits without it, whatever offset / T is."""
+    print(T, offset, R, V, k, mass, flush=True)
+    near, far, ids, d_loss = far_inputs(R, V, k, float(torch.tensor(T)), offset, step, mass)
+    T = float(torch.tensor(T))  # as the call's fp32 holds it
+    ref = distill_reference(near[0], ids, near[1], T, teacher_lse=near[2], d_loss=d_loss)
+    out = distill_step(fs, far[0], ids, far[1], T, d_loss, teacher_lse=far[2])
+    compare(out, {a: ref[a] for a in ("loss", "d_logits")})
+    compare(out, {"lse": distill_reference(far[0], ids, far[1], T)["lse"]})
+
+
+@TYPES
+@pytest.mark.parametrize("mass", [False, True])
+@pytest.mark.parametrize("T", [0.25, 1.0, 2.0])
+def test_distill_teacher_masked_by_the_lowest_number(fs, dtype, mass, T):
+    """Entries and columns that hold the type's lowest number weigh nothing, also where
+    their quotient by the temperature is no fp32 number."""
+    g = gen(6)
+    x, t = randn(g, 4, 500, dtype=dtype, std=2.0), randn(g, 4, 6)
+    ids = torch.stack([torch.randperm(500, generator=g)[:6] for _ in range(4)]).to(I4)
+    t[:, 4:] = torch.finfo(F4).min
+    lse = (torch.logsumexp(t[:, :4].double() / T, 1) + 0.3).float() if mass else None
+    dl = 0.5 + torch.rand(4, generator=g)
+    ref = distill_reference(x, ids[:, :4], t[:, :4], T, teacher_lse=lse, d_loss=dl)
+    compare(distill_step(fs, x, ids, t, T, dl, teacher_lse=lse), ref)
+    x[:, 400:] = torch.finfo(dtype).min
+    ids = ids % 400
+    ref = distill_reference(x[:, :400], ids[:, :4], t[:, :4], T, teacher_lse=lse, d_loss=dl)
+    out = distill_step(fs, x, ids, t, T, dl, teacher_lse=lse)
+    assert (out["d_logits"][:, 400:] == 0).all()
+    out["d_logits"] = out["d_logits"][:, :400]
+    compare(out, ref)
+
+
+@pytest.mark.parametrize("mass", [False, True])
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_distill_teacher_that_is_not_finite(fs, bad, mass):
+    """A NaN or +inf of the teacher's shows in its row's loss and gradient, and in no
+    other row."""
+    g = gen(7)
+    x, t = randn(g, 4, 700), randn(g, 4, 5)
+    ids = torch.randint(0, 700, (4, 5), generator=g, dtype=I4)
+    t[2, 3] = bad
+    lse = torch.full((4,), 3.0) if mass else None
+    out = distill_step(fs, x, ids, t, 1.5, torch.ones(4), teacher_lse=lse)
+    torch.cuda.synchronize()
+    assert torch.isnan(out["loss"][2]) and torch.isnan(out["d_logits"][2]).all()
+    for name in ("loss", "d_logits"):
+        assert torch.isfinite(out[name][[0, 1, 3]]).all()
+    assert torch.isfinite(out["lse"]).all()
