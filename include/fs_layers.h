@@ -141,6 +141,11 @@ typedef struct {
     const float* teacher;     /* device [rows][k] */
     const float* teacher_lse; /* device [rows] or NULL */
     const uint8_t* active;    /* device [rows] or NULL */
+    /* device fp32 [rows] or NULL: what lse lacks in fp32, written with it and read by
+     * the gradient call.  Without it that call's p are off by a factor of up to 1 +
+     * 2^-24 |lse| (5e-7 at 8), and T has to be 2^-10 or more; the one call for both
+     * never needs it. */
+    float* lse_rest;
 } fs_distill_desc;
 
 /* Bytes of workspace of fs_distill_loss; at least 256, or 0 for an invalid desc

@@ -125,7 +125,7 @@ class DistillDesc(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("rows", ctypes.c_int32), ("classes", ctypes.c_int32),
                 ("k", ctypes.c_int32), ("temperature", ctypes.c_float), ("ids", ctypes.c_void_p),
                 ("teacher", ctypes.c_void_p), ("teacher_lse", ctypes.c_void_p),
-                ("active", ctypes.c_void_p)]
+                ("active", ctypes.c_void_p), ("lse_rest", ctypes.c_void_p)]
 
 
 class BalanceDesc(ctypes.Structure):
@@ -1248,7 +1248,7 @@ def fs_quantized_product(q_x: torch.Tensor, scale_x: torch.Tensor, q_w: torch.Te
     return _call(lib.fs_quantized_product, "fs_quantized_product", dev, stream, pa, ws, size)
 
 
-def _distill_desc(logits, ids, teacher, temperature, teacher_lse, active):
+def _distill_desc(logits, ids, teacher, temperature, teacher_lse, active, lse_rest):
     """The description and the device's number."""
     dtype = _dtype_of(logits, "logits")
     if logits.dim() != 2:
@@ -1270,6 +1270,8 @@ def _distill_desc(logits, ids, teacher, temperature, teacher_lse, active):
                 not active.is_contiguous():
             raise TypeError(f"active must be a contiguous uint8 or bool tensor of ({rows},)")
         a.active = active.data_ptr()
+    if lse_rest is not None:
+        a.lse_rest = _flat(lse_rest, "lse_rest", dev, torch.float32, (rows,))
     return a, dev
 
 
@@ -1285,14 +1287,15 @@ def fs_distill_workspace_bytes(logits: torch.Tensor, k: int) -> int:
 
 def fs_distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
                     loss: torch.Tensor, lse: torch.Tensor, *, temperature: float = 1.0,
-                    teacher_lse=None, active=None, d_loss=None, d_logits=None,
+                    teacher_lse=None, active=None, d_loss=None, d_logits=None, lse_rest=None,
                     workspace: Optional[torch.Tensor] = None, stream=None):
     """loss <- T^2 KL(teacher's top entries || softmax(logits / T)) of each row, lse
     <- the rows' log-sum-exps.  logits: [rows, classes]; ids (int32), teacher
     (float32): [rows, k]; loss, lse: [rows] float32.  With d_loss ([rows] float32)
-    and d_logits the gradient is written in the same pass."""
+    and d_logits the gradient is written in the same pass; lse_rest ([rows] float32,
+    optional): what lse lacks, for a gradient call of its own."""
     lib = load()
-    a, dev = _distill_desc(logits, ids, teacher, temperature, teacher_lse, active)
+    a, dev = _distill_desc(logits, ids, teacher, temperature, teacher_lse, active, lse_rest)
     pa = ctypes.byref(a)
     ws, size, _keep = _work(workspace, lambda: _needed(lib.fs_distill_workspace_bytes,
                                                        "fs_distill_loss", pa), logits, dev, stream)
@@ -1308,9 +1311,11 @@ def fs_distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tens
 
 def fs_distill_loss_backward(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
                              lse: torch.Tensor, d_loss: torch.Tensor, d_logits: torch.Tensor, *,
-                             temperature: float = 1.0, teacher_lse=None, active=None, stream=None):
-    """Gradient of fs_distill_loss: writes d_logits from d_loss and the rows' lse."""
-    a, dev = _distill_desc(logits, ids, teacher, temperature, teacher_lse, active)
+                             temperature: float = 1.0, teacher_lse=None, active=None, lse_rest=None,
+                             stream=None):
+    """Gradient of fs_distill_loss: writes d_logits from d_loss and the rows' lse (and
+    lse_rest, which temperatures below 2^-10 need)."""
+    a, dev = _distill_desc(logits, ids, teacher, temperature, teacher_lse, active, lse_rest)
     f32, xs = torch.float32, logits.shape
     rows = xs[:1]
     return _call(load().fs_distill_loss_backward, "fs_distill_loss_backward", dev, stream,

@@ -269,6 +269,8 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void distill_kernel(const D
         if (tid == 0) {
             a.loss[row] = some ? a.T * a.T * sum : 0.f;
             a.lse[row] = on ? lse : 0.f;
+            if (a.lse_rest)
+                a.lse_rest[row] = on && fabsf(lse) < INFINITY ? fmaf(ms.x, inv_t, -lse) + log_sum : 0.f;
         }
     }
     if (!a.gx) return;
@@ -281,11 +283,15 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void distill_kernel(const D
         for (uint32_t at = 0; at < size; at += kStep) store(at, zero);
         return;
     }
-    // p_c = p1 2^((f x_c - f0) f2)
+    // p_c = p1 2^((f x_c - f0 - f1) f2)
+    const float f1 = MODE == BACK && a.lse_rest ? a.lse_rest[row] : 0.f;
     const float f = MODE == BACK ? inv_t : 1.f, f0 = MODE == BACK ? lse : ms.x;
     const float f2 = MODE == BACK ? kLog2e : c, p1 = MODE == BACK ? 1.f : 1.f / ms.y;
     const float gt = g * a.T, gp = gt * weight * p1;
-    const auto grad = [&](float xc) { return gp * ex2(fmaf(xc, f, -f0) * f2); };
+    const auto grad = [&](float xc) {
+        const float z = fmaf(xc, f, -f0);
+        return gp * ex2((MODE == BACK ? z - f1 : z) * f2);
+    };
 #pragma unroll
     for (int u = 0; u < CH; ++u) {
         forget(v[u]);

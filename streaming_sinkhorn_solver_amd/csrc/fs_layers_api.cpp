@@ -346,6 +346,9 @@ fs_status take_distill(const fs_distill_desc* p, bool backward, DistillArgs& a) 
         return fail(FS_ERR_INVALID_ARG, "k must be in [1, %d] (got %d)", kDistillMaxTop, d.k);
     if (!(d.temperature >= 0x1p-20f && d.temperature <= 0x1p20f))
         return fail(FS_ERR_INVALID_ARG, "temperature must be in [2^-20, 2^20]");
+    // (logits of 16 have an lse of 2^14 there, of whose rounding 2^-10 of p is left)
+    if (backward && d.temperature < 0x1p-10f && !d.lse_rest)
+        return fail(FS_ERR_INVALID_ARG, "a temperature below 2^-10 needs lse_rest");
     a.op = op_of(d.dtype);
     a.rows = d.rows;
     a.classes = d.classes;
@@ -355,6 +358,7 @@ fs_status take_distill(const fs_distill_desc* p, bool backward, DistillArgs& a) 
     a.teacher = d.teacher;
     a.teacher_lse = d.teacher_lse;
     a.active = d.active;
+    a.lse_rest = d.lse_rest;
     a.split = distill_split(d.rows, d.classes, backward, &a.split_cols);
     return FS_OK;
 }
@@ -394,11 +398,12 @@ fs_status fs_distill_loss(const fs_distill_desc* desc, fs_rows logits, float* lo
                           size_t workspace_bytes, void* stream) {
     DistillArgs a{};
     FS_TRY(take_distill(desc, false, a));
-    Extent in[7], out[3];
+    Extent in[7], out[4];
     bool vec = false;
     FS_TRY(distill_inputs(*desc, logits, a, vec, in));
     FS_TRY(take_flat("loss", loss, a.rows, 4, out[0]));
     FS_TRY(take_flat("lse", lse, a.rows, 4, out[1]));
+    if (a.lse_rest) FS_TRY(take_flat("lse_rest", a.lse_rest, a.rows, 4, out[3]));
     if (a.rows > 0 && !d_loss != !d_logits.data)
         return fail(FS_ERR_INVALID_ARG, "d_loss and d_logits are given both or neither");
     AttnView g{};
@@ -411,8 +416,8 @@ fs_status fs_distill_loss(const fs_distill_desc* desc, fs_rows logits, float* lo
     FS_TRY(check_workspace(workspace, workspace_bytes, need));
     in[6] = flat(workspace, need);
     Outputs o;
-    const char* names[3] = {"loss", "lse", "d_logits"};
-    for (int i = 0; i < 3; ++i) o.add(names[i], out[i]);
+    const char* names[4] = {"loss", "lse", "d_logits", "lse_rest"};
+    for (int i = 0; i < 4; ++i) o.add(names[i], out[i]);
     FS_TRY(o.check(in, 7));
     FS_TRY(check_gpu());
     if (a.rows == 0) return FS_OK;
@@ -430,15 +435,16 @@ fs_status fs_distill_loss_backward(const fs_distill_desc* desc, fs_rows logits, 
                                    const float* d_loss, fs_rows d_logits, void* stream) {
     DistillArgs a{};
     FS_TRY(take_distill(desc, true, a));
-    Extent in[7], out;
+    Extent in[8], out;
     bool vec = false;
     FS_TRY(distill_inputs(*desc, logits, a, vec, in));
     FS_TRY(take_flat("lse", lse, a.rows, 4, in[5]));
     FS_TRY(take_flat("d_loss", d_loss, a.rows, 4, in[6]));
+    if (a.lse_rest) FS_TRY(take_flat("lse_rest", a.lse_rest, a.rows, 4, in[7]));
     AttnView g{};
     FS_TRY(take_view("d_logits", d_logits, 1, a.rows, 1, a.classes, elem_size(desc->dtype), true, g,
                      out));
-    FS_TRY(check_apart("d_logits", out, in, 7));
+    FS_TRY(check_apart("d_logits", out, in, 8));
     FS_TRY(check_gpu());
     if (a.rows == 0) return FS_OK;
     a.gx = g.p;

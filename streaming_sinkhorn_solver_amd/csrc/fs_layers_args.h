@@ -90,6 +90,7 @@ struct DistillArgs {
     int64_t sgx;
     float* loss;      // NULL: backward alone
     float* lse;
+    float* lse_rest;  // or NULL
     const float* gloss;
     int split, split_cols;  // ranges of a row's classes
     float2* part;           // [rows][split]: reference and sum

@@ -1,12 +1,27 @@
 """What the binding and the host library of include/fs_layers.h answer at their edges:
 calls that a user may get wrong, and sizes asked for before there is memory.  No
 kernel runs."""
+import ctypes
+
 import pytest
 import torch
 
 from streaming_sinkhorn_solver_amd import binding
+from streaming_sinkhorn_solver_amd.binding import DistillDesc, Rows
 
 F4, I1 = torch.float32, torch.int8
+A = [x << 20 for x in range(1, 16)]  # addresses; no call gets as far as using them
+NONE = Rows(None, 0, 0, 0)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return binding.load()
+
+
+def refused(status, word):
+    assert status == binding.FS_ERR_INVALID_ARG, binding.fs_last_error()
+    assert word in binding.fs_last_error(), binding.fs_last_error()
 
 
 @pytest.fixture
@@ -36,3 +51,24 @@ def test_product_refuses_a_y_of_another_shape(calls, m, n, shape):
     assert not calls
     call(torch.zeros(m, n))
     assert calls == ["fs_quantized_product"]
+
+
+def test_distill_rest_refusals(lib):
+    """lse_rest is an output of the loss and an input of the gradient, which needs it
+    below a temperature of 2^-10."""
+    def desc(rest, T=1.0):
+        return ctypes.byref(DistillDesc(1, 4, 64, 3, T, A[1], A[2], None, None, rest))
+
+    def loss(rest):
+        return lib.fs_distill_loss(desc(rest), Rows(A[0], 0, 64, 0), A[3], A[4], None, NONE, A[7],
+                                   1 << 20, None)
+
+    def back(rest, T=1.0, gx=A[6]):
+        return lib.fs_distill_loss_backward(desc(rest, T), Rows(A[0], 0, 64, 0), A[4], A[5],
+                                            Rows(gx, 0, 64, 0), None)
+    refused(loss(A[8] + 2), "lse_rest is not aligned")
+    refused(loss(A[4]), "lse_rest overlaps lse")
+    refused(loss(A[1]), "lse_rest overlaps an input")
+    refused(back(A[6]), "d_logits overlaps an input")
+    refused(back(A[8] + 2), "lse_rest is not aligned")
+    refused(back(None, 2.0 ** -11), "lse_rest")

@@ -187,3 +187,55 @@ def test_distill_teacher_that_is_not_finite(fs, bad, mass):
     for name in ("loss", "d_logits"):
         assert torch.isfinite(out[name][[0, 1, 3]]).all()
     assert torch.isfinite(out["lse"]).all()
+
+
+@pytest.mark.parametrize("mass", [False, True])
+@pytest.mark.parametrize("R,V,k", [(5, 300, 8), (3, 9000, 200), (2, 70000, 16), (1100, 4100, 3)], ids=str)
+@pytest.mark.parametrize("T,offset,step", FAR, ids=str)
+def test_distill_gradient_alone_of_logits_far_from_zero(fs, T, offset, step, R, V, k, mass):
+    """With what the stored lse lacks in fp32 the gradient call, too, is within the bound
+    of the logits without their offset; rows that take no part, or hold -inf alone, have
+    no such rest."""
+    print(T, offset, R, V, k, mass, flush=True)
+    T = float(torch.tensor(T))
+    near, far, ids, d_loss = far_inputs(R, V, k, T, offset, step, mass)
+    if R > 1000:  # (their reference is slow)
+        near, far, ids, d_loss = ([t if t is None else t[::50] for t in near], far, ids, d_loss)
+        keep = torch.arange(0, R, 50)
+    else:
+        keep = torch.arange(R)
+    loss, lse, rest, dx = fill(R), fill(R), fill(R), fill(R, V)
+    x, t, tl = map(gpu, far)
+    active = torch.ones(R, dtype=torch.uint8)
+    active[R // 2 + 1:R // 2 + 2] = 0
+    kw = dict(temperature=T, teacher_lse=tl, active=gpu(active), lse_rest=rest)
+    fs.fs_distill_loss(x, gpu(ids), t, loss, lse, **kw)
+    fs.fs_distill_loss_backward(x, gpu(ids), t, lse, gpu(d_loss), dx, **kw)
+    ref = distill_reference(near[0], ids[keep], near[1], T, teacher_lse=near[2], d_loss=d_loss[keep],
+                            active=active[keep])
+    compare({"loss": loss[gpu(keep)], "d_logits": dx[gpu(keep)]}, {a: ref[a] for a in ("loss", "d_logits")})
+    assert (rest.abs() <= 2.0 ** -24 * lse.abs() + 1e-37).all()
+    assert (rest[gpu(active) == 0] == 0).all()
+
+
+def test_distill_rest_of_an_lse_that_is_not_finite(fs):
+    x, ids, t = randn(gen(1), 3, 50), torch.zeros(3, 1, dtype=I4), torch.zeros(3, 1)
+    x[0], x[1, 7] = -INF, NAN
+    loss, lse, rest, dx = fill(3), fill(3), fill(3), fill(3, 50)
+    fs.fs_distill_loss(gpu(x), gpu(ids), gpu(t), loss, lse, lse_rest=rest)
+    fs.fs_distill_loss_backward(gpu(x), gpu(ids), gpu(t), lse, torch.ones(3, device="cuda"), dx,
+                                lse_rest=rest)
+    torch.cuda.synchronize()
+    assert lse[0] == -INF and rest[0] == 0 and rest[1] == 0 and (dx[0] == 0).all()
+    assert torch.isnan(dx[1]).all() and torch.isfinite(dx[2]).all()
+
+
+def test_distill_gradient_alone_at_a_small_temperature(fs):
+    """Below 2^-10 the stored lse alone does not carry the gradient: refused."""
+    x, t = gpu(randn(gen(1), 3, 50)), torch.zeros(3, 1, device="cuda")
+    ids = torch.zeros(3, 1, dtype=I4, device="cuda")
+    lse, one, dx = torch.zeros(3, device="cuda"), torch.ones(3, device="cuda"), torch.zeros_like(x)
+    with pytest.raises(fs.FsError, match="lse_rest"):
+        fs.fs_distill_loss_backward(x, ids, t, lse, one, dx, temperature=2.0 ** -11)
+    with pytest.raises(ValueError, match="lse_rest"):
+        fs.fs_distill_loss_backward(x, ids, t, lse, one, dx, lse_rest=one[:2].clone())
