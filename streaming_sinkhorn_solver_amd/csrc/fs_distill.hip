@@ -159,20 +159,13 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void distill_kernel(const D
         for (int u = 0; u < CH; ++u) load(u * kStep, v[u]);
     }
 
-    // The teacher's weights, by the first wave: id (-1: none) and tau of each entry;
-    // a lane keeps log tau of its first ones, the usual case being all of them.  Every
-    // logarithm is formed from differences of logits as they stand: the digits that a
-    // quotient by T or a log-sum-exp of it lacks would count |logit| / T times.
-    constexpr int KEEP = 2;
-    float log_tau[KEEP], most = -INFINITY, ref = 0.f, weight = 0.f;
-    // log tau = (t - most) / T - ref, or t / T - ref where the caller gives ref (the
-    // quotient in two parts; what is too small for one is -inf, too large NaN)
-    const auto log_weight = [&](float t) {
-        if (!a.teacher_lse) return fmaf(t - most, inv_t, -ref);
-        const float q = t * inv_t;
-        return q == -INFINITY ? q : (q - ref) + fmaf(-q, a.T, t) * inv_t;
-    };
+    // The teacher's weights, by the first wave: id (-1: none) and tau of each entry, and
+    // a lane's sum of tau log tau, all that the loss needs of its logarithms.  These are
+    // formed from differences of logits as they stand: the digits that a quotient by T or
+    // a log-sum-exp of it lacks would count |logit| / T times.
+    float own = 0.f, weight = 0.f;
     if (MODE != PARTS && tid < 64) {
+        float most = -INFINITY, ref;
         for (int k = tid; k < a.k; k += 64) {
             int id = -1;
             float t = -INFINITY;
@@ -195,15 +188,18 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void distill_kernel(const D
                 if (ids[k] >= 0) s += ex2((tau[k] - most) * c);
             ref = logf(lanes_sum<64>(s));
         }
-        int n = 0;
-#pragma unroll
-        for (int q = 0; q < KEEP; ++q) log_tau[q] = 0.f;
-        for (int k = tid; k < a.k; k += 64, ++n) {
-            const float lt = log_weight(tau[k]), w = ids[k] >= 0 ? ex2(lt * kLog2e) : 0.f;
-#pragma unroll
-            for (int q = 0; q < KEEP; ++q) log_tau[q] = n == q ? lt : log_tau[q];
+        for (int k = tid; k < a.k; k += 64) {
+            const float t = tau[k];
+            float lt = fmaf(t - most, inv_t, -ref);
+            if (a.teacher_lse) {
+                // the quotient in two parts; what is too small for one is -inf, too large NaN
+                const float q = t * inv_t;
+                lt = q == -INFINITY ? q : (q - ref) + fmaf(-q, a.T, t) * inv_t;
+            }
+            const float w = ids[k] >= 0 ? ex2(lt * kLog2e) : 0.f;
             tau[k] = w;
             weight += w;
+            own += w == 0.f ? 0.f : w * lt;
         }
         weight = lanes_sum<64>(weight);
         if (tid == 0) mass = weight;
@@ -249,20 +245,17 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void distill_kernel(const D
     const float log_sum = MODE == BACK ? 0.f : logf(ms.y);
     const float lse = MODE == BACK ? (on ? a.lse[row] : 0.f)
                                    : ms.y == 0.f ? -INFINITY : fmaf(ms.x, inv_t, log_sum);
+    const float f1 = MODE == BACK && a.lse_rest ? a.lse_rest[row] * kLog2e : 0.f;
     if (MODE != BACK && sec == 0 && tid < 64) {
         float sum = 0.f;
         const bool some = lse != -INFINITY && weight != 0.f;
         if (some) {
-            int n = 0;
-            for (int k = tid; k < a.k; k += 64, ++n) {
+            sum = own;
+            for (int k = tid; k < a.k; k += 64) {
                 const int id = ids[k];
                 const float w = tau[k];
                 if (id < 0 || w == 0.f) continue;
-                float lt = 0.f;
-#pragma unroll
-                for (int q = 0; q < KEEP; ++q) lt = n == q ? log_tau[q] : lt;
-                if (n >= KEEP) lt = log_weight(a.teacher[row * a.k + k]);
-                sum = fmaf(w, lt - fmaf((float)x[id] - ms.x, inv_t, -log_sum), sum);
+                sum = fmaf(-w, fmaf((float)x[id] - ms.x, inv_t, -log_sum), sum);
             }
             sum = lanes_sum<64>(sum);
         }
@@ -283,14 +276,13 @@ __global__ __launch_bounds__(NT, NT == 1024 ? 8 : 1) void distill_kernel(const D
         for (uint32_t at = 0; at < size; at += kStep) store(at, zero);
         return;
     }
-    // p_c = p1 2^((f x_c - f0 - f1) f2)
-    const float f1 = MODE == BACK && a.lse_rest ? a.lse_rest[row] : 0.f;
+    // p_c = p1 2^((f x_c - f0) f2 - f1)
     const float f = MODE == BACK ? inv_t : 1.f, f0 = MODE == BACK ? lse : ms.x;
     const float f2 = MODE == BACK ? kLog2e : c, p1 = MODE == BACK ? 1.f : 1.f / ms.y;
     const float gt = g * a.T, gp = gt * weight * p1;
     const auto grad = [&](float xc) {
         const float z = fmaf(xc, f, -f0);
-        return gp * ex2((MODE == BACK ? z - f1 : z) * f2);
+        return gp * ex2(MODE == BACK ? fmaf(z, f2, -f1) : z * f2);
     };
 #pragma unroll
     for (int u = 0; u < CH; ++u) {
