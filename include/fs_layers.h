@@ -107,8 +107,9 @@ typedef struct {
     int64_t y_stride;
 } fs_quantized_product_desc;
 
-/* Bytes of workspace (from the sizes, the strides and the operands' alignment); at
- * least 256, or 0 if the sizes are out of range.  Pure host function. */
+/* Bytes of workspace (from the sizes, the strides and the operands' alignment; q_x or
+ * q_w NULL: enough for any address); at least 256, or 0 if the sizes are out of range.
+ * Pure host function. */
 size_t fs_quantized_product_workspace_bytes(const fs_quantized_product_desc* desc);
 
 fs_status fs_quantized_product(const fs_quantized_product_desc* desc, void* workspace,

@@ -1212,11 +1212,13 @@ def fs_quantize_rows(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, *, s
                                              (rows,)))
 
 
-def fs_quantized_product_workspace_bytes(m: int, n: int, k: int) -> int:
-    """Bytes of workspace of fs_quantized_product of contiguous, 16-byte aligned [m, k]
-    by [n, k]."""
+def fs_quantized_product_workspace_bytes(m: int, n: int, k: int, *, q_x=None, q_w=None) -> int:
+    """Bytes of workspace of fs_quantized_product of [m, k] by [n, k]: of these q_x and
+    q_w, or of contiguous, 16-byte aligned ones."""
     _i32("a size", m, n, k)
-    a = QuantizedProductDesc(0, m, n, k, None, k, None, None, k)
+    (xp, xs), (wp, ws) = ((256, k) if t is None else _matrix8(t, name, t.get_device(), (rows, k))
+                          for t, name, rows in ((q_x, "q_x", m), (q_w, "q_w", n)))
+    a = QuantizedProductDesc(0, m, n, k, xp, xs, None, wp, ws)
     return _needed(load().fs_quantized_product_workspace_bytes,
                    "fs_quantized_product_workspace_bytes", ctypes.byref(a))
 

@@ -211,9 +211,10 @@ bool product_sizes(int32_t m, int32_t n, int32_t k) {
     return m >= 0 && n >= 0 && k >= 0 && m <= kProductMaxRows && n <= kProductMaxRows &&
            (int64_t)m * n <= (int64_t)1 << 36 && k <= kQuantMaxWidth;
 }
-// (offsets within a tile of 256 rows stay 32-bit numbers)
+// (offsets within a tile of 256 rows stay 32-bit numbers; an operand that is not there
+// yet may come to stand anywhere)
 bool ready_for_tiles(const int8_t* q, int64_t rows, int64_t stride, int32_t k) {
-    return k % 16 == 0 && aligned16(q) && (rows <= 1 || (stride % 16 == 0 && stride <= 1 << 22));
+    return k % 16 == 0 && q && aligned16(q) && (rows <= 1 || (stride % 16 == 0 && stride <= 1 << 22));
 }
 struct ProductLayout {
     int split = 1, split_k = 1;
@@ -222,6 +223,7 @@ struct ProductLayout {
 };
 ProductLayout product_layout(const fs_quantized_product_desc& d) {
     ProductLayout l;
+    if (d.m == 0 || d.n == 0) return l;
     l.split = product_split(d.m, d.n, d.k, &l.split_k);
     size_t at = l.split > 1 ? up((size_t)l.split * d.m * d.n * 4) : 0;
     if (!product_few(d.m) && d.k > 0) {

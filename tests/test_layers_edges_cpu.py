@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from streaming_sinkhorn_solver_amd import binding
-from streaming_sinkhorn_solver_amd.binding import DistillDesc, Rows
+from streaming_sinkhorn_solver_amd.binding import DistillDesc, QuantizedProductDesc, Rows
 
 F4, I1 = torch.float32, torch.int8
 A = [x << 20 for x in range(1, 16)]  # addresses; no call gets as far as using them
@@ -72,3 +72,40 @@ def test_distill_rest_refusals(lib):
     refused(back(A[6]), "d_logits overlaps an input")
     refused(back(A[8] + 2), "lse_rest is not aligned")
     refused(back(None, 2.0 ** -11), "lse_rest")
+
+
+def product_bytes(lib, m, n, k, x, sx, w, sw):
+    a = QuantizedProductDesc(0, m, n, k, x, sx, None, w, sw)
+    return int(lib.fs_quantized_product_workspace_bytes(ctypes.byref(a)))
+
+
+@pytest.mark.parametrize("m,n,k", [(33, 40, 64), (1800, 1700, 256), (70, 90, 8192), (2000, 33, 16)])
+def test_product_workspace_before_there_is_memory(lib, m, n, k):
+    """An operand that is not there yet may come to stand anywhere: the answer is enough
+    for every address that its stride allows."""
+    asked = product_bytes(lib, m, n, k, None, k, None, k)
+    for x in (A[0], A[0] + 1, A[0] + 8):
+        for w in (A[1], A[1] + 2):
+            need = product_bytes(lib, m, n, k, x, k, w, k)
+            assert need <= asked
+            assert (need < asked) == (x == A[0] or w == A[1])
+            assert need <= product_bytes(lib, m, n, k, x, k, None, k) <= asked
+    # few rows are read as they stand, and nothing is to be formed without rows
+    assert product_bytes(lib, 8, n, k, None, k, None, k) == 256
+    assert product_bytes(lib, m, 0, k, None, k, None, k) == 256
+
+
+def test_product_workspace_of_given_operands(lib, calls):
+    """The binding answers for contiguous, aligned operands, or for those it is given."""
+    m, n, k = 70, 90, 320
+    x, w = torch.zeros(m, k + 16, dtype=I1), torch.zeros(n, k + 5, dtype=I1)
+    aligned = binding.fs_quantized_product_workspace_bytes(m, n, k)
+    assert aligned == product_bytes(lib, m, n, k, A[0], k, A[1], k)
+    for qx, qw in ((x[:, :k], None), (x[:, 1:k + 1], None), (None, w[:, :k]), (x[:, :k], w[:, 1:k + 1]),
+                   (x[:, 3:k + 3], w[:, 1:k + 1])):
+        p = [(t.data_ptr(), t.stride(0)) if t is not None else (A[0], k) for t in (qx, qw)]
+        assert binding.fs_quantized_product_workspace_bytes(m, n, k, q_x=qx, q_w=qw) == \
+            product_bytes(lib, m, n, k, *p[0], *p[1])
+    assert binding.fs_quantized_product_workspace_bytes(m, n, k, q_w=w[:, 1:k + 1]) > aligned
+    with pytest.raises(ValueError, match="q_x must be"):
+        binding.fs_quantized_product_workspace_bytes(m, n, k, q_x=x)

@@ -30,6 +30,30 @@ def test_product_refuses_a_y_of_another_shape(fs, dtype):
         assert (buf == 7).all()
 
 
+
+@pytest.mark.parametrize("m,n,k", [(70, 90, 320), (1800, 1700, 256)])
+def test_product_workspace_of_a_slice(fs, m, n, k):
+    """A program that keeps its own workspace asks with the operands it has; the call
+    writes nothing behind what was asked for."""
+    g = gen(k)
+    x = torch.randint(-128, 128, (m, k + 5), generator=g, dtype=I1).cuda()[:, 1:k + 1]
+    w = torch.randint(-128, 128, (n, k), generator=g, dtype=I1).cuda()
+    sx, sw = torch.rand(m, device="cuda"), torch.rand(n, device="cuda")
+    small = fs.fs_quantized_product_workspace_bytes(m, n, k)
+    need = fs.fs_quantized_product_workspace_bytes(m, n, k, q_x=x, q_w=w)
+    assert need > small
+    own, y = fill(m, n), fill(m, n)
+    with pytest.raises(fs.FsError, match="workspace"):
+        fs.fs_quantized_product(x, sx, w, sw, y,
+                                workspace=torch.zeros(small, dtype=torch.uint8, device="cuda"))
+    space = torch.full((need + 256,), 0x55, dtype=torch.uint8, device="cuda")
+    fs.fs_quantized_product(x, sx, w, sw, y, workspace=space[:need])
+    fs.fs_quantized_product(x, sx, w, sw, own)
+    assert torch.equal(y, own) and (space[need:] == 0x55).all()
+    p = (x.double() @ w.double().t().contiguous()) * sx.double()[:, None] * sw.double()
+    assert ((y - p).abs() <= 4 * 2.0 ** -24 * p.abs()).all()
+
+
 # ---- balance -----------------------------------------------------------------
 
 def poison(x):
