@@ -19,8 +19,8 @@
  *    with a width of whole 16-byte chunks are read with wide loads (the layer
  *    norm's also where they start at whole dwords), others element by element.
  *    Arrays given by plain pointers are contiguous.  Outputs may not overlap
- *    themselves, one another, an input or the workspace (slices of one buffer
- *    side by side do not overlap; against an input whole extents count).
+ *    themselves, one another, an input or the workspace (slices of one buffer side
+ *    by side, of equal strides, do not; against an input whole extents count).
  *  - Work is enqueued on `stream` and is asynchronous; nothing synchronises,
  *    nothing is allocated, and every call may be captured into a graph (a replay
  *    uses the same buffers: two captured calls that may overlap need a workspace

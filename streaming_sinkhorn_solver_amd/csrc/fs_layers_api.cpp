@@ -3,6 +3,9 @@
 // synchronises or throws.
 #include "fs_layers.h"
 
+#include <cstdlib>
+#include <utility>
+
 #include "fs_host.hpp"
 #include "fs_layers_args.h"
 
@@ -29,21 +32,44 @@ fs_status take_flat(const char* name, const void* p, int64_t count, size_t size,
     return FS_OK;
 }
 
-// Outputs against the inputs and against one another.  Two views may be slices
-// of one buffer side by side: only those that start together are refused.
+// Whether two views of b x r rows of w elements, neither of which overlaps itself, share
+// one.  Of equal strides: whether their offset d comes nearer than w to a difference of
+// two rows' places, i L + j S with |i| < the longer stride's rows and |j| < the shorter's;
+// a block of the shorter's rows ends before the longer stride does, so that only the i
+// next to -d / L can do it, and of those the j next to the rest.  Other strides: taken to.
+bool views_meet(const AttnView& x, const AttnView& y, int64_t b, int64_t r, int64_t w, int es) {
+    if (x.sb != y.sb || x.sr != y.sr) return true;
+    int64_t L = x.sb, nl = b, S = x.sr, ns = r;
+    if (L < S) std::swap(L, S), std::swap(nl, ns);
+    const auto near = [](int64_t d, int64_t s, int64_t n) { return n > 1 ? -d / s : 0; };
+    const int64_t d = (y.p - x.p) / es, i0 = near(d, L, nl);
+    for (int64_t i = i0 - 1; i <= i0 + 1; ++i) {
+        if (i <= -nl || i >= nl) continue;
+        const int64_t rest = d + i * L, j0 = near(rest, S, ns);
+        for (int64_t j = j0 - 1; j <= j0 + 1; ++j)
+            if (j > -ns && j < ns && std::abs(rest + j * S) < w) return true;
+    }
+    return false;
+}
+
+// Outputs against the inputs and against one another.  Two views (of b x r rows of w
+// elements) may be slices of one buffer side by side.
 struct Outputs {
     Extent e[8];
     const char* name[8];
-    bool view[8];
+    const AttnView* view[8];
     int n = 0;
-    void add(const char* what, const Extent& x, bool is_view = false) {
-        if (x.hi > x.lo) e[n] = x, view[n] = is_view, name[n++] = what;
+    int64_t b = 0, r = 0, w = 0;
+    int es = 1;
+    void add(const char* what, const Extent& x, const AttnView* v = nullptr) {
+        if (x.hi > x.lo) e[n] = x, view[n] = v, name[n++] = what;
     }
     fs_status check(const Extent* in, int n_in) const {
         for (int i = 0; i < n; ++i) {
             FS_TRY(check_apart(name[i], e[i], in, n_in));
             for (int j = 0; j < i; ++j)
-                if (view[i] && view[j] ? e[i].lo == e[j].lo : e[i].overlaps(e[j]))
+                if (e[i].overlaps(e[j]) &&
+                    (!view[i] || !view[j] || views_meet(*view[i], *view[j], b, r, w, es)))
                     return fail(FS_ERR_INVALID_ARG, "%s overlaps %s", name[i], name[j]);
         }
         return FS_OK;
@@ -136,8 +162,11 @@ fs_status fs_layer_norm(const fs_layer_norm_desc* desc, fs_rows x, fs_rows resid
     if (mean) FS_TRY(take_flat("mean", mean, rows, 4, out[2]));
     if (rstd) FS_TRY(take_flat("rstd", rstd, rows, 4, out[3]));
     Outputs o;
-    const char* names[4] = {"y", "total", "mean", "rstd"};
-    for (int i = 0; i < 4; ++i) o.add(names[i], out[i], i < 2);
+    o.b = a.B, o.r = a.n, o.w = a.width, o.es = es;
+    o.add("y", out[0], &a.y);
+    o.add("total", out[1], &a.z);
+    o.add("mean", out[2]);
+    o.add("rstd", out[3]);
     FS_TRY(o.check(in, 5));
     FS_TRY(check_gpu());
     if (rows == 0) return FS_OK;

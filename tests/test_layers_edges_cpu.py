@@ -2,12 +2,13 @@
 calls that a user may get wrong, and sizes asked for before there is memory.  No
 kernel runs."""
 import ctypes
+import random
 
 import pytest
 import torch
 
 from streaming_sinkhorn_solver_amd import binding
-from streaming_sinkhorn_solver_amd.binding import DistillDesc, QuantizedProductDesc, Rows
+from streaming_sinkhorn_solver_amd.binding import DistillDesc, LayerNormDesc, QuantizedProductDesc, Rows
 
 F4, I1 = torch.float32, torch.int8
 A = [x << 20 for x in range(1, 16)]  # addresses; no call gets as far as using them
@@ -109,3 +110,65 @@ def test_product_workspace_of_given_operands(lib, calls):
     assert binding.fs_quantized_product_workspace_bytes(m, n, k, q_w=w[:, 1:k + 1]) > aligned
     with pytest.raises(ValueError, match="q_x must be"):
         binding.fs_quantized_product_workspace_bytes(m, n, k, q_x=x)
+
+
+def two_outputs(lib, batch, n, width, at_y, y, at_total, total):
+    """What the layer norm says of y and total as these views (offsets and strides in
+    elements); a call that it allows is refused for its rstd, which is its mean."""
+    a = LayerNormDesc(0, batch, n, width, 1e-5)
+    view = lambda base, s: Rows(base, s[0], s[1], 0)
+    flat = (n * width, width)
+    status = lib.fs_layer_norm(ctypes.byref(a), view(A[0], flat), view(A[1], flat), None, None,
+                               view(A[2] + 4 * at_total, total), view(A[2] + 4 * at_y, y), A[3], A[3],
+                               None)
+    assert status == binding.FS_ERR_INVALID_ARG
+    return binding.fs_last_error()
+
+
+def elements(batch, n, width, at, strides):
+    rows = [at + b * strides[0] + i * strides[1] for b in range(batch) for i in range(n)]
+    all_ = [r + e for r in rows for e in range(width)]
+    return set(all_), len(set(all_)) == len(all_)
+
+
+def test_two_output_views_of_one_buffer(lib):
+    """Rows 0..9 and 5..14 of one buffer overlap; slices side by side, rows or batches in
+    turn do not."""
+    flat = (640, 64)
+    assert "total overlaps y" in two_outputs(lib, 1, 10, 64, 0, flat, 5 * 64, flat)
+    assert "total overlaps y" in two_outputs(lib, 2, 10, 64, 0, flat, 64, flat)
+    assert "total overlaps y" in two_outputs(lib, 1, 10, 64, 5 * 64 + 3, flat, 0, flat)
+    assert "total overlaps y" in two_outputs(lib, 1, 10, 64, 0, (0, 100), 32, (0, 100))
+    assert "total overlaps y" in two_outputs(lib, 1, 10, 64, 0, (0, 128), 64, (0, 192))
+    # (the second batch entry of one is the first of the other)
+    assert "total overlaps y" in two_outputs(lib, 2, 10, 64, 0, flat, 640, flat)
+    for y, total, s in ((0, 1280, flat), (0, 64, (1280, 128)), (64, 0, (1280, 128)),
+                        (0, 64, (1440, 144)), (8, 72, (1584, 144)), (0, 640, (1280, 64)),
+                        (0, 1 << 16, flat), (0, 64, (128, 640))):
+        assert "rstd overlaps mean" in two_outputs(lib, 2, 10 if s[1] != 640 else 3, 64, y, s, total, s)
+
+
+def test_two_output_views_of_any_strides(lib):
+    """Against the sets of their elements: views that share one are refused, views of equal
+    strides that share none are not."""
+    rng = random.Random(5)
+    seen = {True: 0, False: 0}
+    while min(seen.values()) < 3000:
+        batch, n, width = rng.randint(1, 4), rng.randint(1, 4), rng.randint(1, 5)
+        s = (rng.randint(1, 40), rng.randint(1, 40))
+        t = s if rng.random() < 0.8 else (rng.randint(1, 40), rng.randint(1, 40))
+        at = rng.randint(0, 60), rng.randint(0, 60)
+        (one, fits), (other, fits2) = (elements(batch, n, width, x, y) for x, y in zip(at, (s, t)))
+        if not (fits and fits2):
+            continue
+        said = two_outputs(lib, batch, n, width, at[0], s, at[1], t)
+        if "is written and its strides overlap" in said:
+            continue  # (rows and batches that interleave: refused for themselves)
+        meet = bool(one & other)
+        used = [x for x, size in ((0, batch), (1, n)) if size > 1]
+        alike = all(s[x] == t[x] for x in used)
+        apart = max(one) < min(other) or max(other) < min(one)
+        if meet or alike or apart:
+            assert ("total overlaps y" in said) == meet, (batch, n, width, at, s, t, said)
+            assert meet or "rstd overlaps mean" in said
+            seen[meet] += 1
