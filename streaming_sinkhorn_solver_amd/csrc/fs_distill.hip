@@ -344,12 +344,23 @@ hipError_t held(const DistillArgs& a, int cols, int sections, hipStream_t s) {
     if (cols <= 4096) return go<OP, 128, 4, false, WIDE, MODE>(a, sections, s);
     if (cols <= 8192) return go<OP, 256, 4, false, WIDE, MODE>(a, sections, s);
     if constexpr (MODE == WHOLE) {
-        // little more than 256 threads keep, or no gradient: many rows go better with
-        // smaller workgroups that read a rest again (us, 512 threads / 256 and a rest:
-        // 1500 x 10007, fp32, 27.3 / 23.5, loss alone 15.7 / 13.5; 4096 x 10000, bf16, 41.6
-        // / 37.4, 25.2 / 21.3; 4096 x 16384, bf16, 50.7 / 58.3, 30.0 / 25.5; 256 x 10000, 7.4
-        // / 7.5)
-        if (cols <= 16384 && a.rows >= 512 && (cols <= 10240 || !a.gx))
+        // Many rows go better with smaller workgroups, which read a rest again: without a
+        // gradient, and with one where the rest is small; in fp32 while all of the logits
+        // are small, too (us, 256 threads and a rest / 512; rows x classes):
+        //                         bf16                           fp32
+        //                 loss alone   and gradient    loss alone    and gradient
+        //    512 x 8200   6.1 / 6.1     9.8 / 9.7      7.8 / 7.4     13.4 / 12.2
+        //   1024 x 10007  9.2 / 10.5   15.1 / 17.0    10.9 / 12.6    21.0 / 23.7
+        //   1024 x 10000  8.7 / 8.6    13.8 / 14.2    10.7 / 10.6    22.0 / 21.1
+        //   1500 x 10007 11.6 / 13.0   18.8 / 21.8    13.8 / 15.6    30.7 / 31.7
+        //   2048 x 8200  12.0 / 14.2   20.0 / 23.3    15.6 / 17.7    31.5 / 34.2
+        //   2048 x 10000 12.2 / 15.2   24.2 / 27.1    17.7 / 19.9    43.8 / 40.6
+        //   4096 x 8200  19.8 / 24.3   38.7 / 43.5    27.4 / 31.6    63.0 / 58.2
+        //   4096 x 10000 22.0 / 27.1   43.0 / 46.3    31.4 / 34.3    80.6 / 69.1
+        //   4096 x 16384 28.0 / 32.6   65.5 / 56.9    48.2 / 48.4   127.1 / 113.5
+        const bool small =
+            cols <= 10240 && (OP != OP_F32 || (int64_t)a.rows * cols * 4 <= 70 << 20);
+        if (cols <= 16384 && a.rows >= 1024 && (small || !a.gx))
             return go<OP, 256, 4, true, WIDE, MODE>(a, sections, s);
         if (cols <= 16384) return go<OP, 512, 4, false, WIDE, MODE>(a, sections, s);
         if (cols <= 32768) return go<OP, 1024, 4, false, WIDE, MODE>(a, sections, s);

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from layers_reference import balance_reference, distill_reference
-from test_layers_gpu import balance_run, compare, fill, gen, gpu, randn
+from test_layers_gpu import balance_run, compare, distill_run, fill, gen, gpu, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -263,3 +263,21 @@ def test_distill_gradient_alone_at_a_small_temperature(fs):
         fs.fs_distill_loss_backward(x, ids, t, lse, one, dx, temperature=2.0 ** -11)
     with pytest.raises(ValueError, match="lse_rest"):
         fs.fs_distill_loss_backward(x, ids, t, lse, one, dx, lse_rest=one[:2].clone())
+
+
+@TYPES
+@pytest.mark.parametrize("rows,classes", [(1024, 8200), (1030, 8201), (1024, 10240), (1100, 10241),
+                                          (1024, 16384), (2048, 8200), (2300, 8203)], ids=str)
+def test_distill_many_rows_of_medium_length(fs, dtype, rows, classes):
+    """From 1024 rows on, rows of 8193 to 10240 classes (fp32: of 70 MB in all; to 16384
+    for the loss alone) are kept in part and read again."""
+    print(dtype, rows, classes, flush=True)
+    g = gen(classes)
+    x = randn(g, rows, classes, dtype=dtype, std=2.0)
+    ids = torch.randint(0, classes, (rows, 3), generator=g, dtype=I4)
+    ids[0, 0] = classes - 1
+    t, dl = randn(g, rows, 3), 0.5 + torch.rand(rows, generator=g)
+    keep = torch.arange(0, rows, 97)
+    ref = distill_reference(x[keep], ids[keep], t[keep], 1.5, d_loss=dl[keep])
+    for out in distill_run(fs, x, ids, t, 1.5, dl):
+        compare({k: v[keep.cuda()] for k, v in out.items()}, ref)
