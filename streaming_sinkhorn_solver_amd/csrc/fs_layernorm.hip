@@ -18,12 +18,6 @@ namespace fs {
 
 namespace {
 
-// LPR threads a row, CH groups of 8 elements a thread.
-template <int LPR>
-constexpr int threads_of() {
-    return LPR > 256 ? LPR : 256;
-}
-
 __device__ __forceinline__ void place(const LayerNormArgs& a, int64_t row, int& b, int& i) {
     b = a.B == 1 ? 0 : (int)((uint32_t)row / (uint32_t)a.n);
     i = (int)(row - (int64_t)b * a.n);
@@ -32,6 +26,7 @@ __device__ __forceinline__ bool row_on(const LayerNormArgs& a, int b, int i) {
     return !a.lengths || i < a.lengths[b];
 }
 
+// LPR threads a row, CH groups of 8 elements a thread.
 template <int LPR, int CH, ShareForm FORM>
 __device__ __forceinline__ void load_weight(const float* w, int lane, int width, float fill,
                                             float (&out)[CH][8]) {

@@ -39,11 +39,6 @@ __device__ __forceinline__ int quantized(float x, float a, float inv) {
     return n;
 }
 
-template <int LPR>
-constexpr int threads_of() {
-    return LPR > 256 ? LPR : 256;
-}
-
 // Bound by memory: a row is read once and stays in registers over its maximum.
 template <int OP, int LPR, int CH, bool WIDE_ROWS>
 __global__ __launch_bounds__(threads_of<LPR>()) void quantize_kernel(const QuantArgs a) {

@@ -55,6 +55,12 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
     return lanes_fold<LPR>(x, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 
+// Threads of a workgroup whose rows lie with LPR threads each.
+template <int LPR>
+constexpr int threads_of() {
+    return LPR > 256 ? LPR : 256;
+}
+
 // Sums over the LPR threads of a row, of whole waves if more than 64: the waves'
 // sums meet in LDS.  Two buffers in turn, so that one barrier a sum is enough: a
 // buffer is written again only behind the next sum's barrier, in front of which
