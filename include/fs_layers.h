@@ -42,13 +42,15 @@ extern "C" {
  *   z = x + residual (rounded to dtype: the sum that goes on), or x
  *   mean = mean(z), rstd = 1 / sqrt(mean((z - mean)^2) + eps)
  *   y = weight (z - mean) rstd + bias
- * Rows i >= lengths[b] are padding: never read, whatever they hold, and written
- * as zeros (y, total, mean, rstd, d_x); they take no part in a gradient. */
+ * Rows i >= lengths[b] are padding: nothing depends on what they hold (a first few
+ * elements may be fetched, and are dropped), they are written as zeros (y, total,
+ * mean, rstd, d_x) and take no part in a gradient. */
 typedef struct {
     int32_t dtype;           /* fs_dtype of x, residual, total, y and their gradients */
     int32_t batch, n;        /* >= 0; batch * n <= 2^31 - 1 */
     int32_t width;           /* 1..16384 */
-    float eps;               /* >= 0 (0: a constant row gives NaN) */
+    float eps;               /* >= 0 (0: y of a constant row is not defined: NaN, or what
+                                the rounding of its mean leaves) */
     const int32_t* lengths;  /* device [batch], clamped to 0..n; or NULL (n) */
 } fs_layer_norm_desc;
 
@@ -87,8 +89,8 @@ fs_status fs_quantize_rows(int32_t dtype, int32_t rows, int32_t width, const voi
                            void* stream);
 
 /* y[i][j] = scale_x[i] scale_w[j] sum_k q_x[i][k] q_w[j][k] + bias[j].  The sum is
- * exact; it and the two products with the scales are rounded to fp32, y to its
- * type.  q_x: [m][k] and q_w: [n][k] int8 (any value, -128 too), y: [m][n] of
+ * exact; it, its product with scale_x and the rest in one are rounded to fp32, y to
+ * its type.  q_x: [m][k] and q_w: [n][k] int8 (any value, -128 too), y: [m][n] of
  * dtype; strides of rows in elements.  bias: device fp32 [n] or NULL.  0 <= m, n
  * <= 2^24, m n <= 2^36, 0 <= k <= 65536 (k = 0: the sum is 0).  With more than 32
  * rows an operand whose rows are not 16-byte aligned, or whose k is no multiple of
@@ -172,10 +174,11 @@ fs_status fs_distill_loss_backward(const fs_distill_desc* desc, fs_rows logits, 
  *   loss[b][0] = experts sum_e (c_e / (k N)) (mean_i p_ie),
  *   loss[b][1] = mean_i lse_i^2,
  *   gates_ij = p[ids_ij], over the row's sum of them if normalize.
- * Rows i >= lengths[b] (never read, whatever they hold) and rows of -inf alone
- * take no part: ids -1, gates and lse 0.  Where no row takes part the losses are
- * 0.  The columns chosen have no gradient.  A NaN or +inf among a row's logits (or a
- * row of NaN alone) makes its gates, lse and gradient NaN, and its batch entry's losses. */
+ * Rows i >= lengths[b] (padding: nothing depends on what they hold, though a first
+ * few elements may be fetched) and rows of -inf alone take no part: ids -1, gates
+ * and lse 0.  Where no row takes part the losses are 0.  The columns chosen have no
+ * gradient.  A NaN or +inf among a row's logits (or a row of NaN alone) makes its
+ * gates, lse and gradient NaN, and its batch entry's losses. */
 typedef struct {
     int32_t dtype;           /* fs_dtype of the logits and their gradient */
     int32_t batch, n;        /* >= 0; batch <= 65535, batch * n and n * k <= 2^31 - 1 */

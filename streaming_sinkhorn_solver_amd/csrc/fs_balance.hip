@@ -5,11 +5,11 @@
 //   dp_e = dL0 E f_e / N + sum_{id = e} (dgate - (sum dgate gate)) / S,
 //   dx = p (dp - sum p dp + dL1 2 lse / N).
 // A row's columns lie with LPT lanes.  Sums over rows run in the lanes' registers over
-// a workgroup's rows, then over workgroups in a second launch (in 64 bits, in a fixed
-// order).  (65536 rows of 256 columns, 8 chosen, bf16:
-// forward 20.7 us for 38 MB and 6.5 for the join, backward 23 us for 71 MB; bound by
-// the vector unit: 564 instructions for four rows forward, 421 backward, which issue
-// in 15 and 11 us.)
+// a workgroup's rows (fp32: four rows a lane at 65536 x 256), then over workgroups in a
+// second launch (in 64 bits, in a fixed order).  (65536 rows of 256 columns, 8 chosen,
+// bf16: forward 20.2 us for 38 MB and 6.4 for the join, backward 24.6 us for 71 MB;
+// bound by the vector unit: 564 instructions for four rows forward, 421 backward, which
+// issue in 15 and 11 us.)
 #include "fs_layers_args.h"
 #include "fs_rowops.hpp"
 

@@ -4,7 +4,7 @@
 //   u = w g,  dx = rstd (u - mean u - h mean(u h)) + dz,  dw = sum g h,  db = sum g.
 // Bound by memory: a row is read once and stays in registers over both sums of
 // its statistics (the second is of squared distances from the mean, so that a
-// large mean costs no digits).  Up to 1024 elements a row lies with 8 to 64 lanes
+// large mean costs the variance no digits; the mean itself is an fp32 number).  Up to 1024 elements a row lies with 8 to 64 lanes
 // of a wave, whose sums need no barrier, beyond with a workgroup.  (16384 rows of
 // 4096, bf16, with the residual: forward 90 us for 537 MB, 6.0 TB/s; backward 116
 // us for 537 MB, 4.6 TB/s, and 5 us for the weights' sums; a large copy reaches
@@ -136,7 +136,9 @@ __global__ __launch_bounds__(threads_of<LPR>()) void layer_norm_bwd_kernel(const
         r.mean = r.on ? a.mean[row] : 0.f;
         r.rstd = r.on ? a.rstd[row] : 0.f;
     };
-    constexpr bool AHEAD = LPR <= 256;  // (1024 threads a row have no registers for it)
+    // (1024 threads a row have no registers for it: single elements in bf16 and fp32 and
+    // fp32 from whole dwords on keep one or two of 128 in memory as it is)
+    constexpr bool AHEAD = LPR <= 256;
     Row next;
     int64_t first = (int64_t)blockIdx.x * GRP;
     if (AHEAD && first + grp < rows) fetch(first + grp, next);

@@ -247,8 +247,9 @@ __global__ __launch_bounds__(256) void product_pack_kernel(const ProductArgs a) 
     *(i32x4*)(to + at * 16) = v;
 }
 
-// Tiles of BM x BN outputs over steps of 128 k, in two or three buffers of LDS: while
-// the matrix units work on one, the next one or two steps' rows are on their way.
+// Tiles of BM x BN outputs over steps of 128 k, in STAGES buffers of LDS (2 for tiles of
+// 256, 2 or 4 for 128, 5 for 64): while the matrix units work on one, the rows of the next
+// STAGES - 1 steps are on their way.
 // The 16-byte chunks of a row of 128 bytes stand in an order that depends on its
 // number, so that 16 lanes reading one chunk of 16 rows use all banks.  WM x WN
 // waves.  Bound, for tiles of 256, by the matrix units at the clock that is left: at
