@@ -131,9 +131,9 @@ fs_status fs_quantized_product(const fs_quantized_product_desc* desc, void* work
  * loss 0 and a gradient of zeros; lse of rows that are not active is 0 (of a row
  * of -inf alone: -inf).  Where d_loss is 0 the gradient is zeros.  A class of the
  * teacher's whose logit is -inf makes the loss infinite, not the gradient.  A NaN or
- * +inf among a row's logits makes its loss, lse and gradient NaN, one among its
- * teacher's logits (or one whose quotient by T is too large for fp32 beside a
- * teacher_lse) its loss and gradient. */
+ * +inf among a row's logits makes its lse NaN and, where the row has an entry, its
+ * loss and gradient; one among its teacher's logits (or, beside a teacher_lse, one
+ * whose quotient by T is too large for fp32) its loss and gradient. */
 typedef struct {
     int32_t dtype;            /* fs_dtype of the logits and their gradient */
     int32_t rows;             /* >= 0 */
